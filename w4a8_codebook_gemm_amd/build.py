@@ -1,7 +1,8 @@
-"""Compile the HIP sources under csrc/ for gfx950 into w4a8_codebook_gemm_amd/libw4a8.so.
+"""Compile the HIP sources for gfx950 into two shared libraries: csrc/ into libw4a8.so (the
+quantised layer, exporting the C ABI declared in include/w4a8.h) and csrc/attn/ into
+libw4a8_attn.so (the attention operators, include/w4a8_attn.h).
 
-Each source is compiled to an object in _build/ (in parallel), then linked into one shared
-library that exports only the C ABI declared in include/w4a8.h.
+Each source is compiled to an object in _build/ (in parallel), then linked.
 """
 from __future__ import annotations
 
@@ -16,6 +17,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build", "w4a8")
 LIB = os.path.join(PKG, "libw4a8.so")
+ATTN_CSRC = os.path.join(CSRC, "attn")
+ATTN_LIB = os.path.join(PKG, "libw4a8_attn.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -35,6 +38,10 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.hip")))
 
 
+def attn_sources():
+    return sorted(glob.glob(os.path.join(ATTN_CSRC, "*.hip")))
+
+
 def _compile(src: str, verbose: bool) -> str:
     obj = os.path.join(BUILD, os.path.basename(src) + ".o")
     cmd = [HIPCC, *FLAGS, "-c", src, "-o", obj]
@@ -48,16 +55,23 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
-def build(verbose: bool = False, jobs: int = 8) -> str:
-    os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
-        objs = list(ex.map(lambda s: _compile(s, verbose), sources()))
-    tmp = LIB + ".tmp%d" % os.getpid()
+def _link(objs, lib: str, verbose: bool) -> None:
+    tmp = lib + ".tmp%d" % os.getpid()
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
+    os.replace(tmp, lib)
+
+
+def build(verbose: bool = False, jobs: int = 8) -> str:
+    os.makedirs(BUILD, exist_ok=True)
+    parts = [(sources(), LIB), (attn_sources(), ATTN_LIB)]
+    with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        futs = [[ex.submit(_compile, s, verbose) for s in srcs] for srcs, _ in parts]
+        objs = [[f.result() for f in fs] for fs in futs]
+    for (_, lib), o in zip(parts, objs):
+        _link(o, lib, verbose)
     return LIB
 
 
