@@ -42,6 +42,7 @@ struct AttnArgs {
     void *o;
     void *ws;
 };
+constexpr int64_t kAttnCounterBytes = 8192;  // arrival counters at the workspace's start
 int64_t attn_workspace_bytes(int64_t M, int64_t B, int hq, int hkv, int head_dim, int num_cu);
 hipError_t launch_kv_attention(const AttnArgs &a, int bf16, int num_cu, hipStream_t stream);
 

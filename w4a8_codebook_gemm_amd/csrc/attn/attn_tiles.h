@@ -1,0 +1,69 @@
+// What the attention kernels share: operand fragments of v_mfma_f32_16x16x32_f16 made from
+// int8 codes, queries as fp16, and the running softmax in powers of two.
+#pragma once
+
+#include "attn_internal.h"
+
+namespace w4a8 {
+
+typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint32_t kSign4 = 0x80808080u;  // code ^ 0x80 = code + 128, four at a time
+
+// Eight consecutive codes (two dwords) as fp16, exact: the byte code + 128 under the exponent
+// byte 0x64 is the fp16 number 1024 + 128 + code.
+__device__ __forceinline__ half8_t codes_natural(uint32_t w0, uint32_t w1) {
+    const half2_t bias = {(_Float16)1152.0f, (_Float16)1152.0f};
+    uint32_t r[4];
+    const uint32_t w[2] = {w0 ^ kSign4, w1 ^ kSign4};
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        r[2 * i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(0x64646464u, w[i], 0x04010400u)) - bias);
+        r[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(0x64646464u, w[i], 0x04030402u)) - bias);
+    }
+    return __builtin_bit_cast(half8_t, make_uint4(r[0], r[1], r[2], r[3]));
+}
+
+// Byte J of two tokens' dwords (already ^ kSign4) as two fp16 numbers code * 2^-24, exact: the
+// byte code + 128 alone is the subnormal (code + 128) 2^-24.  Picking the bytes and turning
+// token rows into a fragment of consecutive tokens are the same permute.
+template <int J>
+__device__ __forceinline__ uint32_t codes_pair(uint32_t first, uint32_t second) {
+    const half2_t bias = __builtin_bit_cast(half2_t, 0x00800080u);  // 128 * 2^-24
+    const uint32_t u = __builtin_amdgcn_perm(second, first, 0x0C000C00u | (uint32_t)J | (uint32_t)(4 + J) << 16);
+    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, u) - bias);
+}
+constexpr int kCodeExp = 24;   // codes_pair's values are code * 2^-kCodeExp
+constexpr int kProbExp = 14;   // probabilities enter the second product as p * 2^kProbExp
+
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+    const half2_t h = {(_Float16)a, (_Float16)b};
+    return __builtin_bit_cast(uint32_t, h);
+}
+
+// Eight consecutive query values.
+template <bool BF16>
+__device__ __forceinline__ void load_q8(const void *q, int64_t off, float v[8]) {
+    if constexpr (BF16) {
+        const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(q) + off);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    } else {
+        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(q) + off);
+        const float4 a = p[0], b = p[1];
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+}
+
+// 2^x for a whole-numbered x <= 0 of any size (0 below fp32's range).
+__device__ __forceinline__ float pow2_down(float x) { return __builtin_amdgcn_exp2f(x); }
+
+}  // namespace w4a8

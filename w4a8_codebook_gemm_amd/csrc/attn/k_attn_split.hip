@@ -1,0 +1,589 @@
+// Attention over the int8 paged cache for few query rows a sequence (decode).
+//
+//   o = sum_t p_t v_t / sum_t p_t,  p_t = exp2(s_t - m),  s_t = scale log2(e) q . k_t
+//
+// HBM bound: each code is read once and used for the few query rows that share its head.
+// The rows of a unit are the (token, query head) pairs of one sequence and one cache head, in
+// blocks of 16 NB; they are the columns of v_mfma_f32_16x16x32_f16:
+//   S^T [32 positions x 16 rows] = K [positions x D] Q^T,   O^T [D x 16] += V^T P^T.
+// With S^T's rows taken as the positions 8 (m / 4) + 4 u + m % 4 of tile u, a lane's eight
+// scores are those of eight consecutive positions of its row, which is the fragment the
+// second product wants: probabilities never leave their lane.  Codes become fp16 in
+// registers: K rows by bytes in order, V by a permute that transposes 2 tokens x 1 value, one
+// permute and one packed addition for two codes.  No LDS until waves join.
+//
+// The running maximum m and the exponent E are whole numbers: with e the exponent of a page's
+// value scale sv < 2^e, a probability enters the second product as p sv 2^(14 - E), E the
+// largest (m_page - m) + e so far, so it is below 2^14 whatever the pages' scales, and every
+// rescaling is by a power of two, exact.  o = O 2^(24 - 14 + E) / sum p.
+//
+// Split: the 32-position tiles of all units form one line that is cut evenly over the
+// workgroups whatever the lengths are; a workgroup's waves take its tiles in turn and join in
+// LDS.  A unit that is cut leaves its pieces in the workspace, and the piece that arrives last
+// (an atomic count) joins them in order of position, so the result does not depend on who that is.
+#include "attn_tiles.h"
+
+namespace w4a8 {
+namespace {
+
+constexpr int kWaves = 8;
+constexpr int kThreads = 64 * kWaves;
+constexpr float kLow = -3.0e38f;  // "no score yet"
+
+template <int D>
+struct VLoad;
+template <> struct VLoad<256> { typedef uint4 type; };
+template <> struct VLoad<128> { typedef uint2 type; };
+template <> struct VLoad<64> { typedef uint32_t type; };
+
+// How a sequence contributes to the line of tiles.
+struct Work {
+    Seq q;
+    int lo, tiles;   // first tile, tiles of each unit
+    int64_t total;   // tiles of all its units
+};
+
+template <int RB>
+__device__ __forceinline__ Work seq_work(const AttnArgs &a, int64_t b) {
+    Work w;
+    w.q = load_seq(a.s, a.M, a.page_shift, b);
+    w.lo = w.tiles = 0;
+    w.total = 0;
+    if (w.q.n > 0) {
+        if (a.window && (int64_t)w.q.pos0 - a.window + 1 > 0) w.lo = (int)(w.q.pos0 - a.window + 1) >> 5;
+        w.tiles = ((w.q.len + 31) >> 5) - w.lo;
+        if (w.tiles < 1) w.tiles = 1;  // rows that see nothing are still written
+        const int64_t blocks = ((int64_t)w.q.n * a.group + RB - 1) / RB;
+        w.total = blocks * a.c.kv_heads * w.tiles;
+    }
+    return w;
+}
+
+__device__ __forceinline__ int64_t uniform64(int64_t x) {
+    return (int64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)x) | (int64_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32;
+}
+
+__device__ __forceinline__ int64_t scan64(int64_t x, int lane) {
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+        const int64_t o = __shfl_up((long long)x, s);
+        if (lane >= s) x += o;
+    }
+    return x;
+}
+
+// a / b for a >= 0, b > 0
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
+}
+
+// A value that other workgroups read or wrote: past the per-XCD caches.
+__device__ __forceinline__ void put_shared(float *p, float v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float get_shared(const float *p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+constexpr int kSumRows = 8;  // rows that join at a time
+
+template <int D, int NB>
+struct Layout {
+    static constexpr int RB = 16 * NB;
+    static constexpr int kRecord = RB * (D + 3);        // floats of a piece: O, then m, E, L
+    static constexpr int kRow = D + 4;                  // LDS row, padded
+    static constexpr int kLds = kWaves * kSumRows * kRow;  // floats
+};
+
+template <int D, int NB, bool BF16>
+__global__ __launch_bounds__(kThreads, D == 256 || NB == 2 ? 2 : 4) void k_attn_split(AttnArgs a, int wgs) {
+    using Lay = Layout<D, NB>;
+    using VT = typename VLoad<D>::type;
+    constexpr int RB = Lay::RB;
+    constexpr int kParts = BF16 ? 1 : 2;   // fp16 numbers that make a query value or a probability
+    constexpr int kC = D / 64;             // 16-byte chunks of a key row in a lane
+    constexpr int kVD = D / 64 > 0 ? D / 64 : 1;  // dwords of a value row in a lane
+    constexpr int kT = D / 16;             // tiles of O^T
+    __shared__ float s_o[Lay::kLds];
+    __shared__ float s_m[kWaves][RB], s_e[kWaves][RB], s_l[kWaves][RB];
+    __shared__ int s_last;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
+    uint32_t *counters = static_cast<uint32_t *>(a.ws);
+    float *pieces = reinterpret_cast<float *>(static_cast<char *>(a.ws) + kAttnCounterBytes);
+
+    // the line's length, and this workgroup's part of it
+    int64_t line = 0;
+    for (int64_t b0 = 0; b0 < a.s.B; b0 += 64)
+        line += __shfl((long long)scan64(b0 + lane < a.s.B ? seq_work<RB>(a, b0 + lane).total : 0, lane), 63);
+    line = uniform64(line);
+    if (line == 0) return;
+    int64_t used = (line + kWaves - 1) / kWaves;  // at least a tile for each wave
+    if (used > wgs) used = wgs;
+    const int64_t w = blockIdx.x;
+    if (w >= used) return;
+    const int64_t t0 = div64(w * line, used), t1 = div64((w + 1) * line, used);
+
+    for (int64_t at = t0; at < t1;) {
+        // the sequence and unit that tile `at` is in
+        int64_t base = 0, b = 0;
+        Work wk{};
+        for (int64_t b0 = 0; b0 < a.s.B; b0 += 64) {
+            Work x{};
+            if (b0 + lane < a.s.B) x = seq_work<RB>(a, b0 + lane);
+            const int64_t incl = scan64(x.total, lane);
+            const int64_t sum = uniform64(__shfl((long long)incl, 63));
+            if (at < base + sum) {
+                const uint64_t hit = __ballot(at - base < incl);
+                const int src = __ffsll((unsigned long long)hit) - 1;
+                b = b0 + src;
+                base += uniform64(__shfl((long long)(incl - x.total), src));
+                wk.q.first = uniform64(__shfl((long long)x.q.first, src));
+                wk.q.n = __builtin_amdgcn_readfirstlane(__shfl(x.q.n, src));
+                wk.q.len = __builtin_amdgcn_readfirstlane(__shfl(x.q.len, src));
+                wk.q.pos0 = wk.q.len - wk.q.n;
+                wk.lo = __builtin_amdgcn_readfirstlane(__shfl(x.lo, src));
+                wk.tiles = __builtin_amdgcn_readfirstlane(__shfl(x.tiles, src));
+                break;
+            }
+            base += sum;
+        }
+        const int64_t unit = div64(at - base, wk.tiles);
+        const int64_t unit0 = base + unit * wk.tiles;       // the unit's first tile on the line
+        const int tile0 = (int)(at - unit0);
+        const int take = (int)(wk.tiles - tile0 < t1 - at ? wk.tiles - tile0 : t1 - at);
+        const int64_t rblock = div64(unit, a.c.kv_heads);
+        const int h = (int)(unit - rblock * a.c.kv_heads);
+
+        // this lane's rows
+        const int64_t rows = (int64_t)wk.q.n * a.group;
+        const int64_t r0 = rblock * RB;
+        const int nrows = (int)(rows - r0 < RB ? rows - r0 : RB);
+        int lo[NB], hi[NB];
+        float fac[NB];
+        half8_t qf[NB][kParts][2 * kC];
+        auto row_at = [&](int r, int64_t &token, int &head) {  // row r < nrows of the block
+            const int64_t i = div64(r0 + r, a.group);
+            token = i;
+            head = h * a.group + (int)(r0 + r - i * a.group);
+        };
+        auto sees = [&](int64_t token, int &from, int &to) {
+            const int64_t pos = wk.q.pos0 + token;
+            const int64_t f = a.window ? pos - a.window + 1 : 0;
+            from = f > 0 ? (int)f : 0;
+            to = a.causal ? (pos + 1 > 0 ? (int)(pos + 1) : 0) : wk.q.len;
+        };
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++) {
+            const int r = 16 * nb + n;
+            float v[kC][2][8];
+            float top = 0.0f;
+            int64_t token = 0;
+            int head = 0;
+            lo[nb] = 0;
+            hi[nb] = 0;
+            if (r < nrows) {
+                row_at(r, token, head);
+                sees(token, lo[nb], hi[nb]);
+            }
+#pragma unroll
+            for (int c = 0; c < kC; c++)
+#pragma unroll
+                for (int u = 0; u < 2; u++) {
+                    if (r < nrows) {
+                        load_q8<BF16>(a.q, (wk.q.first + token) * a.q_stride + head * D + 64 * c + 16 * g + 8 * u, v[c][u]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; i++) v[c][u][i] = 0.0f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; i++) top = fmaxf(top, fabsf(v[c][u][i]));
+                }
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            // the row's largest value at 2^13 .. 2^14: bf16 values are then exact in fp16 down
+            // to 2^-28 of it (fp32 as two fp16 numbers to 2^-22 relative), below off by 2^-39
+            int ex = 0;
+            if (top > 0.0f) frexpf(top, &ex);
+            fac[nb] = ldexpf(fabsf(a.scale) * kLog2e, ex - 14);
+#pragma unroll
+            for (int c = 0; c < kC; c++)
+#pragma unroll
+                for (int u = 0; u < 2; u++)
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        const float x = ldexpf(a.scale < 0.0f ? -v[c][u][i] : v[c][u][i], 14 - ex);
+                        const _Float16 x0 = (_Float16)x;
+                        qf[nb][0][2 * c + u][i] = x0;
+                        if constexpr (kParts == 2) qf[nb][1][2 * c + u][i] = (_Float16)(x - (float)x0);
+                    }
+        }
+        // positions that all rows of the block see, and that any does
+        int all_lo, all_hi, any_lo, any_hi;
+        {
+            int64_t t_first, t_last;
+            int hd;
+            row_at(0, t_first, hd);
+            row_at(nrows - 1, t_last, hd);
+            sees(t_first, any_lo, all_hi);
+            sees(t_last, all_lo, any_hi);
+        }
+
+        floatx4 o[NB][kT];
+        float m[NB], E[NB], L[NB];
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++) {
+            m[nb] = kLow;
+            E[nb] = 0.0f;
+            L[nb] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kT; i++) o[nb][i] = floatx4{0, 0, 0, 0};
+        }
+
+        const int end = wk.lo + tile0 + take;
+        int first = wk.lo + tile0 + wave;
+        if (first < any_lo >> 5) first += ((any_lo >> 5) - first + kWaves - 1) / kWaves * kWaves;
+        const int stop = end < (any_hi + 31) >> 5 ? end : (any_hi + 31) >> 5;
+        const int P = a.c.page_size, pm = P - 1;
+        const bool small = a.page_shift == 4;  // two pages in a tile
+        const int32_t *table = a.s.page_table + b * a.s.table_width;
+        const int tokk = small ? 16 * (n >> 3) : 0, toks = small ? 16 * (g >> 1) : 0;
+
+        auto page_of = [&](int t) {  // page of position t, -1 past the end
+            return t < wk.q.len ? table[t >> a.page_shift] : -1;
+        };
+        auto block_of = [&](int page) {  // its block of this head; a page that is not there reads page 0, masked
+            return (int64_t)((uint32_t)page < (uint32_t)a.c.num_pages ? page : 0) * a.c.kv_heads + h;
+        };
+        uint4 kr[2][kC];
+        VT vr[8];
+        float ks = 0.0f, vs = 0.0f;
+        int pk = -1, ps = -1;       // pages of the tile to load next
+        auto load_k = [&](int tile) {
+            const int8_t *p = a.c.k + (block_of(pk) * P + ((32 * tile + 8 * (n >> 2) + (n & 3)) & pm)) * D + 16 * g;
+#pragma unroll
+            for (int u = 0; u < 2; u++)
+#pragma unroll
+                for (int c = 0; c < kC; c++) kr[u][c] = *reinterpret_cast<const uint4 *>(p + 4 * u * D + 64 * c);
+        };
+        auto load_v = [&](int tile) {
+            const int8_t *p = a.c.v + (block_of(ps) * P + ((32 * tile + 8 * g) & pm)) * D + n * (D / 16);
+#pragma unroll
+            for (int j = 0; j < 8; j++) vr[j] = *reinterpret_cast<const VT *>(p + j * D);
+        };
+        auto load_scales = [&]() {
+            const int64_t blk = block_of(ps);
+            ks = a.c.k_scale[blk];
+            vs = a.c.v_scale[blk];
+        };
+        int page_s = -1;            // page of this lane's positions in the current tile
+        if (first < stop) {
+            pk = page_of(32 * first + tokk);
+            ps = page_of(32 * first + toks);
+            load_scales();
+            load_k(first);
+            load_v(first);
+            page_s = ps;
+            if (first + kWaves < stop) {
+                pk = page_of(32 * (first + kWaves) + tokk);
+                ps = page_of(32 * (first + kWaves) + toks);
+            }
+        }
+        for (int tile = first; tile < stop; tile += kWaves) {
+            const bool more = tile + kWaves < stop;
+            floatx4 s[NB][2];
+#pragma unroll
+            for (int nb = 0; nb < NB; nb++) s[nb][0] = s[nb][1] = floatx4{0, 0, 0, 0};
+#pragma unroll
+            for (int u = 0; u < 2; u++)
+#pragma unroll
+                for (int c = 0; c < kC; c++) {
+                    const half8_t k0 = codes_natural(kr[u][c].x, kr[u][c].y), k1 = codes_natural(kr[u][c].z, kr[u][c].w);
+#pragma unroll
+                    for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                        for (int pt = 0; pt < kParts; pt++) {
+                            s[nb][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qf[nb][pt][2 * c], s[nb][u], 0, 0, 0);
+                            s[nb][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qf[nb][pt][2 * c + 1], s[nb][u], 0, 0, 0);
+                        }
+                }
+            const float tks = ks, tvs = vs;
+            const int tpage = page_s;
+            int npk = -1, nps = -1;
+            if (more) {
+                if (tile + 2 * kWaves < stop) {
+                    npk = page_of(32 * (tile + 2 * kWaves) + tokk);
+                    nps = page_of(32 * (tile + 2 * kWaves) + toks);
+                }
+                load_scales();
+                load_k(tile + kWaves);
+            }
+            const bool there = (uint32_t)tpage < (uint32_t)a.c.num_pages;
+            const bool whole = 32 * tile >= all_lo && 32 * tile + 32 <= all_hi && __all(there);
+            half8_t pf[NB][kParts];
+#pragma unroll
+            for (int nb = 0; nb < NB; nb++) {
+                const float f = fac[nb] * tks;
+                float x[8], mx = -INFINITY;
+                float sv = tvs;
+                if (whole) {
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        x[j] = s[nb][j >> 2][j & 3] * f;
+                        mx = fmaxf(mx, x[j]);
+                    }
+                } else {
+                    const int t = 32 * tile + 8 * g;
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        const bool see = there && t + j >= lo[nb] && t + j < hi[nb];
+                        x[j] = see ? s[nb][j >> 2][j & 3] * f : -INFINITY;
+                        mx = fmaxf(mx, x[j]);
+                    }
+                }
+                float all = fmaxf(mx, __shfl_xor(mx, 16));
+                all = fmaxf(all, __shfl_xor(all, 32));
+                // nothing seen of this page: its scale, whatever it holds, stays out
+                if ((small ? mx : all) == -INFINITY) sv = 0.0f;
+                const float mn = fmaxf(m[nb], ceilf(all));
+                const float down = m[nb] - mn;             // <= 0
+                int e = -300;
+                if (sv > 0.0f) frexpf(sv, &e);
+                float top = (small ? ceilf(mx) : ceilf(all)) - mn + (float)e;
+                if (small) {
+                    top = fmaxf(top, __shfl_xor(top, 16));
+                    top = fmaxf(top, __shfl_xor(top, 32));
+                }
+                const float En = fmaxf(E[nb] + down, top);
+                const float turn = down + (E[nb] - En);    // exponent of the rescaling of o, <= 0
+                float sum = 0.0f;
+                const float scale = sv > 0.0f ? fminf(ldexpf(sv, (int)((float)kProbExp - En)), 1e38f) : 0.0f;
+                float pv[8];
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const float p = __builtin_amdgcn_exp2f(x[j] - mn);
+                    sum += p;
+                    pv[j] = fminf(p * scale, 32768.0f);
+                }
+                L[nb] = L[nb] * pow2_down(down) + sum;
+                if (__any(turn < 0.0f)) {
+                    const float q = pow2_down(turn);
+#pragma unroll
+                    for (int i = 0; i < kT; i++) o[nb][i] *= q;
+                }
+                m[nb] = mn;
+                E[nb] = En;
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const _Float16 p0 = (_Float16)pv[j];
+                    pf[nb][0][j] = p0;
+                    if constexpr (kParts == 2) pf[nb][1][j] = (_Float16)(pv[j] - (float)p0);
+                }
+            }
+            auto dword = [&](int j, int i) -> uint32_t {
+                if constexpr (D == 256) return (i == 0 ? vr[j].x : i == 1 ? vr[j].y : i == 2 ? vr[j].z : vr[j].w) ^ kSign4;
+                else if constexpr (D == 128) return (i == 0 ? vr[j].x : vr[j].y) ^ kSign4;
+                else return vr[j] ^ kSign4;
+            };
+#pragma unroll
+            for (int i = 0; i < kVD; i++) {
+                uint32_t d[8];
+#pragma unroll
+                for (int j = 0; j < 8; j++) d[j] = dword(j, i);
+                half8_t f[4];
+                f[0] = __builtin_bit_cast(half8_t, make_uint4(codes_pair<0>(d[0], d[1]), codes_pair<0>(d[2], d[3]), codes_pair<0>(d[4], d[5]), codes_pair<0>(d[6], d[7])));
+                f[1] = __builtin_bit_cast(half8_t, make_uint4(codes_pair<1>(d[0], d[1]), codes_pair<1>(d[2], d[3]), codes_pair<1>(d[4], d[5]), codes_pair<1>(d[6], d[7])));
+                f[2] = __builtin_bit_cast(half8_t, make_uint4(codes_pair<2>(d[0], d[1]), codes_pair<2>(d[2], d[3]), codes_pair<2>(d[4], d[5]), codes_pair<2>(d[6], d[7])));
+                f[3] = __builtin_bit_cast(half8_t, make_uint4(codes_pair<3>(d[0], d[1]), codes_pair<3>(d[2], d[3]), codes_pair<3>(d[4], d[5]), codes_pair<3>(d[6], d[7])));
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+#pragma unroll
+                    for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                        for (int pt = 0; pt < kParts; pt++)
+                            o[nb][4 * i + k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[k], pf[nb][pt], o[nb][4 * i + k], 0, 0, 0);
+            }
+            if (more) {
+                load_v(tile + kWaves);
+                page_s = ps;
+                pk = npk;
+                ps = nps;
+            }
+        }
+
+        // join the waves: the column's sum first (a lane has summed its own positions)
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++) {
+            L[nb] += __shfl_xor(L[nb], 16);
+            L[nb] += __shfl_xor(L[nb], 32);
+            if (g == 0) {
+                s_m[wave][16 * nb + n] = m[nb];
+                s_e[wave][16 * nb + n] = E[nb];
+                s_l[wave][16 * nb + n] = L[nb];
+            }
+        }
+        __syncthreads();
+        float mj[NB], ej[NB];
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++) {
+            const int r = 16 * nb + n;
+            float mm = s_m[0][r], ee = kLow;
+            for (int x = 1; x < kWaves; x++) mm = fmaxf(mm, s_m[x][r]);
+            for (int x = 0; x < kWaves; x++) ee = fmaxf(ee, s_e[x][r] + (s_m[x][r] - mm));
+            mj[nb] = mm;
+            ej[nb] = ee;
+            const float q = pow2_down((m[nb] - mm) + (E[nb] - ee));
+#pragma unroll
+            for (int i = 0; i < kT; i++) o[nb][i] *= q;
+        }
+        // what becomes of row r, value d
+        const bool cut = take < wk.tiles;
+        const int64_t w_first = div64((unit0 + 1) * used - 1, line), w_end = div64((unit0 + wk.tiles) * used - 1, line);
+        float *piece = pieces + (2 * w + (w == w_first ? 1 : 0)) * Lay::kRecord;
+        auto write_row = [&](int r, int d, const float v[4]) {  // four final values
+            int64_t token;
+            int head;
+            row_at(r, token, head);
+            const int64_t off = ((wk.q.first + token) * a.hq + head) * D + d;
+            if constexpr (BF16) {
+                uint2 u;
+                u.x = (uint32_t)f32_to_bf16_rne(v[0]) | (uint32_t)f32_to_bf16_rne(v[1]) << 16;
+                u.y = (uint32_t)f32_to_bf16_rne(v[2]) | (uint32_t)f32_to_bf16_rne(v[3]) << 16;
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.o) + off) = u;
+            } else {
+                *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + off) = make_float4(v[0], v[1], v[2], v[3]);
+            }
+        };
+        if (cut && wave == 0 && g == 0) {
+#pragma unroll
+            for (int nb = 0; nb < NB; nb++) {
+                const int r = 16 * nb + n;
+                float l = 0.0f;
+                for (int x = 0; x < kWaves; x++) l += s_l[x][r] * pow2_down(s_m[x][r] - mj[nb]);
+                put_shared(piece + RB * D + r, mj[nb]);
+                put_shared(piece + RB * D + RB + r, ej[nb]);
+                put_shared(piece + RB * D + 2 * RB + r, l);
+            }
+        }
+        for (int q0 = 0; q0 < nrows; q0 += kSumRows) {
+#pragma unroll
+            for (int nb = 0; nb < NB; nb++) {
+                const int r = 16 * nb + n - q0;
+                if (r >= 0 && r < kSumRows) {
+                    float *p = s_o + (wave * kSumRows + r) * Lay::kRow;
+#pragma unroll
+                    for (int ii = 0; ii < 4; ii++)
+#pragma unroll
+                        for (int i = 0; i < kT; i += 4)
+                            *reinterpret_cast<float4 *>(p + (4 * g + ii) * kT + i) =
+                                make_float4(o[nb][i][ii], o[nb][i + 1][ii], o[nb][i + 2][ii], o[nb][i + 3][ii]);
+                }
+            }
+            __syncthreads();
+            for (int x = tid; x < kSumRows * (D / 4); x += kThreads) {
+                const int r = x / (D / 4), d = 4 * (x % (D / 4));
+                if (q0 + r < nrows) {
+                    float v[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int y = 0; y < kWaves; y++) {
+                        const float4 f = *reinterpret_cast<const float4 *>(s_o + (y * kSumRows + r) * Lay::kRow + d);
+                        v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+                    }
+                    if (cut) {
+#pragma unroll
+                        for (int i = 0; i < 4; i++) put_shared(piece + (q0 + r) * D + d + i, v[i]);
+                    } else {
+                        float mm = s_m[0][q0 + r], ee = kLow, l = 0.0f;
+                        for (int y = 1; y < kWaves; y++) mm = fmaxf(mm, s_m[y][q0 + r]);
+                        for (int y = 0; y < kWaves; y++) {
+                            ee = fmaxf(ee, s_e[y][q0 + r] + (s_m[y][q0 + r] - mm));
+                            l += s_l[y][q0 + r] * pow2_down(s_m[y][q0 + r] - mm);
+                        }
+                        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 4; i++) v[i] = ldexpf(v[i] * inv, (int)ee + kCodeExp - kProbExp);
+                        write_row(q0 + r, d, v);
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        if (cut) {
+            // every store of the piece has left before its arrival is counted
+            __builtin_amdgcn_s_waitcnt(0);
+            __syncthreads();
+            const unsigned parts = (unsigned)(w_end - w_first + 1);
+            if (tid == 0) s_last = atomicInc(counters + w_first, parts - 1) == parts - 1;
+            __syncthreads();
+            if (s_last) {
+                // piece x of the unit: the first one's starts in its workgroup's part, the others lead theirs
+                auto piece_at = [&](unsigned x) { return pieces + (2 * (w_first + x) + (x == 0 ? 1 : 0)) * Lay::kRecord; };
+                for (int x = tid; x < nrows * (D / 4); x += kThreads) {
+                    const int r = x / (D / 4), d = 4 * (x % (D / 4));
+                    float mm = kLow, ee = 0.0f, l = 0.0f, v[4] = {0, 0, 0, 0};
+                    for (unsigned y = 0; y < parts; y++) {
+                        const float *p = piece_at(y);
+                        const float pm2 = get_shared(p + RB * D + r), pe = get_shared(p + RB * D + RB + r), pl = get_shared(p + RB * D + 2 * RB + r);
+                        float pv[4];
+#pragma unroll
+                        for (int i = 0; i < 4; i++) pv[i] = get_shared(p + r * D + d + i);
+                        const float mn = fmaxf(mm, pm2), da = mm - mn, db = pm2 - mn;
+                        const float en = fmaxf(ee + da, pe + db);
+                        l = l * pow2_down(da) + pl * pow2_down(db);
+                        const float qa = pow2_down(da + (ee - en)), qb = pow2_down(db + (pe - en));
+#pragma unroll
+                        for (int i = 0; i < 4; i++) v[i] = v[i] * qa + pv[i] * qb;
+                        mm = mn;
+                        ee = en;
+                    }
+                    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 4; i++) v[i] = ldexpf(v[i] * inv, (int)ee + kCodeExp - kProbExp);
+                    write_row(r, d, v);
+                }
+            }
+            __syncthreads();
+        }
+        at += take;
+    }
+}
+
+template <int D, int NB>
+int wgs_of(int num_cu) { return num_cu * (D == 256 || NB == 2 ? 1 : 2); }
+
+template <int D, int NB>
+hipError_t launch_nb(const AttnArgs &a, int bf16, int num_cu, hipStream_t stream) {
+    const int wgs = wgs_of<D, NB>(num_cu);
+    if (bf16) k_attn_split<D, NB, true><<<wgs, kThreads, 0, stream>>>(a, wgs);
+    else k_attn_split<D, NB, false><<<wgs, kThreads, 0, stream>>>(a, wgs);
+    return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_d(const AttnArgs &a, int bf16, int num_cu, hipStream_t stream) {
+    return a.M * a.group <= 16 * a.s.B ? launch_nb<D, 1>(a, bf16, num_cu, stream) : launch_nb<D, 2>(a, bf16, num_cu, stream);
+}
+
+template <int D>
+int64_t bytes_d(int num_cu) {
+    const int64_t one = 2 * (int64_t)wgs_of<D, 1>(num_cu) * Layout<D, 1>::kRecord;
+    const int64_t two = 2 * (int64_t)wgs_of<D, 2>(num_cu) * Layout<D, 2>::kRecord;
+    return kAttnCounterBytes + 4 * (one > two ? one : two);
+}
+
+}  // namespace
+
+int64_t attn_workspace_bytes(int64_t, int64_t, int, int, int head_dim, int num_cu) {
+    return head_dim == 64 ? bytes_d<64>(num_cu) : head_dim == 128 ? bytes_d<128>(num_cu) : bytes_d<256>(num_cu);
+}
+
+hipError_t launch_kv_attention(const AttnArgs &a, int bf16, int num_cu, hipStream_t stream) {
+    if (2 * num_cu > kAttnCounterBytes / 4) return hipErrorInvalidConfiguration;
+    switch (a.c.head_dim) {
+        case 64: return launch_d<64>(a, bf16, num_cu, stream);
+        case 128: return launch_d<128>(a, bf16, num_cu, stream);
+        default: return launch_d<256>(a, bf16, num_cu, stream);
+    }
+}
+
+}  // namespace w4a8
