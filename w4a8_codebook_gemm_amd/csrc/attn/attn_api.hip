@@ -168,6 +168,16 @@ int w4a8_kv_append(const void *k, int64_t k_stride, const void *v, int64_t v_str
     return status_of(w4a8::launch_kv_append(a, dtype == W4A8_BF16, static_cast<hipStream_t>(stream)));
 }
 
+// Rows (new tokens x query heads of a cache head) a sequence has on average decide the kernel:
+// to 16 they are the split kernel's block of 16, to 32 its block of 32, above that the prompt kernel.
+static int64_t rows_per_sequence(int64_t M, int64_t B, int group) { return (M * group + B - 1) / B; }
+
+// The pieces of cut units that the kernel for this shape leaves behind the counters.
+static int64_t attn_bytes(int64_t M, int64_t B, int group, int head_dim, int num_cu) {
+    return w4a8::kAttnCounterBytes + (rows_per_sequence(M, B, group) <= 32 ? w4a8::attn_split_bytes(head_dim, num_cu)
+                                                                           : w4a8::attn_prompt_bytes(head_dim, num_cu));
+}
+
 static int check_attn_shape(int64_t M, int64_t B, int q_heads, int kv_heads, int head_dim) {
     if (B < 1 || B > 65536 || kv_heads < 1 || kv_heads > 1024 || !valid_dim(head_dim)) return W4A8_ERR_SHAPE;
     if (q_heads < 1 || q_heads > 8192 || q_heads % kv_heads != 0 || M < 1 || M > kMaxTokens ||
@@ -182,7 +192,9 @@ int64_t w4a8_kv_attention_workspace_bytes(int64_t M, int64_t B, int q_heads, int
     int num_cu = 0;
     st = current_device(&num_cu);
     if (st != W4A8_OK) return -st;
-    return w4a8::attn_workspace_bytes(M, B, q_heads, kv_heads, head_dim, num_cu);
+    // a call of fewer tokens or sequences may take either kernel
+    const int64_t split = w4a8::attn_split_bytes(head_dim, num_cu), prompt = w4a8::attn_prompt_bytes(head_dim, num_cu);
+    return w4a8::kAttnCounterBytes + (M * (q_heads / kv_heads) <= 32 || split > prompt ? split : prompt);
 }
 
 int w4a8_kv_attention(const void *q, int64_t q_stride, int dtype, int64_t M, int q_heads, const w4a8_kv_cache *cache,
@@ -201,13 +213,18 @@ int w4a8_kv_attention(const void *q, int64_t q_stride, int dtype, int64_t M, int
     int num_cu = 0;
     st = current_device(&num_cu);
     if (st != W4A8_OK) return st;
-    const int64_t need = w4a8::attn_workspace_bytes(M, seqs->B, q_heads, cache->kv_heads, cache->head_dim, num_cu);
-    if (need > 0 && (!workspace || workspace_bytes < need)) return W4A8_ERR_WORKSPACE;
+    const int group = q_heads / cache->kv_heads;
+    if (!workspace || workspace_bytes < attn_bytes(M, seqs->B, group, cache->head_dim, num_cu)) return W4A8_ERR_WORKSPACE;
+    // a counter for each workgroup of the widest launch
+    if (2 * num_cu > w4a8::kAttnCounterBytes / 4) return W4A8_ERR_DEVICE;
     // a window that no length reaches is none
     if (window > kInt31) window = 0;
-    w4a8::AttnArgs a{q, q_stride, M, q_heads, q_heads / cache->kv_heads, *cache, *seqs, page_shift(cache->page_size),
-                     sm_scale, causal, window, o, workspace};
-    return status_of(w4a8::launch_kv_attention(a, dtype == W4A8_BF16, num_cu, static_cast<hipStream_t>(stream)));
+    w4a8::AttnArgs a{q, q_stride, M, q_heads, group, *cache, *seqs, page_shift(cache->page_size), sm_scale, causal, window, o,
+                     workspace};
+    hipStream_t st2 = static_cast<hipStream_t>(stream);
+    const int64_t rows = rows_per_sequence(M, seqs->B, group);
+    return status_of(rows <= 32 ? w4a8::launch_attn_split(a, dtype == W4A8_BF16, rows <= 16 ? 1 : 2, num_cu, st2)
+                                : w4a8::launch_attn_prompt(a, dtype == W4A8_BF16, num_cu, st2));
 }
 
 }  // extern "C"

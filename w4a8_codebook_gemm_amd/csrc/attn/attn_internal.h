@@ -43,8 +43,12 @@ struct AttnArgs {
     void *ws;
 };
 constexpr int64_t kAttnCounterBytes = 8192;  // arrival counters at the workspace's start
-int64_t attn_workspace_bytes(int64_t M, int64_t B, int hq, int hkv, int head_dim, int num_cu);
-hipError_t launch_kv_attention(const AttnArgs &a, int bf16, int num_cu, hipStream_t stream);
+// Few rows a sequence: blocks of 16 (blocks 1) or 32 (2) rows.
+int64_t attn_split_bytes(int head_dim, int num_cu);
+hipError_t launch_attn_split(const AttnArgs &a, int bf16, int blocks, int num_cu, hipStream_t stream);
+// Many rows a sequence.
+int64_t attn_prompt_bytes(int head_dim, int num_cu);
+hipError_t launch_attn_prompt(const AttnArgs &a, int bf16, int num_cu, hipStream_t stream);
 
 // One sequence as the kernels see it, every number held to its range: rows first .. first + n - 1,
 // length, and the position of the first row (negative where the length is shorter than n).

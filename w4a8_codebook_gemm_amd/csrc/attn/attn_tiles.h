@@ -66,4 +66,41 @@ __device__ __forceinline__ void load_q8(const void *q, int64_t off, float v[8]) 
 // 2^x for a whole-numbered x <= 0 of any size (0 below fp32's range).
 __device__ __forceinline__ float pow2_down(float x) { return __builtin_amdgcn_exp2f(x); }
 
+constexpr float kLow = -3.0e38f;  // "no score yet"
+
+__device__ __forceinline__ int64_t uniform64(int64_t x) {
+    return (int64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)x) | (int64_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32;
+}
+
+__device__ __forceinline__ int64_t scan64(int64_t x, int lane) {
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+        const int64_t o = __shfl_up((long long)x, s);
+        if (lane >= s) x += o;
+    }
+    return x;
+}
+
+// a / b for a >= 0, b > 0
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
+}
+
+// A value that other workgroups read or wrote: past the per-XCD caches.
+__device__ __forceinline__ void put_shared(float *p, float v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float get_shared(const float *p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The positions [from, to) that new token i of a sequence sees.
+__device__ __forceinline__ void sees(const AttnArgs &a, const Seq &q, int64_t i, int &from, int &to) {
+    const int64_t pos = q.pos0 + i;
+    const int64_t f = a.window ? pos - a.window + 1 : 0;
+    from = f > 0 ? (int)f : 0;
+    to = a.causal ? (pos + 1 > 0 ? (int)(pos + 1) : 0) : q.len;
+}
+
 }  // namespace w4a8

@@ -1,0 +1,494 @@
+// Attention over the int8 paged cache for many query rows a sequence (prompts, their chunks).
+//
+//   o = sum_t p_t v_t / sum_t p_t,  p_t = exp2(s_t - m),  s_t = scale log2(e) q . k_t
+//
+// Matrix-core bound: 4 D flops for each row and position.  A unit is a block of 32 kWaves rows (the
+// (token, query head) pairs of one sequence and cache head); each wave has 32 of them as the
+// columns of v_mfma_f32_32x32x16_f16, queries and O^T in registers:
+//   S^T [32 positions x 32 rows] = K Q^T,   O^T [D x 32] += V^T P^T.
+// The codes of a tile of 8192 / D positions become fp16 once for all waves, in LDS, two tiles
+// deep: loads of the next tile are in flight while this one is used.  K lies as rows of
+// positions, V transposed as rows of values (a permute picks one value of two positions), both in
+// 16-byte slots placed so that eight neighbouring lanes touch all banks in reading and in writing.
+// V's positions are kept in the order in which a lane of S^T holds them, 4 (lane / 32) + 8 b + c,
+// so probabilities never leave their lane.
+//
+// Pages hold at least 16 positions, so the scales are the same for the 16 positions of a group.
+// The running maximum m and the exponent E are whole numbers as in the split kernel:
+// a probability enters the second product as p w, w = sv 2^(14 - E), at most 2^14.  With bf16
+// outputs the factor goes into the exponent, p w = exp2(s - m + log2 w), which is good to
+// 2^-18 for |log2 w| <= 60; w is held at 2^-60 or more, where the products are below fp16's
+// range and only the sum of p counts them.
+//
+// Split: as in the split kernel, the tiles of all units form one line that is cut evenly over the
+// workgroups; a cut unit's pieces are joined by the last workgroup to arrive, in order.
+#include "attn_tiles.h"
+
+namespace w4a8 {
+namespace {
+
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+
+constexpr int kMinTiles = 4;  // tiles a workgroup is worth cutting for
+
+template <int D, bool BF16>
+struct Shape {
+    // fp32 rows need twice the registers for their queries: half the waves share a CU
+    static constexpr int kWaves = BF16 ? 8 : 4;
+    static constexpr int kThreads = 64 * kWaves;
+    static constexpr int RB = 32 * kWaves;
+    static constexpr int T = 8192 / D;       // positions of a tile
+    static constexpr int kGroups = T / 16;
+    static constexpr int kRegs = D / 2;      // floats of O^T in a lane
+    static constexpr int kRecord = kWaves * 64 * (kRegs + 3);
+};
+
+// First tile and tiles of row block rb of a sequence.
+template <int D, bool BF16>
+__device__ __forceinline__ int block_tiles(const AttnArgs &a, const Seq &q, int64_t rb, int &first) {
+    using S = Shape<D, BF16>;
+    const int64_t rows = (int64_t)q.n * a.group, r0 = rb * S::RB;
+    const int64_t last = (r0 + S::RB < rows ? r0 + S::RB : rows) - 1;
+    int lo, hi, x;
+    sees(a, q, div64(r0, a.group), lo, x);
+    sees(a, q, div64(last, a.group), x, hi);
+    first = lo / S::T;
+    const int n = (hi + S::T - 1) / S::T - first;
+    return n < 1 ? 1 : n;  // rows that see nothing are still written
+}
+
+struct Blocks {
+    Seq q;
+    int64_t blocks, tiles;  // of one cache head
+};
+
+template <int D, bool BF16>
+__device__ __forceinline__ Blocks seq_blocks(const AttnArgs &a, int64_t b) {
+    Blocks w;
+    w.q = load_seq(a.s, a.M, a.page_shift, b);
+    w.blocks = ((int64_t)w.q.n * a.group + Shape<D, BF16>::RB - 1) / Shape<D, BF16>::RB;
+    w.tiles = 0;
+    int x;
+    for (int64_t i = 0; i < w.blocks; i++) w.tiles += block_tiles<D, BF16>(a, w.q, i, x);
+    return w;
+}
+
+// Byte offset of 16-byte slot `slot` (8 values) of position t in a K tile: even slots first, then
+// odd ones, mixed by the position's low bits.
+template <int D>
+__device__ __forceinline__ int k_at(int t, int slot) {
+    const int key = (t & 1) << 2 | (t & 2) | (t >> 2 & 1);
+    return t * 2 * D + (((slot >> 1) + (slot & 1) * (D / 16)) ^ key) * 16;
+}
+// Byte offset of slot `slot` (8 positions) of value d in a V tile.
+template <int D>
+__device__ __forceinline__ int v_at(int d, int slot) {
+    if constexpr (D == 256) {  // rows of 64 bytes, two to the banks' 128
+        const int x = (d >> 2 & 1) | ((d >> 1 ^ d >> 3) & 1) << 1;
+        return (d >> 1) * 128 + ((d ^ d >> 4) & 1) * 64 + (slot ^ x) * 16;
+    } else {
+        const int x = (d >> 2 & 1) | ((d ^ d >> 3) & 1) << 1 | ((d >> 1 ^ d >> 4) & 1) << 2;
+        return d * (16384 / D) + (slot ^ x) * 16;
+    }
+}
+
+template <int D, bool BF16>
+__global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_attn_prompt(AttnArgs a, int wgs) {
+    using S = Shape<D, BF16>;
+    constexpr int T = S::T, kParts = BF16 ? 1 : 2, kSteps = D / 16, kTiles = D / 32;
+    constexpr int kItems = 512 / S::kThreads;  // staging items of a thread: 256 of keys, 256 of values
+    __shared__ __attribute__((aligned(16))) char s_k[2][16384], s_v[2][16384];
+    __shared__ float s_ks[2][S::kGroups], s_vs[2][S::kGroups];
+    __shared__ int s_ok[2][S::kGroups];
+    __shared__ int s_last;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 31, hh = lane >> 5;
+    uint32_t *counters = static_cast<uint32_t *>(a.ws);
+    float *pieces = reinterpret_cast<float *>(static_cast<char *>(a.ws) + kAttnCounterBytes);
+
+    int64_t line = 0;
+    for (int64_t b0 = 0; b0 < a.s.B; b0 += 64)
+        line += __shfl((long long)scan64(b0 + lane < a.s.B ? seq_blocks<D, BF16>(a, b0 + lane).tiles * a.c.kv_heads : 0, lane), 63);
+    line = uniform64(line);
+    if (line == 0) return;
+    int64_t used = (line + kMinTiles - 1) / kMinTiles;
+    if (used > wgs) used = wgs;
+    // workgroups go to the XCDs in turn: neighbours on the line, which read the same pages, share one's L2
+    int64_t w = blockIdx.x;
+    if (used == wgs && wgs % 8 == 0) w = w % 8 * (wgs / 8) + w / 8;
+    if (w >= used) return;
+    const int64_t t0 = div64(w * line, used), t1 = div64((w + 1) * line, used);
+
+    for (int64_t at = t0; at < t1;) {
+        // the sequence, cache head and row block that tile `at` is in
+        int64_t base = 0, b = 0, blocks = 0, per_head = 0;
+        Seq q{};
+        for (int64_t b0 = 0; b0 < a.s.B; b0 += 64) {
+            Blocks x{};
+            if (b0 + lane < a.s.B) x = seq_blocks<D, BF16>(a, b0 + lane);
+            const int64_t mine = x.tiles * a.c.kv_heads;
+            const int64_t incl = scan64(mine, lane);
+            const int64_t sum = uniform64(__shfl((long long)incl, 63));
+            if (at < base + sum) {
+                const int src = __ffsll((unsigned long long)__ballot(at - base < incl)) - 1;
+                b = b0 + src;
+                base += uniform64(__shfl((long long)(incl - mine), src));
+                q.first = uniform64(__shfl((long long)x.q.first, src));
+                q.n = __builtin_amdgcn_readfirstlane(__shfl(x.q.n, src));
+                q.len = __builtin_amdgcn_readfirstlane(__shfl(x.q.len, src));
+                q.pos0 = q.len - q.n;
+                blocks = uniform64(__shfl((long long)x.blocks, src));
+                per_head = uniform64(__shfl((long long)x.tiles, src));
+                break;
+            }
+            base += sum;
+        }
+        const int h = (int)div64(at - base, per_head);
+        int64_t unit0 = base + h * per_head, rb = 0;  // the unit's first tile on the line
+        int first_tile = 0, tiles = 1;
+        for (int64_t r = 0; r < blocks; r += 64) {
+            int f = 0, c = 0;
+            if (r + lane < blocks) c = block_tiles<D, BF16>(a, q, r + lane, f);
+            const int64_t incl = scan64(c, lane), sum = uniform64(__shfl((long long)incl, 63));
+            if (at < unit0 + sum) {
+                const int src = __ffsll((unsigned long long)__ballot(at - unit0 < incl)) - 1;
+                unit0 += uniform64(__shfl((long long)(incl - c), src));
+                rb = r + src;
+                first_tile = __builtin_amdgcn_readfirstlane(__shfl(f, src));
+                tiles = __builtin_amdgcn_readfirstlane(__shfl(c, src));
+                break;
+            }
+            unit0 += sum;
+        }
+        const int tile0 = (int)(at - unit0);
+        const int take = (int)(tiles - tile0 < t1 - at ? tiles - tile0 : t1 - at);
+
+        // this wave's rows
+        const int64_t rows = (int64_t)q.n * a.group, r0 = rb * S::RB + 32 * wave;
+        const int nrows = rows - r0 < 0 ? 0 : rows - r0 < 32 ? (int)(rows - r0) : 32;
+        const int64_t my = r0 + (n < nrows ? n : 0);
+        const int64_t token = nrows ? div64(my, a.group) : 0;
+        const int head = h * a.group + (int)(my - token * a.group);
+        int lo = 0, hi = 0, all_lo = 0, all_hi = 0, any_lo = 0, any_hi = 0;
+        if (nrows) {
+            if (n < nrows) sees(a, q, token, lo, hi);
+            sees(a, q, div64(r0, a.group), any_lo, all_hi);
+            sees(a, q, div64(r0 + nrows - 1, a.group), all_lo, any_hi);
+        }
+        half8_t qf[kParts][kSteps];
+        float fac;
+        {
+            float top = 0.0f;
+            const int64_t off = (q.first + token) * a.q_stride + (int64_t)head * D + 8 * hh;
+#pragma unroll
+            for (int s = 0; s < kSteps; s++) {
+                float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                if (n < nrows) load_q8<BF16>(a.q, off + 16 * s, v);
+#pragma unroll
+                for (int i = 0; i < 8; i++) top = fmaxf(top, fabsf(v[i]));
+            }
+            top = fmaxf(top, __shfl_xor(top, 32));
+            // the row's largest value at 2^13 .. 2^14, as in the split kernel
+            int ex = 0;
+            if (top > 0.0f) frexpf(top, &ex);
+            fac = ldexpf(fabsf(a.scale) * kLog2e, ex - 14);
+#pragma unroll
+            for (int s = 0; s < kSteps; s++) {
+                float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                if (n < nrows) load_q8<BF16>(a.q, off + 16 * s, v);
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const float x = ldexpf(a.scale < 0.0f ? -v[i] : v[i], 14 - ex);
+                    qf[0][s][i] = (_Float16)x;
+                    if constexpr (kParts == 2) qf[1][s][i] = (_Float16)(x - (float)(_Float16)x);
+                }
+            }
+        }
+        floatx16 o[kTiles];
+#pragma unroll
+        for (int i = 0; i < kTiles; i++) o[i] = floatx16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+        float m = kLow, E = 0.0f, L = 0.0f;
+
+        // staging: item i < 256 holds 4 values of 8 positions of V, the others 32 values of a position of K
+        const int P = a.c.page_size, pm = P - 1;
+        const int32_t *table = a.s.page_table + b * a.s.table_width;
+        uint32_t st[kItems][8];
+        float st_ks = 0.0f, st_vs = 0.0f;
+        int st_page = -1;
+        int page[kItems];
+        auto item_v = [&](int i) { return S::kWaves == 8 ? wave < 4 : i == 0; };
+        const int it = tid & 255;
+        const int vg = it / (D / 4), vd = 4 * (it % (D / 4));   // V: position group, first value
+        const int kt = it / (D / 32), kc = it % (D / 32);       // K: position, chunk
+        const bool scaler = item_v(0) && it % (D / 2) == 0;      // brings a group's scales
+        const int vpos = 16 * (vg >> 1);
+        auto find_page = [&](int tile, int i) {
+            const int t = tile * T + (item_v(i) ? vpos : kt);
+            return t < q.len ? table[t >> a.page_shift] : -1;
+        };
+        auto load = [&](int tile) {
+#pragma unroll
+            for (int i = 0; i < kItems; i++) {
+                const bool ok = (uint32_t)page[i] < (uint32_t)a.c.num_pages;
+                const int64_t blk = (int64_t)(ok ? page[i] : 0) * a.c.kv_heads + h;
+                if (item_v(i)) {
+                    const int8_t *p = a.c.v + (blk * P + ((tile * T + vpos) & pm) + 4 * (vg & 1)) * D + vd;
+#pragma unroll
+                    for (int j = 0; j < 8; j++) st[i][j] = *reinterpret_cast<const uint32_t *>(p + ((j & 3) + 8 * (j >> 2)) * D);
+                    if (scaler) {
+                        st_ks = a.c.k_scale[blk];
+                        st_vs = a.c.v_scale[blk];
+                        st_page = ok;
+                    }
+                } else {
+                    const int8_t *p = a.c.k + (blk * P + ((tile * T + kt) & pm)) * D + 16 * kc;
+                    const uint4 x = *reinterpret_cast<const uint4 *>(p), y = *reinterpret_cast<const uint4 *>(p + D / 2);
+                    st[i][0] = x.x; st[i][1] = x.y; st[i][2] = x.z; st[i][3] = x.w;
+                    st[i][4] = y.x; st[i][5] = y.y; st[i][6] = y.z; st[i][7] = y.w;
+                }
+            }
+        };
+        auto store = [&](int buf) {
+#pragma unroll
+            for (int i = 0; i < kItems; i++) {
+                if (item_v(i)) {
+                    uint32_t d[8];
+#pragma unroll
+                    for (int j = 0; j < 8; j++) d[j] = st[i][j] ^ kSign4;
+                    char *p = s_v[buf];
+                    *reinterpret_cast<uint4 *>(p + v_at<D>(vd, vg)) = make_uint4(codes_pair<0>(d[0], d[1]), codes_pair<0>(d[2], d[3]), codes_pair<0>(d[4], d[5]), codes_pair<0>(d[6], d[7]));
+                    *reinterpret_cast<uint4 *>(p + v_at<D>(vd + 1, vg)) = make_uint4(codes_pair<1>(d[0], d[1]), codes_pair<1>(d[2], d[3]), codes_pair<1>(d[4], d[5]), codes_pair<1>(d[6], d[7]));
+                    *reinterpret_cast<uint4 *>(p + v_at<D>(vd + 2, vg)) = make_uint4(codes_pair<2>(d[0], d[1]), codes_pair<2>(d[2], d[3]), codes_pair<2>(d[4], d[5]), codes_pair<2>(d[6], d[7]));
+                    *reinterpret_cast<uint4 *>(p + v_at<D>(vd + 3, vg)) = make_uint4(codes_pair<3>(d[0], d[1]), codes_pair<3>(d[2], d[3]), codes_pair<3>(d[4], d[5]), codes_pair<3>(d[6], d[7]));
+                    if (scaler) {
+                        s_ks[buf][vg >> 1] = st_ks;
+                        s_vs[buf][vg >> 1] = st_vs;
+                        s_ok[buf][vg >> 1] = st_page;
+                    }
+                } else {
+                    char *p = s_k[buf];
+#pragma unroll
+                    for (int x = 0; x < 4; x++) {
+                        const int slot = 2 * kc + (x & 1) + (x >> 1) * (D / 16);
+                        *reinterpret_cast<half8_t *>(p + k_at<D>(kt, slot)) = codes_natural(st[i][2 * x], st[i][2 * x + 1]);
+                    }
+                }
+            }
+        };
+
+        const int begin = first_tile + tile0, end = begin + take;
+#pragma unroll
+        for (int i = 0; i < kItems; i++) page[i] = find_page(begin, i);
+        load(begin);
+#pragma unroll
+        for (int i = 0; i < kItems; i++) page[i] = begin + 1 < end ? find_page(begin + 1, i) : -1;
+        store(0);
+        __syncthreads();
+        for (int tile = begin; tile < end; tile++) {
+            const int buf = (tile - begin) & 1;
+            if (tile + 1 < end) {
+                load(tile + 1);
+#pragma unroll
+                for (int i = 0; i < kItems; i++) page[i] = tile + 2 < end ? find_page(tile + 2, i) : -1;
+            }
+#pragma unroll 1
+            for (int sub = 0; sub < T / 32; sub++) {
+                const int p0 = tile * T + 32 * sub;
+                if (p0 >= any_hi || p0 + 32 <= any_lo) continue;  // uniform over the wave
+                floatx16 s = floatx16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+                for (int i = 0; i < kSteps; i++) {
+                    const half8_t kf = *reinterpret_cast<const half8_t *>(s_k[buf] + k_at<D>(32 * sub + n, 2 * i + hh));
+#pragma unroll
+                    for (int pt = 0; pt < kParts; pt++) s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[pt][i], s, 0, 0, 0);
+                }
+                // the two groups of 16 positions: s[0..7], s[8..15]
+                float ks[2], vs[2], top[2];
+                bool whole = p0 >= all_lo && p0 + 32 <= all_hi;
+#pragma unroll
+                for (int u = 0; u < 2; u++) {
+                    ks[u] = s_ks[buf][2 * sub + u];
+                    vs[u] = s_vs[buf][2 * sub + u];
+                    whole = whole && s_ok[buf][2 * sub + u];
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int j = 0; j < 16; j++) {
+                        const int t = p0 + 4 * hh + 8 * (j >> 2) + (j & 3);
+                        if (!(t >= lo && t < hi && s_ok[buf][2 * sub + (j >> 3)])) s[j] = -INFINITY;
+                    }
+                }
+                float f[2], w[2];
+#pragma unroll
+                for (int u = 0; u < 2; u++) {
+                    float x = s[8 * u];
+#pragma unroll
+                    for (int j = 1; j < 8; j++) x = fmaxf(x, s[8 * u + j]);
+                    x = fmaxf(x, __shfl_xor(x, 32));
+                    // a masked score is -inf whatever the page's scale holds
+                    f[u] = fmaxf(fac * ks[u], 0x1p-126f);
+                    top[u] = ceilf(x * f[u]);
+                    if (x == -INFINITY) vs[u] = 0.0f;
+                }
+                const float mn = fmaxf(m, fmaxf(top[0], top[1]));
+                const float down = m - mn;
+                float En = E + down;
+#pragma unroll
+                for (int u = 0; u < 2; u++) {
+                    int e = -300;
+                    if (vs[u] > 0.0f) frexpf(vs[u], &e);
+                    En = fmaxf(En, (top[u] - mn) + (float)e);
+                }
+                const float turn = down + (E - En);
+#pragma unroll
+                for (int u = 0; u < 2; u++) w[u] = fminf(fmaxf(ldexpf(vs[u], (int)((float)kProbExp - En)), 0x1p-60f), 0x1p100f);
+                L *= pow2_down(down);
+                half8_t pf[2][kParts];
+                if constexpr (BF16) {
+                    const half2_t most = {(_Float16)32768.0f, (_Float16)32768.0f};
+#pragma unroll
+                    for (int u = 0; u < 2; u++) {
+                        const float c = __builtin_amdgcn_logf(w[u]) - mn;
+                        float sum = 0.0f;
+                        uint32_t r[4];
+#pragma unroll
+                        for (int j = 0; j < 8; j += 2) {
+                            const float p0x = __builtin_amdgcn_exp2f(fmaf(s[8 * u + j], f[u], c));
+                            const float p1x = __builtin_amdgcn_exp2f(fmaf(s[8 * u + j + 1], f[u], c));
+                            sum += p0x + p1x;
+                            r[j / 2] = __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(half2_t, pack_half(p0x, p1x)), most));
+                        }
+                        pf[u][0] = __builtin_bit_cast(half8_t, make_uint4(r[0], r[1], r[2], r[3]));
+                        L += sum * __builtin_amdgcn_rcpf(w[u]);
+                    }
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 2; u++)
+#pragma unroll
+                        for (int j = 0; j < 8; j++) {
+                            const float p = __builtin_amdgcn_exp2f(fmaf(s[8 * u + j], f[u], -mn));
+                            L += p;
+                            const float x = fminf(p * w[u], 32768.0f);
+                            pf[u][0][j] = (_Float16)x;
+                            pf[u][kParts - 1][j] = (_Float16)(x - (float)(_Float16)x);
+                        }
+                }
+                if (__any(turn < 0.0f)) {
+                    const float x = pow2_down(turn);
+#pragma unroll
+                    for (int i = 0; i < kTiles; i++) o[i] *= x;
+                }
+                m = mn;
+                E = En;
+#pragma unroll
+                for (int i = 0; i < kTiles; i++)
+#pragma unroll
+                    for (int u = 0; u < 2; u++) {
+                        const half8_t vf = *reinterpret_cast<const half8_t *>(s_v[buf] + v_at<D>(32 * i + n, 4 * sub + 2 * u + hh));
+#pragma unroll
+                        for (int pt = 0; pt < kParts; pt++) o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf[u][pt], o[i], 0, 0, 0);
+                    }
+            }
+            if (tile + 1 < end) store(buf ^ 1);
+            __syncthreads();
+        }
+        L += __shfl_xor(L, 32);
+
+        const bool cut = take < tiles;
+        bool write = !cut;
+        if (cut) {
+            const int64_t w_first = div64((unit0 + 1) * used - 1, line), w_end = div64((unit0 + tiles) * used - 1, line);
+            const unsigned parts = (unsigned)(w_end - w_first + 1);
+            auto piece_at = [&](int64_t x) { return pieces + (2 * x + (x == w_first ? 1 : 0)) * S::kRecord + wave * 64 * (S::kRegs + 3) + lane; };
+            if (nrows) {
+                float *p = piece_at(w);
+#pragma unroll
+                for (int i = 0; i < kTiles; i++)
+#pragma unroll
+                    for (int j = 0; j < 16; j++) put_shared(p + (16 * i + j) * 64, o[i][j]);
+                put_shared(p + S::kRegs * 64, m);
+                put_shared(p + S::kRegs * 64 + 64, E);
+                put_shared(p + S::kRegs * 64 + 128, L);
+            }
+            // every store of the piece has left before its arrival is counted
+            __builtin_amdgcn_s_waitcnt(0);
+            __syncthreads();
+            if (tid == 0) s_last = atomicInc(counters + w_first, parts - 1) == parts - 1;
+            __syncthreads();
+            write = s_last;
+            if (write && nrows) {
+                m = kLow;
+                E = 0.0f;
+                L = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kTiles; i++) o[i] = floatx16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 1
+                for (int64_t x = w_first; x <= w_end; x++) {
+                    const float *p = piece_at(x);
+                    const float pmx = get_shared(p + S::kRegs * 64), pe = get_shared(p + S::kRegs * 64 + 64), pl = get_shared(p + S::kRegs * 64 + 128);
+                    const float mn = fmaxf(m, pmx), da = m - mn, db = pmx - mn;
+                    const float en = fmaxf(E + da, pe + db);
+                    const float qa = pow2_down(da + (E - en)), qb = pow2_down(db + (pe - en));
+                    L = L * pow2_down(da) + pl * pow2_down(db);
+#pragma unroll
+                    for (int i = 0; i < kTiles; i++)
+#pragma unroll
+                        for (int j = 0; j < 16; j++) o[i][j] = o[i][j] * qa + get_shared(p + (16 * i + j) * 64) * qb;
+                    m = mn;
+                    E = en;
+                }
+            }
+            __syncthreads();  // s_last is read before the next unit's count
+        }
+        if (write && n < nrows) {
+            const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+            const int64_t off = ((q.first + token) * a.hq + head) * D + 4 * hh;
+            const int ex = (int)E + kCodeExp - kProbExp;
+#pragma unroll
+            for (int i = 0; i < kTiles; i++)
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    float v[4];
+#pragma unroll
+                    for (int c = 0; c < 4; c++) v[c] = ldexpf(o[i][4 * j + c] * inv, ex);
+                    const int64_t x = off + 32 * i + 8 * j;
+                    if constexpr (BF16) {
+                        uint2 u;
+                        u.x = (uint32_t)f32_to_bf16_rne(v[0]) | (uint32_t)f32_to_bf16_rne(v[1]) << 16;
+                        u.y = (uint32_t)f32_to_bf16_rne(v[2]) | (uint32_t)f32_to_bf16_rne(v[3]) << 16;
+                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.o) + x) = u;
+                    } else {
+                        *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + x) = make_float4(v[0], v[1], v[2], v[3]);
+                    }
+                }
+        }
+        at += take;
+    }
+}
+
+template <int D, bool BF16>
+hipError_t launch_t(const AttnArgs &a, int num_cu, hipStream_t stream) {
+    k_attn_prompt<D, BF16><<<num_cu, Shape<D, BF16>::kThreads, 0, stream>>>(a, num_cu);
+    return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_d(const AttnArgs &a, int bf16, int num_cu, hipStream_t stream) {
+    return bf16 ? launch_t<D, true>(a, num_cu, stream) : launch_t<D, false>(a, num_cu, stream);
+}
+
+}  // namespace
+
+int64_t attn_prompt_bytes(int head_dim, int num_cu) {
+    const int64_t regs = head_dim / 2;
+    return 4 * 2 * (int64_t)num_cu * 8 * 64 * (regs + 3);
+}
+
+hipError_t launch_attn_prompt(const AttnArgs &a, int bf16, int num_cu, hipStream_t stream) {
+    switch (a.c.head_dim) {
+        case 64: return launch_d<64>(a, bf16, num_cu, stream);
+        case 128: return launch_d<128>(a, bf16, num_cu, stream);
+        default: return launch_d<256>(a, bf16, num_cu, stream);
+    }
+}
+
+}  // namespace w4a8

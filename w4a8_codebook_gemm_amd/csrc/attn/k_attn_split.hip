@@ -28,7 +28,6 @@ namespace {
 
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
-constexpr float kLow = -3.0e38f;  // "no score yet"
 
 template <int D>
 struct VLoad;
@@ -57,33 +56,6 @@ __device__ __forceinline__ Work seq_work(const AttnArgs &a, int64_t b) {
         w.total = blocks * a.c.kv_heads * w.tiles;
     }
     return w;
-}
-
-__device__ __forceinline__ int64_t uniform64(int64_t x) {
-    return (int64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)x) | (int64_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32;
-}
-
-__device__ __forceinline__ int64_t scan64(int64_t x, int lane) {
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-        const int64_t o = __shfl_up((long long)x, s);
-        if (lane >= s) x += o;
-    }
-    return x;
-}
-
-// a / b for a >= 0, b > 0
-__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
-    if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
-    return a / b;
-}
-
-// A value that other workgroups read or wrote: past the per-XCD caches.
-__device__ __forceinline__ void put_shared(float *p, float v) {
-    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ float get_shared(const float *p) {
-    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 constexpr int kSumRows = 8;  // rows that join at a time
@@ -167,12 +139,6 @@ __global__ __launch_bounds__(kThreads, D == 256 || NB == 2 ? 2 : 4) void k_attn_
             token = i;
             head = h * a.group + (int)(r0 + r - i * a.group);
         };
-        auto sees = [&](int64_t token, int &from, int &to) {
-            const int64_t pos = wk.q.pos0 + token;
-            const int64_t f = a.window ? pos - a.window + 1 : 0;
-            from = f > 0 ? (int)f : 0;
-            to = a.causal ? (pos + 1 > 0 ? (int)(pos + 1) : 0) : wk.q.len;
-        };
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
             const int r = 16 * nb + n;
@@ -184,7 +150,7 @@ __global__ __launch_bounds__(kThreads, D == 256 || NB == 2 ? 2 : 4) void k_attn_
             hi[nb] = 0;
             if (r < nrows) {
                 row_at(r, token, head);
-                sees(token, lo[nb], hi[nb]);
+                sees(a, wk.q, token, lo[nb], hi[nb]);
             }
 #pragma unroll
             for (int c = 0; c < kC; c++)
@@ -225,8 +191,8 @@ __global__ __launch_bounds__(kThreads, D == 256 || NB == 2 ? 2 : 4) void k_attn_
             int hd;
             row_at(0, t_first, hd);
             row_at(nrows - 1, t_last, hd);
-            sees(t_first, any_lo, all_hi);
-            sees(t_last, all_lo, any_hi);
+            sees(a, wk.q, t_first, any_lo, all_hi);
+            sees(a, wk.q, t_last, all_lo, any_hi);
         }
 
         floatx4 o[NB][kT];
@@ -560,29 +526,23 @@ hipError_t launch_nb(const AttnArgs &a, int bf16, int num_cu, hipStream_t stream
 }
 
 template <int D>
-hipError_t launch_d(const AttnArgs &a, int bf16, int num_cu, hipStream_t stream) {
-    return a.M * a.group <= 16 * a.s.B ? launch_nb<D, 1>(a, bf16, num_cu, stream) : launch_nb<D, 2>(a, bf16, num_cu, stream);
-}
-
-template <int D>
 int64_t bytes_d(int num_cu) {
     const int64_t one = 2 * (int64_t)wgs_of<D, 1>(num_cu) * Layout<D, 1>::kRecord;
     const int64_t two = 2 * (int64_t)wgs_of<D, 2>(num_cu) * Layout<D, 2>::kRecord;
-    return kAttnCounterBytes + 4 * (one > two ? one : two);
+    return 4 * (one > two ? one : two);
 }
 
 }  // namespace
 
-int64_t attn_workspace_bytes(int64_t, int64_t, int, int, int head_dim, int num_cu) {
+int64_t attn_split_bytes(int head_dim, int num_cu) {
     return head_dim == 64 ? bytes_d<64>(num_cu) : head_dim == 128 ? bytes_d<128>(num_cu) : bytes_d<256>(num_cu);
 }
 
-hipError_t launch_kv_attention(const AttnArgs &a, int bf16, int num_cu, hipStream_t stream) {
-    if (2 * num_cu > kAttnCounterBytes / 4) return hipErrorInvalidConfiguration;
+hipError_t launch_attn_split(const AttnArgs &a, int bf16, int blocks, int num_cu, hipStream_t stream) {
     switch (a.c.head_dim) {
-        case 64: return launch_d<64>(a, bf16, num_cu, stream);
-        case 128: return launch_d<128>(a, bf16, num_cu, stream);
-        default: return launch_d<256>(a, bf16, num_cu, stream);
+        case 64: return blocks == 1 ? launch_nb<64, 1>(a, bf16, num_cu, stream) : launch_nb<64, 2>(a, bf16, num_cu, stream);
+        case 128: return blocks == 1 ? launch_nb<128, 1>(a, bf16, num_cu, stream) : launch_nb<128, 2>(a, bf16, num_cu, stream);
+        default: return blocks == 1 ? launch_nb<256, 1>(a, bf16, num_cu, stream) : launch_nb<256, 2>(a, bf16, num_cu, stream);
     }
 }
 
