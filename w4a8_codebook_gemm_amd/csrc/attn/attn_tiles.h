@@ -66,6 +66,7 @@ __device__ __forceinline__ void load_q8(const void *q, int64_t off, float v[8]) 
 // 2^x for a whole-numbered x <= 0 of any size (0 below fp32's range).
 __device__ __forceinline__ float pow2_down(float x) { return __builtin_amdgcn_exp2f(x); }
 
+constexpr int kZeroExp = -300;       // exponent of a value scale of zero
 constexpr float kLow = -3.0e38f;  // "no score yet"
 
 __device__ __forceinline__ int64_t uniform64(int64_t x) {

@@ -29,6 +29,8 @@ namespace {
 
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 
+constexpr int kMaxAhead = 4;
+constexpr float kNoPage = 1e9f;
 constexpr int kMinTiles = 4;  // tiles a workgroup is worth cutting for
 
 template <int D, bool BF16>
@@ -73,33 +75,32 @@ __device__ __forceinline__ Blocks seq_blocks(const AttnArgs &a, int64_t b) {
     return w;
 }
 
-// Byte offset of 16-byte slot `slot` (8 values) of position t in a K tile: even slots first, then
-// odd ones, mixed by the position's low bits.
+// The tiles in LDS.  Rows are 16 bytes longer than their values, so that the same 16-byte slot of
+// eight consecutive rows touches all banks, and every fragment is one address plus a constant.
+//   K: a row for each position; its 8-value slots even ones first, then odd ones (a staging thread
+//      writes a pair of them, its neighbour the next pair).
+//   V: row d / 4 + (d % 4) (D / 4) for value d (a staging thread writes four values, its neighbour the
+//      next four); slot g has the positions 16 (g / 2) + 4 (g % 2) + {0..3, 8..11}.  Row r of
+//      O^T is then value v_value(r).
 template <int D>
-__device__ __forceinline__ int k_at(int t, int slot) {
-    const int key = (t & 1) << 2 | (t & 2) | (t >> 2 & 1);
-    return t * 2 * D + (((slot >> 1) + (slot & 1) * (D / 16)) ^ key) * 16;
-}
-// Byte offset of slot `slot` (8 positions) of value d in a V tile.
-template <int D>
-__device__ __forceinline__ int v_at(int d, int slot) {
-    if constexpr (D == 256) {  // rows of 64 bytes, two to the banks' 128
-        const int x = (d >> 2 & 1) | ((d >> 1 ^ d >> 3) & 1) << 1;
-        return (d >> 1) * 128 + ((d ^ d >> 4) & 1) * 64 + (slot ^ x) * 16;
-    } else {
-        const int x = (d >> 2 & 1) | ((d ^ d >> 3) & 1) << 1 | ((d >> 1 ^ d >> 4) & 1) << 2;
-        return d * (16384 / D) + (slot ^ x) * 16;
-    }
-}
+struct Tile {
+    static constexpr int kRow = 2 * D + 16, kBytes = 8192 / D * kRow;
+    static constexpr int vRow = 16384 / D + 16, vBytes = D * vRow;
+    static __device__ __forceinline__ int k_at(int t, int slot) { return t * kRow + ((slot >> 1) + (slot & 1) * (D / 16)) * 16; }
+    static __device__ __forceinline__ int v_row(int d) { return (d >> 2) + (d & 3) * (D / 4); }
+    static __device__ __forceinline__ int v_at(int row, int slot) { return row * vRow + slot * 16; }
+};
 
 template <int D, bool BF16>
 __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_attn_prompt(AttnArgs a, int wgs) {
     using S = Shape<D, BF16>;
+    constexpr int kAhead = 2 * (D / 32) < kMaxAhead ? 2 * (D / 32) : kMaxAhead;  // V fragments in flight
     constexpr int T = S::T, kParts = BF16 ? 1 : 2, kSteps = D / 16, kTiles = D / 32;
     constexpr int kItems = 512 / S::kThreads;  // staging items of a thread: 256 of keys, 256 of values
-    __shared__ __attribute__((aligned(16))) char s_k[2][16384], s_v[2][16384];
-    __shared__ float s_ks[2][S::kGroups], s_vs[2][S::kGroups];
-    __shared__ int s_ok[2][S::kGroups];
+    using L8 = Tile<D>;
+    __shared__ __attribute__((aligned(16))) char s_k[2][L8::kBytes], s_v[2][L8::vBytes];
+    // of each group of 16 positions: key scale, value scale, its log2, its exponent (kNoPage: no such page)
+    __shared__ float4 s_sc[2][S::kGroups];
     __shared__ int s_last;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 31, hh = lane >> 5;
     uint32_t *counters = static_cast<uint32_t *>(a.ws);
@@ -255,21 +256,21 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
 #pragma unroll
                     for (int j = 0; j < 8; j++) d[j] = st[i][j] ^ kSign4;
                     char *p = s_v[buf];
-                    *reinterpret_cast<uint4 *>(p + v_at<D>(vd, vg)) = make_uint4(codes_pair<0>(d[0], d[1]), codes_pair<0>(d[2], d[3]), codes_pair<0>(d[4], d[5]), codes_pair<0>(d[6], d[7]));
-                    *reinterpret_cast<uint4 *>(p + v_at<D>(vd + 1, vg)) = make_uint4(codes_pair<1>(d[0], d[1]), codes_pair<1>(d[2], d[3]), codes_pair<1>(d[4], d[5]), codes_pair<1>(d[6], d[7]));
-                    *reinterpret_cast<uint4 *>(p + v_at<D>(vd + 2, vg)) = make_uint4(codes_pair<2>(d[0], d[1]), codes_pair<2>(d[2], d[3]), codes_pair<2>(d[4], d[5]), codes_pair<2>(d[6], d[7]));
-                    *reinterpret_cast<uint4 *>(p + v_at<D>(vd + 3, vg)) = make_uint4(codes_pair<3>(d[0], d[1]), codes_pair<3>(d[2], d[3]), codes_pair<3>(d[4], d[5]), codes_pair<3>(d[6], d[7]));
+                    *reinterpret_cast<uint4 *>(p + L8::v_at(L8::v_row(vd), vg)) = make_uint4(codes_pair<0>(d[0], d[1]), codes_pair<0>(d[2], d[3]), codes_pair<0>(d[4], d[5]), codes_pair<0>(d[6], d[7]));
+                    *reinterpret_cast<uint4 *>(p + L8::v_at(L8::v_row(vd + 1), vg)) = make_uint4(codes_pair<1>(d[0], d[1]), codes_pair<1>(d[2], d[3]), codes_pair<1>(d[4], d[5]), codes_pair<1>(d[6], d[7]));
+                    *reinterpret_cast<uint4 *>(p + L8::v_at(L8::v_row(vd + 2), vg)) = make_uint4(codes_pair<2>(d[0], d[1]), codes_pair<2>(d[2], d[3]), codes_pair<2>(d[4], d[5]), codes_pair<2>(d[6], d[7]));
+                    *reinterpret_cast<uint4 *>(p + L8::v_at(L8::v_row(vd + 3), vg)) = make_uint4(codes_pair<3>(d[0], d[1]), codes_pair<3>(d[2], d[3]), codes_pair<3>(d[4], d[5]), codes_pair<3>(d[6], d[7]));
                     if (scaler) {
-                        s_ks[buf][vg >> 1] = st_ks;
-                        s_vs[buf][vg >> 1] = st_vs;
-                        s_ok[buf][vg >> 1] = st_page;
+                        int e = kZeroExp;
+                        if (st_vs > 0.0f) frexpf(st_vs, &e);
+                        s_sc[buf][vg >> 1] = make_float4(st_ks, st_vs, __builtin_amdgcn_logf(st_vs), st_page ? (float)e : kNoPage);
                     }
                 } else {
                     char *p = s_k[buf];
 #pragma unroll
                     for (int x = 0; x < 4; x++) {
                         const int slot = 2 * kc + (x & 1) + (x >> 1) * (D / 16);
-                        *reinterpret_cast<half8_t *>(p + k_at<D>(kt, slot)) = codes_natural(st[i][2 * x], st[i][2 * x + 1]);
+                        *reinterpret_cast<half8_t *>(p + L8::k_at(kt, slot)) = codes_natural(st[i][2 * x], st[i][2 * x + 1]);
                     }
                 }
             }
@@ -294,60 +295,60 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
             for (int sub = 0; sub < T / 32; sub++) {
                 const int p0 = tile * T + 32 * sub;
                 if (p0 >= any_hi || p0 + 32 <= any_lo) continue;  // uniform over the wave
+                const float4 sc[2] = {s_sc[buf][2 * sub], s_sc[buf][2 * sub + 1]};
+                const char *kp = s_k[buf] + L8::k_at(32 * sub + n, hh), *vp = s_v[buf] + L8::v_at(n, 4 * sub + hh);
+                auto v_frag = [&](int x) {  // fragment x: values 32 (x / 2) .., group x % 2
+                    return *reinterpret_cast<const half8_t *>(vp + L8::v_at(32 * (x >> 1), 2 * (x & 1)));
+                };
                 floatx16 s = floatx16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
                 for (int i = 0; i < kSteps; i++) {
-                    const half8_t kf = *reinterpret_cast<const half8_t *>(s_k[buf] + k_at<D>(32 * sub + n, 2 * i + hh));
+                    const half8_t kf = *reinterpret_cast<const half8_t *>(kp + 16 * i);
 #pragma unroll
                     for (int pt = 0; pt < kParts; pt++) s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[pt][i], s, 0, 0, 0);
                 }
-                // the two groups of 16 positions: s[0..7], s[8..15]
-                float ks[2], vs[2], top[2];
-                bool whole = p0 >= all_lo && p0 + 32 <= all_hi;
+                half8_t vf[kAhead];
 #pragma unroll
-                for (int u = 0; u < 2; u++) {
-                    ks[u] = s_ks[buf][2 * sub + u];
-                    vs[u] = s_vs[buf][2 * sub + u];
-                    whole = whole && s_ok[buf][2 * sub + u];
-                }
-                if (!whole) {
+                for (int x = 0; x < kAhead; x++) vf[x] = v_frag(x);
+                __builtin_amdgcn_sched_barrier(0);
+                // the two groups of 16 positions: s[0..7], s[8..15]
+                if (!(p0 >= all_lo && p0 + 32 <= all_hi && fmaxf(sc[0].w, sc[1].w) < kNoPage)) {
+                    const int from = lo - p0 - 4 * hh, to = hi - p0 - 4 * hh;
 #pragma unroll
                     for (int j = 0; j < 16; j++) {
-                        const int t = p0 + 4 * hh + 8 * (j >> 2) + (j & 3);
-                        if (!(t >= lo && t < hi && s_ok[buf][2 * sub + (j >> 3)])) s[j] = -INFINITY;
+                        const int t = 8 * (j >> 2) + (j & 3);
+                        const bool see = (t >= from) & (t < to) & (sc[j >> 3].w < kNoPage);
+                        s[j] = see ? s[j] : -INFINITY;
                     }
                 }
-                float f[2], w[2];
+                float f[2], top[2], e[2];
 #pragma unroll
                 for (int u = 0; u < 2; u++) {
-                    float x = s[8 * u];
-#pragma unroll
-                    for (int j = 1; j < 8; j++) x = fmaxf(x, s[8 * u + j]);
+                    float x = fmaxf(fmaxf(s[8 * u], s[8 * u + 1]), s[8 * u + 2]);
+                    x = fmaxf(fmaxf(x, s[8 * u + 3]), s[8 * u + 4]);
+                    x = fmaxf(fmaxf(x, s[8 * u + 5]), fmaxf(s[8 * u + 6], s[8 * u + 7]));
                     x = fmaxf(x, __shfl_xor(x, 32));
                     // a masked score is -inf whatever the page's scale holds
-                    f[u] = fmaxf(fac * ks[u], 0x1p-126f);
+                    f[u] = fmaxf(fac * sc[u].x, 0x1p-126f);
                     top[u] = ceilf(x * f[u]);
-                    if (x == -INFINITY) vs[u] = 0.0f;
+                    e[u] = x == -INFINITY ? (float)kZeroExp : sc[u].w;
                 }
                 const float mn = fmaxf(m, fmaxf(top[0], top[1]));
                 const float down = m - mn;
-                float En = E + down;
-#pragma unroll
-                for (int u = 0; u < 2; u++) {
-                    int e = -300;
-                    if (vs[u] > 0.0f) frexpf(vs[u], &e);
-                    En = fmaxf(En, (top[u] - mn) + (float)e);
-                }
+                // E grows by more than it has to, so that it seldom does; not where the products are
+                // wanted to fp32's precision, 2^-25 of the largest then
+                const float need = fmaxf((top[0] - mn) + e[0], (top[1] - mn) + e[1]);
+                const float En = need > E + down ? need + (BF16 ? 4.0f : 0.0f) : E + down;
                 const float turn = down + (E - En);
-#pragma unroll
-                for (int u = 0; u < 2; u++) w[u] = fminf(fmaxf(ldexpf(vs[u], (int)((float)kProbExp - En)), 0x1p-60f), 0x1p100f);
                 L *= pow2_down(down);
                 half8_t pf[2][kParts];
                 if constexpr (BF16) {
                     const half2_t most = {(_Float16)32768.0f, (_Float16)32768.0f};
 #pragma unroll
                     for (int u = 0; u < 2; u++) {
-                        const float c = __builtin_amdgcn_logf(w[u]) - mn;
+                        // a page whose values are not seen may hold any scale
+                        const float lw = e[u] > (float)kZeroExp ? fmaxf(sc[u].z + ((float)kProbExp - En), -60.0f) : -60.0f;
+                        const float c = lw - mn;
                         float sum = 0.0f;
                         uint32_t r[4];
 #pragma unroll
@@ -358,19 +359,21 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
                             r[j / 2] = __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(half2_t, pack_half(p0x, p1x)), most));
                         }
                         pf[u][0] = __builtin_bit_cast(half8_t, make_uint4(r[0], r[1], r[2], r[3]));
-                        L += sum * __builtin_amdgcn_rcpf(w[u]);
+                        L = fmaf(sum, __builtin_amdgcn_exp2f(-lw), L);
                     }
                 } else {
 #pragma unroll
-                    for (int u = 0; u < 2; u++)
+                    for (int u = 0; u < 2; u++) {
+                        const float w = e[u] > (float)kZeroExp ? fminf(ldexpf(sc[u].y, (int)((float)kProbExp - En)), 0x1p100f) : 0.0f;
 #pragma unroll
                         for (int j = 0; j < 8; j++) {
                             const float p = __builtin_amdgcn_exp2f(fmaf(s[8 * u + j], f[u], -mn));
                             L += p;
-                            const float x = fminf(p * w[u], 32768.0f);
+                            const float x = fminf(p * w, 32768.0f);
                             pf[u][0][j] = (_Float16)x;
                             pf[u][kParts - 1][j] = (_Float16)(x - (float)(_Float16)x);
                         }
+                    }
                 }
                 if (__any(turn < 0.0f)) {
                     const float x = pow2_down(turn);
@@ -379,14 +382,16 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
                 }
                 m = mn;
                 E = En;
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int i = 0; i < kTiles; i++)
+                for (int x = 0; x < 2 * kTiles; x++) {
+                    const half8_t v = vf[x % kAhead];
+                    if (x + kAhead < 2 * kTiles) vf[x % kAhead] = v_frag(x + kAhead);
 #pragma unroll
-                    for (int u = 0; u < 2; u++) {
-                        const half8_t vf = *reinterpret_cast<const half8_t *>(s_v[buf] + v_at<D>(32 * i + n, 4 * sub + 2 * u + hh));
-#pragma unroll
-                        for (int pt = 0; pt < kParts; pt++) o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf[u][pt], o[i], 0, 0, 0);
-                    }
+                    for (int pt = 0; pt < kParts; pt++)
+                        o[x >> 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, pf[x & 1][pt], o[x >> 1], 0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
             if (tile + 1 < end) store(buf ^ 1);
             __syncthreads();
@@ -441,25 +446,28 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
         }
         if (write && n < nrows) {
             const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-            const int64_t off = ((q.first + token) * a.hq + head) * D + 4 * hh;
+            const int64_t off = ((q.first + token) * a.hq + head) * D;
             const int ex = (int)E + kCodeExp - kProbExp;
+            // value 4 x + y is in row x + y (D / 4) of O^T; this lane has the rows 32 i + 8 j + 4 hh + c
 #pragma unroll
-            for (int i = 0; i < kTiles; i++)
+            for (int z = 0; z < D / 8; z++) {
+                const int x = (z >> 2) * 8 + (z & 3);   // and + 4 hh
+                float v[4];
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    float v[4];
-#pragma unroll
-                    for (int c = 0; c < 4; c++) v[c] = ldexpf(o[i][4 * j + c] * inv, ex);
-                    const int64_t x = off + 32 * i + 8 * j;
-                    if constexpr (BF16) {
-                        uint2 u;
-                        u.x = (uint32_t)f32_to_bf16_rne(v[0]) | (uint32_t)f32_to_bf16_rne(v[1]) << 16;
-                        u.y = (uint32_t)f32_to_bf16_rne(v[2]) | (uint32_t)f32_to_bf16_rne(v[3]) << 16;
-                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.o) + x) = u;
-                    } else {
-                        *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + x) = make_float4(v[0], v[1], v[2], v[3]);
-                    }
+                for (int y = 0; y < 4; y++) {
+                    const int row = x + y * (D / 4);
+                    v[y] = ldexpf(o[row >> 5][((row & 31) >> 3) * 4 + (row & 3)] * inv, ex);
                 }
+                const int64_t d = off + 4 * (x + 4 * hh);
+                if constexpr (BF16) {
+                    uint2 u;
+                    u.x = (uint32_t)f32_to_bf16_rne(v[0]) | (uint32_t)f32_to_bf16_rne(v[1]) << 16;
+                    u.y = (uint32_t)f32_to_bf16_rne(v[2]) | (uint32_t)f32_to_bf16_rne(v[3]) << 16;
+                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.o) + d) = u;
+                } else {
+                    *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + d) = make_float4(v[0], v[1], v[2], v[3]);
+                }
+            }
         }
         at += take;
     }
