@@ -59,20 +59,32 @@ __device__ __forceinline__ int block_tiles(const AttnArgs &a, const Seq &q, int6
     return n < 1 ? 1 : n;  // rows that see nothing are still written
 }
 
-struct Blocks {
-    Seq q;
-    int64_t blocks, tiles;  // of one cache head
-};
-
 template <int D, bool BF16>
-__device__ __forceinline__ Blocks seq_blocks(const AttnArgs &a, int64_t b) {
-    Blocks w;
-    w.q = load_seq(a.s, a.M, a.page_shift, b);
-    w.blocks = ((int64_t)w.q.n * a.group + Shape<D, BF16>::RB - 1) / Shape<D, BF16>::RB;
-    w.tiles = 0;
+__device__ __forceinline__ int64_t blocks_of(const AttnArgs &a, const Seq &q) {
+    return div64((int64_t)q.n * a.group + Shape<D, BF16>::RB - 1, Shape<D, BF16>::RB);
+}
+
+// Tiles of sequence b0 + lane on the line.  Called by whole waves: sequences of many blocks are
+// summed by all lanes together.
+template <int D, bool BF16>
+__device__ __forceinline__ int64_t seq_tiles(const AttnArgs &a, int64_t b0, int lane) {
+    Seq q{0, 0, 0, 0};
+    if (b0 + lane < a.s.B) q = load_seq(a.s, a.M, a.page_shift, b0 + lane);
+    const int64_t blocks = blocks_of<D, BF16>(a, q);
+    int64_t tiles = 0;
     int x;
-    for (int64_t i = 0; i < w.blocks; i++) w.tiles += block_tiles<D, BF16>(a, w.q, i, x);
-    return w;
+    for (int64_t i = 0; i < (blocks <= 4 ? blocks : 0); i++) tiles += block_tiles<D, BF16>(a, q, i, x);
+    for (uint64_t many = __ballot(blocks > 4); many; many &= many - 1) {
+        const int src = __ffsll((unsigned long long)many) - 1;
+        const Seq r = {0, __shfl(q.n, src), __shfl(q.len, src), __shfl(q.pos0, src)};
+        const int64_t rb = blocks_of<D, BF16>(a, r);
+        int64_t sum = 0;
+        for (int64_t i = lane; i < rb; i += 64) sum += block_tiles<D, BF16>(a, r, i, x);
+#pragma unroll
+        for (int s = 1; s < 64; s <<= 1) sum += __shfl_xor((long long)sum, s);
+        if (lane == src) tiles = sum;
+    }
+    return tiles * a.c.kv_heads;
 }
 
 // The tiles in LDS.  Rows are 16 bytes longer than their values, so that the same 16-byte slot of
@@ -106,9 +118,13 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
     uint32_t *counters = static_cast<uint32_t *>(a.ws);
     float *pieces = reinterpret_cast<float *>(static_cast<char *>(a.ws) + kAttnCounterBytes);
 
-    int64_t line = 0;
-    for (int64_t b0 = 0; b0 < a.s.B; b0 += 64)
-        line += __shfl((long long)scan64(b0 + lane < a.s.B ? seq_blocks<D, BF16>(a, b0 + lane).tiles * a.c.kv_heads : 0, lane), 63);
+    // the sequences' ends on the line; of the only 64 where there are no more
+    int64_t line = 0, mine = 0, incl = 0;
+    for (int64_t b0 = 0; b0 < a.s.B; b0 += 64) {
+        mine = seq_tiles<D, BF16>(a, b0, lane);
+        incl = scan64(mine, lane);
+        line += __shfl((long long)incl, 63);
+    }
     line = uniform64(line);
     if (line == 0) return;
     int64_t used = (line + kMinTiles - 1) / kMinTiles;
@@ -121,28 +137,28 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
 
     for (int64_t at = t0; at < t1;) {
         // the sequence, cache head and row block that tile `at` is in
-        int64_t base = 0, b = 0, blocks = 0, per_head = 0;
-        Seq q{};
+        int64_t base = 0, b = 0, per_head = 0;
         for (int64_t b0 = 0; b0 < a.s.B; b0 += 64) {
-            Blocks x{};
-            if (b0 + lane < a.s.B) x = seq_blocks<D, BF16>(a, b0 + lane);
-            const int64_t mine = x.tiles * a.c.kv_heads;
-            const int64_t incl = scan64(mine, lane);
+            if (a.s.B > 64) {
+                mine = seq_tiles<D, BF16>(a, b0, lane);
+                incl = scan64(mine, lane);
+            }
             const int64_t sum = uniform64(__shfl((long long)incl, 63));
             if (at < base + sum) {
                 const int src = __ffsll((unsigned long long)__ballot(at - base < incl)) - 1;
                 b = b0 + src;
                 base += uniform64(__shfl((long long)(incl - mine), src));
-                q.first = uniform64(__shfl((long long)x.q.first, src));
-                q.n = __builtin_amdgcn_readfirstlane(__shfl(x.q.n, src));
-                q.len = __builtin_amdgcn_readfirstlane(__shfl(x.q.len, src));
-                q.pos0 = q.len - q.n;
-                blocks = uniform64(__shfl((long long)x.blocks, src));
-                per_head = uniform64(__shfl((long long)x.tiles, src));
+                per_head = div64(uniform64(__shfl((long long)mine, src)), a.c.kv_heads);
                 break;
             }
             base += sum;
         }
+        Seq q = load_seq(a.s, a.M, a.page_shift, b);
+        q.first = uniform64(q.first);
+        q.n = __builtin_amdgcn_readfirstlane(q.n);
+        q.len = __builtin_amdgcn_readfirstlane(q.len);
+        q.pos0 = q.len - q.n;
+        const int64_t blocks = blocks_of<D, BF16>(a, q);
         const int h = (int)div64(at - base, per_head);
         int64_t unit0 = base + h * per_head, rb = 0;  // the unit's first tile on the line
         int first_tile = 0, tiles = 1;
