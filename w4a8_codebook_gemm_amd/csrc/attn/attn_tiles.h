@@ -69,6 +69,12 @@ __device__ __forceinline__ float pow2_down(float x) { return __builtin_amdgcn_ex
 constexpr int kZeroExp = -300;       // exponent of a value scale of zero
 constexpr float kLow = -3.0e38f;  // "no score yet"
 
+// x, as a value the compiler works from anew: what hangs on it is not kept in registers across a loop.
+__device__ __forceinline__ int fresh(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 __device__ __forceinline__ int64_t uniform64(int64_t x) {
     return (int64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)x) | (int64_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32;
 }
@@ -94,6 +100,64 @@ __device__ __forceinline__ void put_shared(float *p, float v) {
 }
 __device__ __forceinline__ float get_shared(const float *p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The same for four values of a piece: `off` bytes from a base that is uniform over the wave, in
+// 16-byte accesses at device scope (cache bit sc1).
+typedef uint32_t uintx4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t shared_piece(const float *base, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc((void *)base, (short)0, bytes, 0x00020000);
+}
+__device__ __forceinline__ void put_shared4(__amdgpu_buffer_rsrc_t r, int off, float a, float b, float c, float d) {
+    const uintx4 v = {__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d)};
+    __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, 16);
+}
+__device__ __forceinline__ floatx4 get_shared4(__amdgpu_buffer_rsrc_t r, int off) {
+    return __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 16));
+}
+
+// A running softmax: maximum m, exponent E of the weighted sum, sum L of the probabilities.  Joining
+// two of them returns the factors for their weighted sums.
+struct State {
+    float m, E, L;
+};
+__device__ __forceinline__ State join(const State &a, const State &b, float &qa, float &qb) {
+    State s;
+    s.m = fmaxf(a.m, b.m);
+    const float da = a.m - s.m, db = b.m - s.m;
+    s.E = fmaxf(a.E + da, b.E + db);
+    s.L = a.L * pow2_down(da) + b.L * pow2_down(db);
+    qa = pow2_down(da + (a.E - s.E));
+    qb = pow2_down(db + (b.E - s.E));
+    return s;
+}
+
+// The pieces of a cut unit are joined two and two in a tree: a workgroup leaves what it holds in the
+// slot of its first piece and counts its arrival at the boundary it shares with its sibling; the
+// second to arrive takes the sibling's, joins, and goes on a level up.  The sums do not depend on
+// the order of arrival.  `counters` has one word for each workgroup: a piece is the first of a right
+// subtree at one boundary of one unit.  put(p) leaves this workgroup's part in piece p's slot, take(p)
+// joins piece p's slot to it.  True for the workgroup that ends with the whole unit.
+template <class Put, class Take>
+__device__ __forceinline__ bool join_pieces(uint32_t *counters, int64_t w_first, int64_t w, int64_t w_end, int *s_flag, Put put, Take take) {
+    const unsigned parts = (unsigned)(w_end - w_first + 1);
+    unsigned lo = (unsigned)(w - w_first);
+    for (unsigned size = 1; size < parts; size *= 2) {
+        const unsigned other = lo & size ? lo - size : lo + size;
+        if (other >= parts) continue;
+        put(lo);
+        // every store has left before the arrival is counted
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        if (threadIdx.x == 0) *s_flag = atomicInc(counters + w_first + (lo > other ? lo : other), 1u) == 1u;
+        __syncthreads();
+        const bool second = *s_flag;
+        __syncthreads();
+        if (!second) return false;
+        take(other);
+        if (other < lo) lo = other;
+    }
+    return true;
 }
 
 // The positions [from, to) that new token i of a sequence sees.

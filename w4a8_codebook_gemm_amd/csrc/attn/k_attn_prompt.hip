@@ -21,7 +21,7 @@
 // range and only the sum of p counts them.
 //
 // Split: as in the split kernel, the tiles of all units form one line that is cut evenly over the
-// workgroups; a cut unit's pieces are joined by the last workgroup to arrive, in order.
+// workgroups; a cut unit's pieces are joined two and two in a tree.
 #include "attn_tiles.h"
 
 namespace w4a8 {
@@ -29,7 +29,7 @@ namespace {
 
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 
-constexpr int kMaxAhead = 4;
+constexpr int kQFar = 2;
 constexpr float kNoPage = 1e9f;
 constexpr int kMinTiles = 4;  // tiles a workgroup is worth cutting for
 
@@ -42,7 +42,8 @@ struct Shape {
     static constexpr int T = 8192 / D;       // positions of a tile
     static constexpr int kGroups = T / 16;
     static constexpr int kRegs = D / 2;      // floats of O^T in a lane
-    static constexpr int kRecord = kWaves * 64 * (kRegs + 3);
+    static constexpr int kWaveRecord = 64 * (kRegs + 4);    // a wave's piece: O^T, then m, E, L
+    static constexpr int kRecord = kWaves * kWaveRecord;
 };
 
 // First tile and tiles of row block rb of a sequence.
@@ -106,24 +107,29 @@ struct Tile {
 template <int D, bool BF16>
 __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_attn_prompt(AttnArgs a, int wgs) {
     using S = Shape<D, BF16>;
-    constexpr int kAhead = 2 * (D / 32) < kMaxAhead ? 2 * (D / 32) : kMaxAhead;  // V fragments in flight
+    constexpr int kAhead = D == 128 ? 4 : 2;  // V fragments in flight
     constexpr int T = S::T, kParts = BF16 ? 1 : 2, kSteps = D / 16, kTiles = D / 32;
+    constexpr int kQLds = D == 256 && BF16 ? kQFar : 0;  // query fragments that stay in LDS
     constexpr int kItems = 512 / S::kThreads;  // staging items of a thread: 256 of keys, 256 of values
     using L8 = Tile<D>;
     __shared__ __attribute__((aligned(16))) char s_k[2][L8::kBytes], s_v[2][L8::vBytes];
     // of each group of 16 positions: key scale, value scale, its log2, its exponent (kNoPage: no such page)
     __shared__ float4 s_sc[2][S::kGroups];
-    __shared__ int s_last;
+    __shared__ __attribute__((aligned(16))) char s_q[kQLds ? kQLds * S::kThreads * 16 : 16];
+    __shared__ int64_t s_mine[64], s_incl[64];  // tiles of the only 64 sequences, and up to each
+    __shared__ int s_flag;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 31, hh = lane >> 5;
     uint32_t *counters = static_cast<uint32_t *>(a.ws);
     float *pieces = reinterpret_cast<float *>(static_cast<char *>(a.ws) + kAttnCounterBytes);
 
-    // the sequences' ends on the line; of the only 64 where there are no more
-    int64_t line = 0, mine = 0, incl = 0;
+    int64_t line = 0;
     for (int64_t b0 = 0; b0 < a.s.B; b0 += 64) {
-        mine = seq_tiles<D, BF16>(a, b0, lane);
-        incl = scan64(mine, lane);
+        const int64_t mine = seq_tiles<D, BF16>(a, b0, lane), incl = scan64(mine, lane);
         line += __shfl((long long)incl, 63);
+        if (a.s.B <= 64) {  // every wave writes the same and reads its own
+            s_mine[lane] = mine;
+            s_incl[lane] = incl;
+        }
     }
     line = uniform64(line);
     if (line == 0) return;
@@ -139,10 +145,8 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
         // the sequence, cache head and row block that tile `at` is in
         int64_t base = 0, b = 0, per_head = 0;
         for (int64_t b0 = 0; b0 < a.s.B; b0 += 64) {
-            if (a.s.B > 64) {
-                mine = seq_tiles<D, BF16>(a, b0, lane);
-                incl = scan64(mine, lane);
-            }
+            const int64_t mine = a.s.B <= 64 ? s_mine[lane] : seq_tiles<D, BF16>(a, b0, lane);
+            const int64_t incl = a.s.B <= 64 ? s_incl[lane] : scan64(mine, lane);
             const int64_t sum = uniform64(__shfl((long long)incl, 63));
             if (at < base + sum) {
                 const int src = __ffsll((unsigned long long)__ballot(at - base < incl)) - 1;
@@ -182,19 +186,29 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
         // this wave's rows
         const int64_t rows = (int64_t)q.n * a.group, r0 = rb * S::RB + 32 * wave;
         const int nrows = rows - r0 < 0 ? 0 : rows - r0 < 32 ? (int)(rows - r0) : 32;
-        const int64_t my = r0 + (n < nrows ? n : 0);
-        const int64_t token = nrows ? div64(my, a.group) : 0;
-        const int head = h * a.group + (int)(my - token * a.group);
-        int lo = 0, hi = 0, all_lo = 0, all_hi = 0, any_lo = 0, any_hi = 0;
+        // the row's token and head, found again where they are wanted: registers are what the loop lacks
+        auto row_of = [&](int64_t &token, int &head) {
+            const int l = fresh(lane) & 31;
+            const int64_t my = r0 + (l < nrows ? l : 0);
+            token = div64(my, a.group);
+            head = h * a.group + (int)(my - token * a.group);
+        };
+        int hi = 0, all_lo = 0, all_hi = 0, any_lo = 0, any_hi = 0;
         if (nrows) {
-            if (n < nrows) sees(a, q, token, lo, hi);
+            int64_t token;
+            int x;
+            row_of(token, x);
+            if (n < nrows) sees(a, q, token, x, hi);
             sees(a, q, div64(r0, a.group), any_lo, all_hi);
             sees(a, q, div64(r0 + nrows - 1, a.group), all_lo, any_hi);
         }
-        half8_t qf[kParts][kSteps];
+        half8_t qf[kParts][kSteps - kQLds];
         float fac;
         {
             float top = 0.0f;
+            int64_t token = 0;
+            int head = 0;
+            if (nrows) row_of(token, head);
             const int64_t off = (q.first + token) * a.q_stride + (int64_t)head * D + 8 * hh;
 #pragma unroll
             for (int s = 0; s < kSteps; s++) {
@@ -214,10 +228,15 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
                 if (n < nrows) load_q8<BF16>(a.q, off + 16 * s, v);
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
-                    const float x = ldexpf(a.scale < 0.0f ? -v[i] : v[i], 14 - ex);
-                    qf[0][s][i] = (_Float16)x;
-                    if constexpr (kParts == 2) qf[1][s][i] = (_Float16)(x - (float)(_Float16)x);
+                    v[i] = ldexpf(a.scale < 0.0f ? -v[i] : v[i], 14 - ex);
+                    if (s < kSteps - kQLds) {
+                        qf[0][s][i] = (_Float16)v[i];
+                        if constexpr (kParts == 2) qf[1][s][i] = (_Float16)(v[i] - (float)(_Float16)v[i]);
+                    }
                 }
+                if (s >= kSteps - kQLds)
+                    *reinterpret_cast<uint4 *>(s_q + (s - (kSteps - kQLds)) * S::kThreads * 16 + tid * 16) =
+                        make_uint4(pack_half(v[0], v[1]), pack_half(v[2], v[3]), pack_half(v[4], v[5]), pack_half(v[6], v[7]));
             }
         }
         floatx16 o[kTiles];
@@ -229,17 +248,30 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
         const int P = a.c.page_size, pm = P - 1;
         const int32_t *table = a.s.page_table + b * a.s.table_width;
         uint32_t st[kItems][8];
-        float st_ks = 0.0f, st_vs = 0.0f;
-        int st_page = -1;
+        float st_ks = 0.0f, st_vs = 0.0f;   // key scale: -1 where the page is not there
         int page[kItems];
         auto item_v = [&](int i) { return S::kWaves == 8 ? wave < 4 : i == 0; };
-        const int it = tid & 255;
-        const int vg = it / (D / 4), vd = 4 * (it % (D / 4));   // V: position group, first value
-        const int kt = it / (D / 32), kc = it % (D / 32);       // K: position, chunk
-        const bool scaler = item_v(0) && it % (D / 2) == 0;      // brings a group's scales
-        const int vpos = 16 * (vg >> 1);
+        // V: position group, first value; K: position, chunk
+        auto place_v = [&](int &vg, int &vd) {
+            const int it = fresh(tid) & 255;
+            vg = it / (D / 4);
+            vd = 4 * (it % (D / 4));
+        };
+        auto place_k = [&](int &kt, int &kc) {
+            const int it = fresh(tid) & 255;
+            kt = it / (D / 32);
+            kc = it % (D / 32);
+        };
+        auto scaler = [&]() { return (fresh(tid) & 255) % (D / 2) == 0; };  // brings a group's scales
         auto find_page = [&](int tile, int i) {
-            const int t = tile * T + (item_v(i) ? vpos : kt);
+            int x, y;
+            if (item_v(i)) {
+                place_v(x, y);
+                x = 16 * (x >> 1);
+            } else {
+                place_k(x, y);
+            }
+            const int t = tile * T + x;
             return t < q.len ? table[t >> a.page_shift] : -1;
         };
         auto load = [&](int tile) {
@@ -248,15 +280,18 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
                 const bool ok = (uint32_t)page[i] < (uint32_t)a.c.num_pages;
                 const int64_t blk = (int64_t)(ok ? page[i] : 0) * a.c.kv_heads + h;
                 if (item_v(i)) {
-                    const int8_t *p = a.c.v + (blk * P + ((tile * T + vpos) & pm) + 4 * (vg & 1)) * D + vd;
+                    int vg, vd;
+                    place_v(vg, vd);
+                    const int8_t *p = a.c.v + (blk * P + ((tile * T + 16 * (vg >> 1)) & pm) + 4 * (vg & 1)) * D + vd;
 #pragma unroll
                     for (int j = 0; j < 8; j++) st[i][j] = *reinterpret_cast<const uint32_t *>(p + ((j & 3) + 8 * (j >> 2)) * D);
-                    if (scaler) {
-                        st_ks = a.c.k_scale[blk];
+                    if (scaler()) {
+                        st_ks = ok ? a.c.k_scale[blk] : -1.0f;
                         st_vs = a.c.v_scale[blk];
-                        st_page = ok;
                     }
                 } else {
+                    int kt, kc;
+                    place_k(kt, kc);
                     const int8_t *p = a.c.k + (blk * P + ((tile * T + kt) & pm)) * D + 16 * kc;
                     const uint4 x = *reinterpret_cast<const uint4 *>(p), y = *reinterpret_cast<const uint4 *>(p + D / 2);
                     st[i][0] = x.x; st[i][1] = x.y; st[i][2] = x.z; st[i][3] = x.w;
@@ -268,26 +303,28 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
 #pragma unroll
             for (int i = 0; i < kItems; i++) {
                 if (item_v(i)) {
+                    int vg, vd;
+                    place_v(vg, vd);
+                    char *p = s_v[buf] + L8::v_at(L8::v_row(vd), vg);  // values vd + y: y (D / 4) rows on
                     uint32_t d[8];
 #pragma unroll
                     for (int j = 0; j < 8; j++) d[j] = st[i][j] ^ kSign4;
-                    char *p = s_v[buf];
-                    *reinterpret_cast<uint4 *>(p + L8::v_at(L8::v_row(vd), vg)) = make_uint4(codes_pair<0>(d[0], d[1]), codes_pair<0>(d[2], d[3]), codes_pair<0>(d[4], d[5]), codes_pair<0>(d[6], d[7]));
-                    *reinterpret_cast<uint4 *>(p + L8::v_at(L8::v_row(vd + 1), vg)) = make_uint4(codes_pair<1>(d[0], d[1]), codes_pair<1>(d[2], d[3]), codes_pair<1>(d[4], d[5]), codes_pair<1>(d[6], d[7]));
-                    *reinterpret_cast<uint4 *>(p + L8::v_at(L8::v_row(vd + 2), vg)) = make_uint4(codes_pair<2>(d[0], d[1]), codes_pair<2>(d[2], d[3]), codes_pair<2>(d[4], d[5]), codes_pair<2>(d[6], d[7]));
-                    *reinterpret_cast<uint4 *>(p + L8::v_at(L8::v_row(vd + 3), vg)) = make_uint4(codes_pair<3>(d[0], d[1]), codes_pair<3>(d[2], d[3]), codes_pair<3>(d[4], d[5]), codes_pair<3>(d[6], d[7]));
-                    if (scaler) {
+                    *reinterpret_cast<uint4 *>(p) = make_uint4(codes_pair<0>(d[0], d[1]), codes_pair<0>(d[2], d[3]), codes_pair<0>(d[4], d[5]), codes_pair<0>(d[6], d[7]));
+                    *reinterpret_cast<uint4 *>(p + L8::v_at(D / 4, 0)) = make_uint4(codes_pair<1>(d[0], d[1]), codes_pair<1>(d[2], d[3]), codes_pair<1>(d[4], d[5]), codes_pair<1>(d[6], d[7]));
+                    *reinterpret_cast<uint4 *>(p + L8::v_at(D / 2, 0)) = make_uint4(codes_pair<2>(d[0], d[1]), codes_pair<2>(d[2], d[3]), codes_pair<2>(d[4], d[5]), codes_pair<2>(d[6], d[7]));
+                    *reinterpret_cast<uint4 *>(p + L8::v_at(3 * D / 4, 0)) = make_uint4(codes_pair<3>(d[0], d[1]), codes_pair<3>(d[2], d[3]), codes_pair<3>(d[4], d[5]), codes_pair<3>(d[6], d[7]));
+                    if (scaler()) {
                         int e = kZeroExp;
                         if (st_vs > 0.0f) frexpf(st_vs, &e);
-                        s_sc[buf][vg >> 1] = make_float4(st_ks, st_vs, __builtin_amdgcn_logf(st_vs), st_page ? (float)e : kNoPage);
+                        s_sc[buf][vg >> 1] = make_float4(st_ks, st_vs, __builtin_amdgcn_logf(st_vs), st_ks < 0.0f ? kNoPage : (float)e);
                     }
                 } else {
-                    char *p = s_k[buf];
+                    int kt, kc;
+                    place_k(kt, kc);
+                    char *p = s_k[buf] + L8::k_at(kt, 2 * kc);
 #pragma unroll
-                    for (int x = 0; x < 4; x++) {
-                        const int slot = 2 * kc + (x & 1) + (x >> 1) * (D / 16);
-                        *reinterpret_cast<half8_t *>(p + L8::k_at(kt, slot)) = codes_natural(st[i][2 * x], st[i][2 * x + 1]);
-                    }
+                    for (int x = 0; x < 4; x++)
+                        *reinterpret_cast<half8_t *>(p + L8::k_at(0, (x & 1) + (x >> 1) * (D / 16))) = codes_natural(st[i][2 * x], st[i][2 * x + 1]);
                 }
             }
         };
@@ -312,16 +349,28 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
                 const int p0 = tile * T + 32 * sub;
                 if (p0 >= any_hi || p0 + 32 <= any_lo) continue;  // uniform over the wave
                 const float4 sc[2] = {s_sc[buf][2 * sub], s_sc[buf][2 * sub + 1]};
-                const char *kp = s_k[buf] + L8::k_at(32 * sub + n, hh), *vp = s_v[buf] + L8::v_at(n, 4 * sub + hh);
+                const int ln = fresh(lane);
+                const char *kp = s_k[buf] + L8::k_at(32 * sub + (ln & 31), ln >> 5), *vp = s_v[buf] + L8::v_at(ln & 31, 4 * sub + (ln >> 5));
                 auto v_frag = [&](int x) {  // fragment x: values 32 (x / 2) .., group x % 2
                     return *reinterpret_cast<const half8_t *>(vp + L8::v_at(32 * (x >> 1), 2 * (x & 1)));
                 };
                 floatx16 s = floatx16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+                half8_t kf[kAhead];
+#pragma unroll
+                for (int x = 0; x < kAhead; x++) kf[x] = *reinterpret_cast<const half8_t *>(kp + 16 * x);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int i = 0; i < kSteps; i++) {
-                    const half8_t kf = *reinterpret_cast<const half8_t *>(kp + 16 * i);
+                    const half8_t k = kf[i % kAhead];
+                    if (i + kAhead < kSteps) kf[i % kAhead] = *reinterpret_cast<const half8_t *>(kp + 16 * (i + kAhead));
+                    if (i >= kSteps - kQLds) {
+                        const half8_t qx = *reinterpret_cast<const half8_t *>(s_q + (i - (kSteps - kQLds)) * S::kThreads * 16 + tid * 16);
+                        s = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, qx, s, 0, 0, 0);
+                    } else {
 #pragma unroll
-                    for (int pt = 0; pt < kParts; pt++) s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[pt][i], s, 0, 0, 0);
+                        for (int pt = 0; pt < kParts; pt++) s = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, qf[pt][i < kSteps - kQLds ? i : 0], s, 0, 0, 0);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
                 half8_t vf[kAhead];
 #pragma unroll
@@ -329,7 +378,7 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
                 __builtin_amdgcn_sched_barrier(0);
                 // the two groups of 16 positions: s[0..7], s[8..15]
                 if (!(p0 >= all_lo && p0 + 32 <= all_hi && fmaxf(sc[0].w, sc[1].w) < kNoPage)) {
-                    const int from = lo - p0 - 4 * hh, to = hi - p0 - 4 * hh;
+                    const int to = hi - p0 - 4 * (ln >> 5), from = a.window ? to - (int)a.window : -p0 - 32;
 #pragma unroll
                     for (int j = 0; j < 16; j++) {
                         const int t = 8 * (j >> 2) + (j & 3);
@@ -414,54 +463,51 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
         }
         L += __shfl_xor(L, 32);
 
-        const bool cut = take < tiles;
-        bool write = !cut;
-        if (cut) {
+        bool write = true;
+        if (take < tiles) {
             const int64_t w_first = div64((unit0 + 1) * used - 1, line), w_end = div64((unit0 + tiles) * used - 1, line);
-            const unsigned parts = (unsigned)(w_end - w_first + 1);
-            auto piece_at = [&](int64_t x) { return pieces + (2 * x + (x == w_first ? 1 : 0)) * S::kRecord + wave * 64 * (S::kRegs + 3) + lane; };
-            if (nrows) {
-                float *p = piece_at(w);
+            auto slot = [&](unsigned x) {
+                return shared_piece(pieces + (2 * (w_first + x) + (x == 0 ? 1 : 0)) * S::kRecord + wave * S::kWaveRecord, 4 * S::kWaveRecord);
+            };
+            write = join_pieces(counters, w_first, w, w_end, &s_flag, [&](unsigned x) {
+                if (nrows == 0) return;
+                const __amdgpu_buffer_rsrc_t p = slot(x);
 #pragma unroll
-                for (int i = 0; i < kTiles; i++)
+                for (int i = 0; i < S::kRegs / 4; i++)
+                    put_shared4(p, i * 1024 + lane * 16, o[i >> 2][4 * (i & 3)], o[i >> 2][4 * (i & 3) + 1], o[i >> 2][4 * (i & 3) + 2], o[i >> 2][4 * (i & 3) + 3]);
+                put_shared4(p, S::kRegs * 256 + lane * 16, m, E, L, 0.0f);
+            }, [&](unsigned x) {
+                if (nrows == 0) return;
+                const __amdgpu_buffer_rsrc_t p = slot(x);
+                const floatx4 st = get_shared4(p, S::kRegs * 256 + lane * 16);
+                constexpr int kAtOnce = S::kRegs / 4 < 16 ? S::kRegs / 4 : 16;  // 16-byte loads in flight
+                float qa = 0.0f, qb = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < 16; j++) put_shared(p + (16 * i + j) * 64, o[i][j]);
-                put_shared(p + S::kRegs * 64, m);
-                put_shared(p + S::kRegs * 64 + 64, E);
-                put_shared(p + S::kRegs * 64 + 128, L);
-            }
-            // every store of the piece has left before its arrival is counted
-            __builtin_amdgcn_s_waitcnt(0);
-            __syncthreads();
-            if (tid == 0) s_last = atomicInc(counters + w_first, parts - 1) == parts - 1;
-            __syncthreads();
-            write = s_last;
-            if (write && nrows) {
-                m = kLow;
-                E = 0.0f;
-                L = 0.0f;
+                for (int i0 = 0; i0 < S::kRegs / 4; i0 += kAtOnce) {
+                    floatx4 v[kAtOnce];
 #pragma unroll
-                for (int i = 0; i < kTiles; i++) o[i] = floatx16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 1
-                for (int64_t x = w_first; x <= w_end; x++) {
-                    const float *p = piece_at(x);
-                    const float pmx = get_shared(p + S::kRegs * 64), pe = get_shared(p + S::kRegs * 64 + 64), pl = get_shared(p + S::kRegs * 64 + 128);
-                    const float mn = fmaxf(m, pmx), da = m - mn, db = pmx - mn;
-                    const float en = fmaxf(E + da, pe + db);
-                    const float qa = pow2_down(da + (E - en)), qb = pow2_down(db + (pe - en));
-                    L = L * pow2_down(da) + pl * pow2_down(db);
+                    for (int i = 0; i < kAtOnce; i++) v[i] = get_shared4(p, (i0 + i) * 1024 + lane * 16);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (i0 == 0) {
+                        const State t = join(State{m, E, L}, State{st[0], st[1], st[2]}, qa, qb);
+                        m = t.m;
+                        E = t.E;
+                        L = t.L;
+                    }
 #pragma unroll
-                    for (int i = 0; i < kTiles; i++)
-#pragma unroll
-                        for (int j = 0; j < 16; j++) o[i][j] = o[i][j] * qa + get_shared(p + (16 * i + j) * 64) * qb;
-                    m = mn;
-                    E = en;
+                    for (int i = 0; i < 4 * kAtOnce; i++) {
+                        const int r = 4 * i0 + i;
+                        o[r >> 4][r & 15] = o[r >> 4][r & 15] * qa + v[i >> 2][i & 3] * qb;
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-            }
-            __syncthreads();  // s_last is read before the next unit's count
+            });
         }
         if (write && n < nrows) {
             const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+            int64_t token;
+            int head;
+            row_of(token, head);
             const int64_t off = ((q.first + token) * a.hq + head) * D;
             const int ex = (int)E + kCodeExp - kProbExp;
             // value 4 x + y is in row x + y (D / 4) of O^T; this lane has the rows 32 i + 8 j + 4 hh + c
@@ -504,7 +550,7 @@ hipError_t launch_d(const AttnArgs &a, int bf16, int num_cu, hipStream_t stream)
 
 int64_t attn_prompt_bytes(int head_dim, int num_cu) {
     const int64_t regs = head_dim / 2;
-    return 4 * 2 * (int64_t)num_cu * 8 * 64 * (regs + 3);
+    return 4 * 2 * (int64_t)num_cu * 8 * 64 * (regs + 4);
 }
 
 hipError_t launch_attn_prompt(const AttnArgs &a, int bf16, int num_cu, hipStream_t stream) {

@@ -19,8 +19,8 @@
 //
 // Split: the 32-position tiles of all units form one line that is cut evenly over the
 // workgroups whatever the lengths are; a workgroup's waves take its tiles in turn and join in
-// LDS.  A unit that is cut leaves its pieces in the workspace, and the piece that arrives last
-// (an atomic count) joins them in order of position, so the result does not depend on who that is.
+// LDS.  The pieces of a unit that is cut are joined through the workspace two and two in a tree
+// (join_pieces), so the result does not depend on the order of arrival.
 #include "attn_tiles.h"
 
 namespace w4a8 {
@@ -63,7 +63,7 @@ constexpr int kSumRows = 8;  // rows that join at a time
 template <int D, int NB>
 struct Layout {
     static constexpr int RB = 16 * NB;
-    static constexpr int kRecord = RB * (D + 3);        // floats of a piece: O, then m, E, L
+    static constexpr int kRecord = RB / 8 * 2 * kThreads * 4;  // floats of a piece: each thread's values and their state
     static constexpr int kRow = D + 4;                  // LDS row, padded
     static constexpr int kLds = kWaves * kSumRows * kRow;  // floats
 };
@@ -79,7 +79,7 @@ __global__ __launch_bounds__(kThreads, D == 256 || NB == 2 ? 2 : 4) void k_attn_
     constexpr int kT = D / 16;             // tiles of O^T
     __shared__ float s_o[Lay::kLds];
     __shared__ float s_m[kWaves][RB], s_e[kWaves][RB], s_l[kWaves][RB];
-    __shared__ int s_last;
+    __shared__ int s_flag;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
     uint32_t *counters = static_cast<uint32_t *>(a.ws);
     float *pieces = reinterpret_cast<float *>(static_cast<char *>(a.ws) + kAttnCounterBytes);
@@ -402,36 +402,16 @@ __global__ __launch_bounds__(kThreads, D == 256 || NB == 2 ? 2 : 4) void k_attn_
 #pragma unroll
             for (int i = 0; i < kT; i++) o[nb][i] *= q;
         }
-        // what becomes of row r, value d
-        const bool cut = take < wk.tiles;
-        const int64_t w_first = div64((unit0 + 1) * used - 1, line), w_end = div64((unit0 + wk.tiles) * used - 1, line);
-        float *piece = pieces + (2 * w + (w == w_first ? 1 : 0)) * Lay::kRecord;
-        auto write_row = [&](int r, int d, const float v[4]) {  // four final values
-            int64_t token;
-            int head;
-            row_at(r, token, head);
-            const int64_t off = ((wk.q.first + token) * a.hq + head) * D + d;
-            if constexpr (BF16) {
-                uint2 u;
-                u.x = (uint32_t)f32_to_bf16_rne(v[0]) | (uint32_t)f32_to_bf16_rne(v[1]) << 16;
-                u.y = (uint32_t)f32_to_bf16_rne(v[2]) | (uint32_t)f32_to_bf16_rne(v[3]) << 16;
-                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.o) + off) = u;
-            } else {
-                *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + off) = make_float4(v[0], v[1], v[2], v[3]);
-            }
-        };
-        if (cut && wave == 0 && g == 0) {
+        // sum over the waves, kSumRows rows at a time; a thread ends with four values of a row of each
+        constexpr int kItems = RB / kSumRows;
+        constexpr bool kAll = kSumRows * (D / 4) == kThreads;
+        const int ir = tid / (D / 4), id = 4 * (tid % (D / 4));
+        float v[kItems][4];
+        State st[kItems];
 #pragma unroll
-            for (int nb = 0; nb < NB; nb++) {
-                const int r = 16 * nb + n;
-                float l = 0.0f;
-                for (int x = 0; x < kWaves; x++) l += s_l[x][r] * pow2_down(s_m[x][r] - mj[nb]);
-                put_shared(piece + RB * D + r, mj[nb]);
-                put_shared(piece + RB * D + RB + r, ej[nb]);
-                put_shared(piece + RB * D + 2 * RB + r, l);
-            }
-        }
-        for (int q0 = 0; q0 < nrows; q0 += kSumRows) {
+        for (int x = 0; x < kItems; x++) {
+            const int q0 = x * kSumRows;
+            if (q0 >= nrows) break;
 #pragma unroll
             for (int nb = 0; nb < NB; nb++) {
                 const int r = 16 * nb + n - q0;
@@ -446,69 +426,77 @@ __global__ __launch_bounds__(kThreads, D == 256 || NB == 2 ? 2 : 4) void k_attn_
                 }
             }
             __syncthreads();
-            for (int x = tid; x < kSumRows * (D / 4); x += kThreads) {
-                const int r = x / (D / 4), d = 4 * (x % (D / 4));
-                if (q0 + r < nrows) {
-                    float v[4] = {0, 0, 0, 0};
+            v[x][0] = v[x][1] = v[x][2] = v[x][3] = 0.0f;
+            st[x] = State{kLow, 0.0f, 0.0f};
+            if (kAll || ir < kSumRows) {
 #pragma unroll
-                    for (int y = 0; y < kWaves; y++) {
-                        const float4 f = *reinterpret_cast<const float4 *>(s_o + (y * kSumRows + r) * Lay::kRow + d);
-                        v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
-                    }
-                    if (cut) {
-#pragma unroll
-                        for (int i = 0; i < 4; i++) put_shared(piece + (q0 + r) * D + d + i, v[i]);
-                    } else {
-                        float mm = s_m[0][q0 + r], ee = kLow, l = 0.0f;
-                        for (int y = 1; y < kWaves; y++) mm = fmaxf(mm, s_m[y][q0 + r]);
-                        for (int y = 0; y < kWaves; y++) {
-                            ee = fmaxf(ee, s_e[y][q0 + r] + (s_m[y][q0 + r] - mm));
-                            l += s_l[y][q0 + r] * pow2_down(s_m[y][q0 + r] - mm);
-                        }
-                        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll
-                        for (int i = 0; i < 4; i++) v[i] = ldexpf(v[i] * inv, (int)ee + kCodeExp - kProbExp);
-                        write_row(q0 + r, d, v);
-                    }
+                for (int y = 0; y < kWaves; y++) {
+                    const float4 f = *reinterpret_cast<const float4 *>(s_o + (y * kSumRows + ir) * Lay::kRow + id);
+                    v[x][0] += f.x; v[x][1] += f.y; v[x][2] += f.z; v[x][3] += f.w;
+                }
+                const int r = q0 + ir;
+                for (int y = 0; y < kWaves; y++) st[x].m = fmaxf(st[x].m, s_m[y][r]);
+                st[x].E = kLow;
+                for (int y = 0; y < kWaves; y++) {
+                    st[x].E = fmaxf(st[x].E, s_e[y][r] + (s_m[y][r] - st[x].m));
+                    st[x].L += s_l[y][r] * pow2_down(s_m[y][r] - st[x].m);
                 }
             }
             __syncthreads();
         }
-        if (cut) {
-            // every store of the piece has left before its arrival is counted
-            __builtin_amdgcn_s_waitcnt(0);
-            __syncthreads();
-            const unsigned parts = (unsigned)(w_end - w_first + 1);
-            if (tid == 0) s_last = atomicInc(counters + w_first, parts - 1) == parts - 1;
-            __syncthreads();
-            if (s_last) {
-                // piece x of the unit: the first one's starts in its workgroup's part, the others lead theirs
-                auto piece_at = [&](unsigned x) { return pieces + (2 * (w_first + x) + (x == 0 ? 1 : 0)) * Lay::kRecord; };
-                for (int x = tid; x < nrows * (D / 4); x += kThreads) {
-                    const int r = x / (D / 4), d = 4 * (x % (D / 4));
-                    float mm = kLow, ee = 0.0f, l = 0.0f, v[4] = {0, 0, 0, 0};
-                    for (unsigned y = 0; y < parts; y++) {
-                        const float *p = piece_at(y);
-                        const float pm2 = get_shared(p + RB * D + r), pe = get_shared(p + RB * D + RB + r), pl = get_shared(p + RB * D + 2 * RB + r);
-                        float pv[4];
+        bool write = true;
+        if (take < wk.tiles) {
+            const int64_t w_first = div64((unit0 + 1) * used - 1, line), w_end = div64((unit0 + wk.tiles) * used - 1, line);
+            auto slot = [&](unsigned x) { return shared_piece(pieces + (2 * (w_first + x) + (x == 0 ? 1 : 0)) * Lay::kRecord, 4 * Lay::kRecord); };
+            write = join_pieces(counters, w_first, w, w_end, &s_flag, [&](unsigned y) {
+                const __amdgpu_buffer_rsrc_t p = slot(y);
 #pragma unroll
-                        for (int i = 0; i < 4; i++) pv[i] = get_shared(p + r * D + d + i);
-                        const float mn = fmaxf(mm, pm2), da = mm - mn, db = pm2 - mn;
-                        const float en = fmaxf(ee + da, pe + db);
-                        l = l * pow2_down(da) + pl * pow2_down(db);
-                        const float qa = pow2_down(da + (ee - en)), qb = pow2_down(db + (pe - en));
-#pragma unroll
-                        for (int i = 0; i < 4; i++) v[i] = v[i] * qa + pv[i] * qb;
-                        mm = mn;
-                        ee = en;
+                for (int x = 0; x < kItems; x++)
+                    if (x * kSumRows < nrows) {
+                        put_shared4(p, (x * 2 + 0) * kThreads * 16 + tid * 16, v[x][0], v[x][1], v[x][2], v[x][3]);
+                        put_shared4(p, (x * 2 + 1) * kThreads * 16 + tid * 16, st[x].m, st[x].E, st[x].L, 0.0f);
                     }
-                    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            }, [&](unsigned y) {
+                const __amdgpu_buffer_rsrc_t p = slot(y);
+                floatx4 f[kItems][2];
 #pragma unroll
-                    for (int i = 0; i < 4; i++) v[i] = ldexpf(v[i] * inv, (int)ee + kCodeExp - kProbExp);
-                    write_row(r, d, v);
+                for (int x = 0; x < kItems; x++)
+                    if (x * kSumRows < nrows) {
+                        f[x][0] = get_shared4(p, (x * 2 + 0) * kThreads * 16 + tid * 16);
+                        f[x][1] = get_shared4(p, (x * 2 + 1) * kThreads * 16 + tid * 16);
+                    }
+#pragma unroll
+                for (int x = 0; x < kItems; x++)
+                    if (x * kSumRows < nrows) {
+                        float qa, qb;
+                        st[x] = join(st[x], State{f[x][1][0], f[x][1][1], f[x][1][2]}, qa, qb);
+#pragma unroll
+                        for (int i = 0; i < 4; i++) v[x][i] = v[x][i] * qa + f[x][0][i] * qb;
+                    }
+            });
+        }
+        if (write) {
+#pragma unroll
+            for (int x = 0; x < kItems; x++) {
+                const int r = x * kSumRows + ir;
+                if ((kAll || ir < kSumRows) && r < nrows) {
+                    const float inv = st[x].L > 0.0f ? 1.0f / st[x].L : 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 4; i++) v[x][i] = ldexpf(v[x][i] * inv, (int)st[x].E + kCodeExp - kProbExp);
+                    int64_t token;
+                    int head;
+                    row_at(r, token, head);
+                    const int64_t off = ((wk.q.first + token) * a.hq + head) * D + id;
+                    if constexpr (BF16) {
+                        uint2 u;
+                        u.x = (uint32_t)f32_to_bf16_rne(v[x][0]) | (uint32_t)f32_to_bf16_rne(v[x][1]) << 16;
+                        u.y = (uint32_t)f32_to_bf16_rne(v[x][2]) | (uint32_t)f32_to_bf16_rne(v[x][3]) << 16;
+                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.o) + off) = u;
+                    } else {
+                        *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + off) = make_float4(v[x][0], v[x][1], v[x][2], v[x][3]);
+                    }
                 }
             }
-            __syncthreads();
         }
         at += take;
     }
