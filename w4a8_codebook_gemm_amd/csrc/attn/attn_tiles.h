@@ -69,6 +69,18 @@ __device__ __forceinline__ float pow2_down(float x) { return __builtin_amdgcn_ex
 constexpr int kZeroExp = -300;       // exponent of a value scale of zero
 constexpr float kLow = -3.0e38f;  // "no score yet"
 
+// The larger of x and that of lane ^ 32 or lane ^ 16: with both operands x, the swap of half waves
+// (of the odd 16-lane rows with the even ones) leaves the two in its two results.
+typedef uint32_t uintx2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ float max_xor32(float x) {
+    const uintx2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float max_xor16(float x) {
+    const uintx2 r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
 // x, as a value the compiler works from anew: what hangs on it is not kept in registers across a loop.
 __device__ __forceinline__ int fresh(int x) {
     asm volatile("" : "+v"(x));
@@ -132,30 +144,33 @@ __device__ __forceinline__ State join(const State &a, const State &b, float &qa,
     return s;
 }
 
-// The pieces of a cut unit are joined two and two in a tree: a workgroup leaves what it holds in the
-// slot of its first piece and counts its arrival at the boundary it shares with its sibling; the
-// second to arrive takes the sibling's, joins, and goes on a level up.  The sums do not depend on
-// the order of arrival.  `counters` has one word for each workgroup: a piece is the first of a right
-// subtree at one boundary of one unit.  put(p) leaves this workgroup's part in piece p's slot, take(p)
-// joins piece p's slot to it.  True for the workgroup that ends with the whole unit.
-template <class Put, class Take>
+// The pieces of a cut unit are joined in a tree, kRadix at a node: a workgroup leaves what it holds
+// in the slot of its first piece and counts its arrival at the node; the last to arrive joins the
+// node's slots in order of position and goes on a level up.  The sums do not depend on the order
+// of arrival.  A node counts at the workgroup of its second child's first piece, which is no other
+// node's, and its count ends at zero.  put(p) leaves this workgroup's part in piece p's slot;
+// take(p, step, n) takes up the n slots p, p + step, ...  True for the workgroup that ends with the
+// whole unit.
+template <int kRadix, class Put, class Take>
 __device__ __forceinline__ bool join_pieces(uint32_t *counters, int64_t w_first, int64_t w, int64_t w_end, int *s_flag, Put put, Take take) {
     const unsigned parts = (unsigned)(w_end - w_first + 1);
     unsigned lo = (unsigned)(w - w_first);
-    for (unsigned size = 1; size < parts; size *= 2) {
-        const unsigned other = lo & size ? lo - size : lo + size;
-        if (other >= parts) continue;
+    for (unsigned size = 1; size < parts; size *= kRadix) {
+        const unsigned node = lo / (size * kRadix) * (size * kRadix);
+        unsigned n = (parts - node + size - 1) / size;  // children
+        if (n > kRadix) n = kRadix;
+        if (n == 1) continue;
         put(lo);
         // every store has left before the arrival is counted
         __builtin_amdgcn_s_waitcnt(0);
         __syncthreads();
-        if (threadIdx.x == 0) *s_flag = atomicInc(counters + w_first + (lo > other ? lo : other), 1u) == 1u;
+        if (threadIdx.x == 0) *s_flag = atomicInc(counters + w_first + node + size, n - 1) == n - 1;
         __syncthreads();
-        const bool second = *s_flag;
+        const bool last = *s_flag;
         __syncthreads();
-        if (!second) return false;
-        take(other);
-        if (other < lo) lo = other;
+        if (!last) return false;
+        take(node, size, n);
+        lo = node;
     }
     return true;
 }

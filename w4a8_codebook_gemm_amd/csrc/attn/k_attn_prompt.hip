@@ -392,7 +392,7 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
                     float x = fmaxf(fmaxf(s[8 * u], s[8 * u + 1]), s[8 * u + 2]);
                     x = fmaxf(fmaxf(x, s[8 * u + 3]), s[8 * u + 4]);
                     x = fmaxf(fmaxf(x, s[8 * u + 5]), fmaxf(s[8 * u + 6], s[8 * u + 7]));
-                    x = fmaxf(x, __shfl_xor(x, 32));
+                    x = max_xor32(x);
                     // a masked score is -inf whatever the page's scale holds
                     f[u] = fmaxf(fac * sc[u].x, 0x1p-126f);
                     top[u] = ceilf(x * f[u]);
@@ -469,16 +469,19 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
             auto slot = [&](unsigned x) {
                 return shared_piece(pieces + (2 * (w_first + x) + (x == 0 ? 1 : 0)) * S::kRecord + wave * S::kWaveRecord, 4 * S::kWaveRecord);
             };
-            write = join_pieces(counters, w_first, w, w_end, &s_flag, [&](unsigned x) {
+            unsigned held = (unsigned)(w - w_first);
+            write = join_pieces<2>(counters, w_first, w, w_end, &s_flag, [&](unsigned x) {
                 if (nrows == 0) return;
                 const __amdgpu_buffer_rsrc_t p = slot(x);
 #pragma unroll
                 for (int i = 0; i < S::kRegs / 4; i++)
                     put_shared4(p, i * 1024 + lane * 16, o[i >> 2][4 * (i & 3)], o[i >> 2][4 * (i & 3) + 1], o[i >> 2][4 * (i & 3) + 2], o[i >> 2][4 * (i & 3) + 3]);
                 put_shared4(p, S::kRegs * 256 + lane * 16, m, E, L, 0.0f);
-            }, [&](unsigned x) {
+            }, [&](unsigned x, unsigned step, unsigned) {
+                // of the node's two slots this workgroup holds one; a sum of two does not ask for their order
                 if (nrows == 0) return;
-                const __amdgpu_buffer_rsrc_t p = slot(x);
+                const __amdgpu_buffer_rsrc_t p = slot(held == x ? x + step : x);
+                held = x;
                 const floatx4 st = get_shared4(p, S::kRegs * 256 + lane * 16);
                 constexpr int kAtOnce = S::kRegs / 4 < 16 ? S::kRegs / 4 : 16;  // 16-byte loads in flight
                 float qa = 0.0f, qb = 0.0f;

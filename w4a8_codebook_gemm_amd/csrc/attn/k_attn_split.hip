@@ -10,17 +10,17 @@
 // scores are those of eight consecutive positions of its row, which is the fragment the
 // second product wants: probabilities never leave their lane.  Codes become fp16 in
 // registers: K rows by bytes in order, V by a permute that transposes 2 tokens x 1 value, one
-// permute and one packed addition for two codes.  No LDS until waves join.
+// permute and one packed addition for two codes.  A wave takes 8192 / D positions at a time, the
+// next ones' codes (16 KiB) on their way while it works; queries lie in LDS, shared by the waves.
 //
 // The running maximum m and the exponent E are whole numbers: with e the exponent of a page's
 // value scale sv < 2^e, a probability enters the second product as p sv 2^(14 - E), E the
 // largest (m_page - m) + e so far, so it is below 2^14 whatever the pages' scales, and every
 // rescaling is by a power of two, exact.  o = O 2^(24 - 14 + E) / sum p.
 //
-// Split: the 32-position tiles of all units form one line that is cut evenly over the
-// workgroups whatever the lengths are; a workgroup's waves take its tiles in turn and join in
-// LDS.  The pieces of a unit that is cut are joined through the workspace two and two in a tree
-// (join_pieces), so the result does not depend on the order of arrival.
+// Split: the tiles of all units form one line that is cut evenly over the workgroups whatever the
+// lengths are; a workgroup's waves take its tiles in turn and join in LDS.  The pieces of a unit
+// that is cut are joined through the workspace (join_pieces).
 #include "attn_tiles.h"
 
 namespace w4a8 {
@@ -35,6 +35,8 @@ template <> struct VLoad<256> { typedef uint4 type; };
 template <> struct VLoad<128> { typedef uint2 type; };
 template <> struct VLoad<64> { typedef uint32_t type; };
 
+constexpr int kRadix = 16;       // pieces that join at a time
+
 // How a sequence contributes to the line of tiles.
 struct Work {
     Seq q;
@@ -42,15 +44,15 @@ struct Work {
     int64_t total;   // tiles of all its units
 };
 
-template <int RB>
+template <int RB, int T>
 __device__ __forceinline__ Work seq_work(const AttnArgs &a, int64_t b) {
     Work w;
     w.q = load_seq(a.s, a.M, a.page_shift, b);
     w.lo = w.tiles = 0;
     w.total = 0;
     if (w.q.n > 0) {
-        if (a.window && (int64_t)w.q.pos0 - a.window + 1 > 0) w.lo = (int)(w.q.pos0 - a.window + 1) >> 5;
-        w.tiles = ((w.q.len + 31) >> 5) - w.lo;
+        if (a.window && (int64_t)w.q.pos0 - a.window + 1 > 0) w.lo = (int)(w.q.pos0 - a.window + 1) / T;
+        w.tiles = (w.q.len + T - 1) / T - w.lo;
         if (w.tiles < 1) w.tiles = 1;  // rows that see nothing are still written
         const int64_t blocks = ((int64_t)w.q.n * a.group + RB - 1) / RB;
         w.total = blocks * a.c.kv_heads * w.tiles;
@@ -69,15 +71,16 @@ struct Layout {
 };
 
 template <int D, int NB, bool BF16>
-__global__ __launch_bounds__(kThreads, D == 256 || NB == 2 ? 2 : 4) void k_attn_split(AttnArgs a, int wgs) {
+__global__ __launch_bounds__(kThreads, 2) void k_attn_split(AttnArgs a, int wgs) {
     using Lay = Layout<D, NB>;
     using VT = typename VLoad<D>::type;
     constexpr int RB = Lay::RB;
+    constexpr int U = 256 / D, T = 32 * U;  // 32-position parts of a tile
     constexpr int kParts = BF16 ? 1 : 2;   // fp16 numbers that make a query value or a probability
-    constexpr int kC = D / 64;             // 16-byte chunks of a key row in a lane
-    constexpr int kVD = D / 64 > 0 ? D / 64 : 1;  // dwords of a value row in a lane
+    constexpr int kC = D / 64;             // 16-byte chunks of a key row, dwords of a value row in a lane
     constexpr int kT = D / 16;             // tiles of O^T
-    __shared__ float s_o[Lay::kLds];
+    __shared__ __attribute__((aligned(16))) float s_o[Lay::kLds];
+    __shared__ half8_t s_q[NB * kParts * 2 * kC * 64];
     __shared__ float s_m[kWaves][RB], s_e[kWaves][RB], s_l[kWaves][RB];
     __shared__ int s_flag;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
@@ -87,7 +90,7 @@ __global__ __launch_bounds__(kThreads, D == 256 || NB == 2 ? 2 : 4) void k_attn_
     // the line's length, and this workgroup's part of it
     int64_t line = 0;
     for (int64_t b0 = 0; b0 < a.s.B; b0 += 64)
-        line += __shfl((long long)scan64(b0 + lane < a.s.B ? seq_work<RB>(a, b0 + lane).total : 0, lane), 63);
+        line += __shfl((long long)scan64(b0 + lane < a.s.B ? seq_work<RB, T>(a, b0 + lane).total : 0, lane), 63);
     line = uniform64(line);
     if (line == 0) return;
     int64_t used = (line + kWaves - 1) / kWaves;  // at least a tile for each wave
@@ -102,7 +105,7 @@ __global__ __launch_bounds__(kThreads, D == 256 || NB == 2 ? 2 : 4) void k_attn_
         Work wk{};
         for (int64_t b0 = 0; b0 < a.s.B; b0 += 64) {
             Work x{};
-            if (b0 + lane < a.s.B) x = seq_work<RB>(a, b0 + lane);
+            if (b0 + lane < a.s.B) x = seq_work<RB, T>(a, b0 + lane);
             const int64_t incl = scan64(x.total, lane);
             const int64_t sum = uniform64(__shfl((long long)incl, 63));
             if (at < base + sum) {
@@ -133,12 +136,87 @@ __global__ __launch_bounds__(kThreads, D == 256 || NB == 2 ? 2 : 4) void k_attn_
         const int nrows = (int)(rows - r0 < RB ? rows - r0 : RB);
         int lo[NB], hi[NB];
         float fac[NB];
-        half8_t qf[NB][kParts][2 * kC];
         auto row_at = [&](int r, int64_t &token, int &head) {  // row r < nrows of the block
             const int64_t i = div64(r0 + r, a.group);
             token = i;
             head = h * a.group + (int)(r0 + r - i * a.group);
         };
+        // positions that all rows of the block see, and that any does
+        int all_lo, all_hi, any_lo, any_hi;
+        {
+            int64_t t_first, t_last;
+            int hd;
+            row_at(0, t_first, hd);
+            row_at(nrows - 1, t_last, hd);
+            sees(a, wk.q, t_first, any_lo, all_hi);
+            sees(a, wk.q, t_last, all_lo, any_hi);
+        }
+
+        const int end = wk.lo + tile0 + take;
+        int first = wk.lo + tile0 + wave;
+        if (first < any_lo / T) first += (any_lo / T - first + kWaves - 1) / kWaves * kWaves;
+        const int stop = end < (any_hi + T - 1) / T ? end : (any_hi + T - 1) / T;
+        const int P = a.c.page_size, pm = P - 1;
+        const bool small = a.page_shift == 4;  // two pages in 32 positions
+        const int32_t *table = a.s.page_table + b * a.s.table_width;
+
+        auto page_of = [&](int t) {  // page of position t, -1 past the end
+            return t < wk.q.len ? table[t >> a.page_shift] : -1;
+        };
+        auto block_of = [&](int page) {  // its block of this head; a page that is not there reads page 0, masked
+            return (int64_t)((uint32_t)page < (uint32_t)a.c.num_pages ? page : 0) * a.c.kv_heads + h;
+        };
+        uint4 kr[U][2][kC];
+        VT vr[U][8];
+        float ks[U], vs[U];
+        int pk[U], ps[U];       // pages of the tile to load next, of this lane's key row and of its positions
+        auto find_pages = [&](int tile) {
+            const int l = fresh(lane);
+#pragma unroll
+            for (int x = 0; x < U; x++) {
+                const int t = tile * T + 32 * x;
+                pk[x] = page_of(t + (small ? 2 * (l & 8) : 0));
+                ps[x] = page_of(t + (small ? (l & 32) >> 1 : 0));
+            }
+        };
+        auto load_k = [&](int tile) {
+            const int l = fresh(lane);
+#pragma unroll
+            for (int x = 0; x < U; x++) {
+                const int8_t *p = a.c.k + (block_of(pk[x]) * P + ((tile * T + 32 * x + 2 * (l & 12) + (l & 3)) & pm)) * D + (l >> 4) * 16;
+#pragma unroll
+                for (int u = 0; u < 2; u++)
+#pragma unroll
+                    for (int c = 0; c < kC; c++) kr[x][u][c] = *reinterpret_cast<const uint4 *>(p + 4 * u * D + 64 * c);
+            }
+        };
+        auto load_v = [&](int tile) {
+            const int l = fresh(lane);
+#pragma unroll
+            for (int x = 0; x < U; x++) {
+                const int8_t *p = a.c.v + (block_of(ps[x]) * P + ((tile * T + 32 * x + (l >> 4) * 8) & pm)) * D + (l & 15) * (D / 16);
+#pragma unroll
+                for (int j = 0; j < 8; j++) vr[x][j] = *reinterpret_cast<const VT *>(p + j * D);
+            }
+        };
+        // value scale -1 where the page is not there
+        auto load_scales = [&]() {
+#pragma unroll
+            for (int x = 0; x < U; x++) {
+                const int64_t blk = block_of(ps[x]);
+                ks[x] = a.c.k_scale[blk];
+                vs[x] = (uint32_t)ps[x] < (uint32_t)a.c.num_pages ? a.c.v_scale[blk] : -1.0f;
+            }
+        };
+        if (first < stop) {
+            find_pages(first);
+            load_scales();
+            load_k(first);
+            load_v(first);
+            if (first + kWaves < stop) find_pages(first + kWaves);
+        }
+
+        // queries as fp16, into LDS: fragment (block, part, step) as its lanes read it
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
             const int r = 16 * nb + n;
@@ -165,35 +243,30 @@ __global__ __launch_bounds__(kThreads, D == 256 || NB == 2 ? 2 : 4) void k_attn_
 #pragma unroll
                     for (int i = 0; i < 8; i++) top = fmaxf(top, fabsf(v[c][u][i]));
                 }
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
+            top = max_xor32(max_xor16(top));
             // the row's largest value at 2^13 .. 2^14: bf16 values are then exact in fp16 down
             // to 2^-28 of it (fp32 as two fp16 numbers to 2^-22 relative), below off by 2^-39
             int ex = 0;
             if (top > 0.0f) frexpf(top, &ex);
             fac[nb] = ldexpf(fabsf(a.scale) * kLog2e, ex - 14);
+            if (wave == nb) {
 #pragma unroll
-            for (int c = 0; c < kC; c++)
+                for (int c = 0; c < kC; c++)
 #pragma unroll
-                for (int u = 0; u < 2; u++)
+                    for (int u = 0; u < 2; u++) {
+                        half8_t q0, q1;
 #pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        const float x = ldexpf(a.scale < 0.0f ? -v[c][u][i] : v[c][u][i], 14 - ex);
-                        const _Float16 x0 = (_Float16)x;
-                        qf[nb][0][2 * c + u][i] = x0;
-                        if constexpr (kParts == 2) qf[nb][1][2 * c + u][i] = (_Float16)(x - (float)x0);
+                        for (int i = 0; i < 8; i++) {
+                            const float x = ldexpf(a.scale < 0.0f ? -v[c][u][i] : v[c][u][i], 14 - ex);
+                            q0[i] = (_Float16)x;
+                            q1[i] = (_Float16)(x - (float)(_Float16)x);
+                        }
+                        s_q[(nb * kParts * 2 * kC + 2 * c + u) * 64 + lane] = q0;
+                        if constexpr (kParts == 2) s_q[((nb * kParts + 1) * 2 * kC + 2 * c + u) * 64 + lane] = q1;
                     }
+            }
         }
-        // positions that all rows of the block see, and that any does
-        int all_lo, all_hi, any_lo, any_hi;
-        {
-            int64_t t_first, t_last;
-            int hd;
-            row_at(0, t_first, hd);
-            row_at(nrows - 1, t_last, hd);
-            sees(a, wk.q, t_first, any_lo, all_hi);
-            sees(a, wk.q, t_last, all_lo, any_hi);
-        }
+        __syncthreads();
 
         floatx4 o[NB][kT];
         float m[NB], E[NB], L[NB];
@@ -205,131 +278,103 @@ __global__ __launch_bounds__(kThreads, D == 256 || NB == 2 ? 2 : 4) void k_attn_
 #pragma unroll
             for (int i = 0; i < kT; i++) o[nb][i] = floatx4{0, 0, 0, 0};
         }
-
-        const int end = wk.lo + tile0 + take;
-        int first = wk.lo + tile0 + wave;
-        if (first < any_lo >> 5) first += ((any_lo >> 5) - first + kWaves - 1) / kWaves * kWaves;
-        const int stop = end < (any_hi + 31) >> 5 ? end : (any_hi + 31) >> 5;
-        const int P = a.c.page_size, pm = P - 1;
-        const bool small = a.page_shift == 4;  // two pages in a tile
-        const int32_t *table = a.s.page_table + b * a.s.table_width;
-        const int tokk = small ? 16 * (n >> 3) : 0, toks = small ? 16 * (g >> 1) : 0;
-
-        auto page_of = [&](int t) {  // page of position t, -1 past the end
-            return t < wk.q.len ? table[t >> a.page_shift] : -1;
-        };
-        auto block_of = [&](int page) {  // its block of this head; a page that is not there reads page 0, masked
-            return (int64_t)((uint32_t)page < (uint32_t)a.c.num_pages ? page : 0) * a.c.kv_heads + h;
-        };
-        uint4 kr[2][kC];
-        VT vr[8];
-        float ks = 0.0f, vs = 0.0f;
-        int pk = -1, ps = -1;       // pages of the tile to load next
-        auto load_k = [&](int tile) {
-            const int8_t *p = a.c.k + (block_of(pk) * P + ((32 * tile + 8 * (n >> 2) + (n & 3)) & pm)) * D + 16 * g;
-#pragma unroll
-            for (int u = 0; u < 2; u++)
-#pragma unroll
-                for (int c = 0; c < kC; c++) kr[u][c] = *reinterpret_cast<const uint4 *>(p + 4 * u * D + 64 * c);
-        };
-        auto load_v = [&](int tile) {
-            const int8_t *p = a.c.v + (block_of(ps) * P + ((32 * tile + 8 * g) & pm)) * D + n * (D / 16);
-#pragma unroll
-            for (int j = 0; j < 8; j++) vr[j] = *reinterpret_cast<const VT *>(p + j * D);
-        };
-        auto load_scales = [&]() {
-            const int64_t blk = block_of(ps);
-            ks = a.c.k_scale[blk];
-            vs = a.c.v_scale[blk];
-        };
-        int page_s = -1;            // page of this lane's positions in the current tile
-        if (first < stop) {
-            pk = page_of(32 * first + tokk);
-            ps = page_of(32 * first + toks);
-            load_scales();
-            load_k(first);
-            load_v(first);
-            page_s = ps;
-            if (first + kWaves < stop) {
-                pk = page_of(32 * (first + kWaves) + tokk);
-                ps = page_of(32 * (first + kWaves) + toks);
-            }
-        }
         for (int tile = first; tile < stop; tile += kWaves) {
             const bool more = tile + kWaves < stop;
-            floatx4 s[NB][2];
+            floatx4 s[NB][U][2];
 #pragma unroll
-            for (int nb = 0; nb < NB; nb++) s[nb][0] = s[nb][1] = floatx4{0, 0, 0, 0};
+            for (int nb = 0; nb < NB; nb++)
 #pragma unroll
-            for (int u = 0; u < 2; u++)
+                for (int x = 0; x < U; x++) s[nb][x][0] = s[nb][x][1] = floatx4{0, 0, 0, 0};
+            const half8_t *qp = s_q + fresh(lane);
 #pragma unroll
-                for (int c = 0; c < kC; c++) {
-                    const half8_t k0 = codes_natural(kr[u][c].x, kr[u][c].y), k1 = codes_natural(kr[u][c].z, kr[u][c].w);
+            for (int c = 0; c < kC; c++) {
+                half8_t qf[NB][kParts][2];
 #pragma unroll
-                    for (int nb = 0; nb < NB; nb++)
+                for (int nb = 0; nb < NB; nb++)
 #pragma unroll
-                        for (int pt = 0; pt < kParts; pt++) {
-                            s[nb][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qf[nb][pt][2 * c], s[nb][u], 0, 0, 0);
-                            s[nb][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qf[nb][pt][2 * c + 1], s[nb][u], 0, 0, 0);
-                        }
-                }
-            const float tks = ks, tvs = vs;
-            const int tpage = page_s;
-            int npk = -1, nps = -1;
+                    for (int pt = 0; pt < kParts; pt++)
+#pragma unroll
+                        for (int i = 0; i < 2; i++) qf[nb][pt][i] = qp[((nb * kParts + pt) * 2 * kC + 2 * c + i) * 64];
+#pragma unroll
+                for (int x = 0; x < U; x++)
+#pragma unroll
+                    for (int u = 0; u < 2; u++) {
+                        const half8_t k0 = codes_natural(kr[x][u][c].x, kr[x][u][c].y), k1 = codes_natural(kr[x][u][c].z, kr[x][u][c].w);
+#pragma unroll
+                        for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                            for (int pt = 0; pt < kParts; pt++) {
+                                s[nb][x][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qf[nb][pt][0], s[nb][x][u], 0, 0, 0);
+                                s[nb][x][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qf[nb][pt][1], s[nb][x][u], 0, 0, 0);
+                            }
+                    }
+            }
+            float tks[U], tvs[U];
+#pragma unroll
+            for (int x = 0; x < U; x++) {
+                tks[x] = ks[x];
+                tvs[x] = vs[x];
+            }
             if (more) {
-                if (tile + 2 * kWaves < stop) {
-                    npk = page_of(32 * (tile + 2 * kWaves) + tokk);
-                    nps = page_of(32 * (tile + 2 * kWaves) + toks);
-                }
                 load_scales();
                 load_k(tile + kWaves);
             }
-            const bool there = (uint32_t)tpage < (uint32_t)a.c.num_pages;
-            const bool whole = 32 * tile >= all_lo && 32 * tile + 32 <= all_hi && __all(there);
-            half8_t pf[NB][kParts];
+            bool whole = tile * T >= all_lo && tile * T + T <= all_hi;
+#pragma unroll
+            for (int x = 0; x < U; x++) whole = whole && __all(tvs[x] >= 0.0f);
+            half8_t pf[NB][U][kParts];
 #pragma unroll
             for (int nb = 0; nb < NB; nb++) {
-                const float f = fac[nb] * tks;
-                float x[8], mx = -INFINITY;
-                float sv = tvs;
-                if (whole) {
+                float x[U][8], mx[U], all = -INFINITY;
+                int e[U];
 #pragma unroll
-                    for (int j = 0; j < 8; j++) {
-                        x[j] = s[nb][j >> 2][j & 3] * f;
-                        mx = fmaxf(mx, x[j]);
-                    }
-                } else {
-                    const int t = 32 * tile + 8 * g;
+                for (int y = 0; y < U; y++) {
+                    const float f = fac[nb] * tks[y];
+                    mx[y] = -INFINITY;
 #pragma unroll
-                    for (int j = 0; j < 8; j++) {
-                        const bool see = there && t + j >= lo[nb] && t + j < hi[nb];
-                        x[j] = see ? s[nb][j >> 2][j & 3] * f : -INFINITY;
-                        mx = fmaxf(mx, x[j]);
+                    for (int j = 0; j < 8; j++) x[y][j] = s[nb][y][j >> 2][j & 3] * f;
+                    if (!whole) {
+                        const int t = tile * T + 32 * y + 8 * g;
+#pragma unroll
+                        for (int j = 0; j < 8; j++) {
+                            const bool see = (tvs[y] >= 0.0f) & (t + j >= lo[nb]) & (t + j < hi[nb]);
+                            x[y][j] = see ? x[y][j] : -INFINITY;
+                        }
                     }
+#pragma unroll
+                    for (int j = 0; j < 8; j++) mx[y] = fmaxf(mx[y], x[y][j]);
+                    all = fmaxf(all, mx[y]);
                 }
-                float all = fmaxf(mx, __shfl_xor(mx, 16));
-                all = fmaxf(all, __shfl_xor(all, 32));
-                // nothing seen of this page: its scale, whatever it holds, stays out
-                if ((small ? mx : all) == -INFINITY) sv = 0.0f;
+                all = max_xor32(max_xor16(all));
                 const float mn = fmaxf(m[nb], ceilf(all));
                 const float down = m[nb] - mn;             // <= 0
-                int e = -300;
-                if (sv > 0.0f) frexpf(sv, &e);
-                float top = (small ? ceilf(mx) : ceilf(all)) - mn + (float)e;
-                if (small) {
-                    top = fmaxf(top, __shfl_xor(top, 16));
-                    top = fmaxf(top, __shfl_xor(top, 32));
+                // the pages this lane's positions are in; of a page that is not seen the scale, whatever it
+                // holds, stays out
+                float top = -INFINITY;
+#pragma unroll
+                for (int y = 0; y < U; y++) {
+                    e[y] = kZeroExp;
+                    if (mx[y] > -INFINITY && tvs[y] > 0.0f) frexpf(tvs[y], &e[y]);
+                    top = fmaxf(top, (ceilf(mx[y]) - mn) + (float)e[y]);
                 }
-                const float En = fmaxf(E[nb] + down, top);
+                top = max_xor32(max_xor16(top));
+                // E grows by more than it has to, so that it seldom does; not where the products are
+                // wanted to fp32's precision, 2^-25 of the largest then
+                const float En = top > E[nb] + down ? top + (BF16 ? 4.0f : 0.0f) : E[nb] + down;
                 const float turn = down + (E[nb] - En);    // exponent of the rescaling of o, <= 0
                 float sum = 0.0f;
-                const float scale = sv > 0.0f ? fminf(ldexpf(sv, (int)((float)kProbExp - En)), 1e38f) : 0.0f;
-                float pv[8];
 #pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const float p = __builtin_amdgcn_exp2f(x[j] - mn);
-                    sum += p;
-                    pv[j] = fminf(p * scale, 32768.0f);
+                for (int y = 0; y < U; y++) {
+                    const float w = e[y] > kZeroExp ? fminf(ldexpf(tvs[y], (int)((float)kProbExp - En)), 1e38f) : 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        const float p = __builtin_amdgcn_exp2f(x[y][j] - mn);
+                        sum += p;
+                        const float v = fminf(p * w, 32768.0f);
+                        const _Float16 p0 = (_Float16)v;
+                        pf[nb][y][0][j] = p0;
+                        if constexpr (kParts == 2) pf[nb][y][1][j] = (_Float16)(v - (float)p0);
+                    }
                 }
                 L[nb] = L[nb] * pow2_down(down) + sum;
                 if (__any(turn < 0.0f)) {
@@ -339,41 +384,36 @@ __global__ __launch_bounds__(kThreads, D == 256 || NB == 2 ? 2 : 4) void k_attn_
                 }
                 m[nb] = mn;
                 E[nb] = En;
-#pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const _Float16 p0 = (_Float16)pv[j];
-                    pf[nb][0][j] = p0;
-                    if constexpr (kParts == 2) pf[nb][1][j] = (_Float16)(pv[j] - (float)p0);
-                }
             }
-            auto dword = [&](int j, int i) -> uint32_t {
-                if constexpr (D == 256) return (i == 0 ? vr[j].x : i == 1 ? vr[j].y : i == 2 ? vr[j].z : vr[j].w) ^ kSign4;
-                else if constexpr (D == 128) return (i == 0 ? vr[j].x : vr[j].y) ^ kSign4;
-                else return vr[j] ^ kSign4;
-            };
 #pragma unroll
-            for (int i = 0; i < kVD; i++) {
-                uint32_t d[8];
+            for (int x = 0; x < U; x++) {
+                auto dword = [&](int j, int i) -> uint32_t {
+                    if constexpr (D == 256) return (i == 0 ? vr[x][j].x : i == 1 ? vr[x][j].y : i == 2 ? vr[x][j].z : vr[x][j].w) ^ kSign4;
+                    else if constexpr (D == 128) return (i == 0 ? vr[x][j].x : vr[x][j].y) ^ kSign4;
+                    else return vr[x][j] ^ kSign4;
+                };
 #pragma unroll
-                for (int j = 0; j < 8; j++) d[j] = dword(j, i);
-                half8_t f[4];
-                f[0] = __builtin_bit_cast(half8_t, make_uint4(codes_pair<0>(d[0], d[1]), codes_pair<0>(d[2], d[3]), codes_pair<0>(d[4], d[5]), codes_pair<0>(d[6], d[7])));
-                f[1] = __builtin_bit_cast(half8_t, make_uint4(codes_pair<1>(d[0], d[1]), codes_pair<1>(d[2], d[3]), codes_pair<1>(d[4], d[5]), codes_pair<1>(d[6], d[7])));
-                f[2] = __builtin_bit_cast(half8_t, make_uint4(codes_pair<2>(d[0], d[1]), codes_pair<2>(d[2], d[3]), codes_pair<2>(d[4], d[5]), codes_pair<2>(d[6], d[7])));
-                f[3] = __builtin_bit_cast(half8_t, make_uint4(codes_pair<3>(d[0], d[1]), codes_pair<3>(d[2], d[3]), codes_pair<3>(d[4], d[5]), codes_pair<3>(d[6], d[7])));
+                for (int i = 0; i < kC; i++) {
+                    uint32_t d[8];
 #pragma unroll
-                for (int k = 0; k < 4; k++)
+                    for (int j = 0; j < 8; j++) d[j] = dword(j, i);
+                    half8_t f[4];
+                    f[0] = __builtin_bit_cast(half8_t, make_uint4(codes_pair<0>(d[0], d[1]), codes_pair<0>(d[2], d[3]), codes_pair<0>(d[4], d[5]), codes_pair<0>(d[6], d[7])));
+                    f[1] = __builtin_bit_cast(half8_t, make_uint4(codes_pair<1>(d[0], d[1]), codes_pair<1>(d[2], d[3]), codes_pair<1>(d[4], d[5]), codes_pair<1>(d[6], d[7])));
+                    f[2] = __builtin_bit_cast(half8_t, make_uint4(codes_pair<2>(d[0], d[1]), codes_pair<2>(d[2], d[3]), codes_pair<2>(d[4], d[5]), codes_pair<2>(d[6], d[7])));
+                    f[3] = __builtin_bit_cast(half8_t, make_uint4(codes_pair<3>(d[0], d[1]), codes_pair<3>(d[2], d[3]), codes_pair<3>(d[4], d[5]), codes_pair<3>(d[6], d[7])));
 #pragma unroll
-                    for (int nb = 0; nb < NB; nb++)
+                    for (int k = 0; k < 4; k++)
 #pragma unroll
-                        for (int pt = 0; pt < kParts; pt++)
-                            o[nb][4 * i + k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[k], pf[nb][pt], o[nb][4 * i + k], 0, 0, 0);
+                        for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                            for (int pt = 0; pt < kParts; pt++)
+                                o[nb][4 * i + k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[k], pf[nb][x][pt], o[nb][4 * i + k], 0, 0, 0);
+                }
             }
             if (more) {
                 load_v(tile + kWaves);
-                page_s = ps;
-                pk = npk;
-                ps = nps;
+                if (tile + 2 * kWaves < stop) find_pages(tile + 2 * kWaves);
             }
         }
 
@@ -448,7 +488,7 @@ __global__ __launch_bounds__(kThreads, D == 256 || NB == 2 ? 2 : 4) void k_attn_
         if (take < wk.tiles) {
             const int64_t w_first = div64((unit0 + 1) * used - 1, line), w_end = div64((unit0 + wk.tiles) * used - 1, line);
             auto slot = [&](unsigned x) { return shared_piece(pieces + (2 * (w_first + x) + (x == 0 ? 1 : 0)) * Lay::kRecord, 4 * Lay::kRecord); };
-            write = join_pieces(counters, w_first, w, w_end, &s_flag, [&](unsigned y) {
+            write = join_pieces<kRadix>(counters, w_first, w, w_end, &s_flag, [&](unsigned y) {
                 const __amdgpu_buffer_rsrc_t p = slot(y);
 #pragma unroll
                 for (int x = 0; x < kItems; x++)
@@ -456,23 +496,31 @@ __global__ __launch_bounds__(kThreads, D == 256 || NB == 2 ? 2 : 4) void k_attn_
                         put_shared4(p, (x * 2 + 0) * kThreads * 16 + tid * 16, v[x][0], v[x][1], v[x][2], v[x][3]);
                         put_shared4(p, (x * 2 + 1) * kThreads * 16 + tid * 16, st[x].m, st[x].E, st[x].L, 0.0f);
                     }
-            }, [&](unsigned y) {
-                const __amdgpu_buffer_rsrc_t p = slot(y);
-                floatx4 f[kItems][2];
+            }, [&](unsigned y0, unsigned step, unsigned pieces_here) {
 #pragma unroll
-                for (int x = 0; x < kItems; x++)
-                    if (x * kSumRows < nrows) {
-                        f[x][0] = get_shared4(p, (x * 2 + 0) * kThreads * 16 + tid * 16);
-                        f[x][1] = get_shared4(p, (x * 2 + 1) * kThreads * 16 + tid * 16);
+                for (int x = 0; x < kItems; x++) {
+                    if (x * kSumRows >= nrows) break;
+                    st[x] = State{kLow, 0.0f, 0.0f};
+                    v[x][0] = v[x][1] = v[x][2] = v[x][3] = 0.0f;
+                    for (unsigned y = 0; y < pieces_here; y += 4) {  // four slots' loads in flight
+                        floatx4 f[4][2];
+#pragma unroll
+                        for (unsigned z = 0; z < 4; z++) {
+                            // past the last slot: the last one, not used
+                            const __amdgpu_buffer_rsrc_t p = slot(y0 + (y + z < pieces_here ? y + z : pieces_here - 1) * step);
+                            f[z][0] = get_shared4(p, (x * 2 + 0) * kThreads * 16 + tid * 16);
+                            f[z][1] = get_shared4(p, (x * 2 + 1) * kThreads * 16 + tid * 16);
+                        }
+#pragma unroll
+                        for (unsigned z = 0; z < 4; z++) {
+                            if (y + z >= pieces_here) break;
+                            float qa, qb;
+                            st[x] = join(st[x], State{f[z][1][0], f[z][1][1], f[z][1][2]}, qa, qb);
+#pragma unroll
+                            for (int i = 0; i < 4; i++) v[x][i] = v[x][i] * qa + f[z][0][i] * qb;
+                        }
                     }
-#pragma unroll
-                for (int x = 0; x < kItems; x++)
-                    if (x * kSumRows < nrows) {
-                        float qa, qb;
-                        st[x] = join(st[x], State{f[x][1][0], f[x][1][1], f[x][1][2]}, qa, qb);
-#pragma unroll
-                        for (int i = 0; i < 4; i++) v[x][i] = v[x][i] * qa + f[x][0][i] * qb;
-                    }
+                }
             });
         }
         if (write) {
@@ -503,7 +551,7 @@ __global__ __launch_bounds__(kThreads, D == 256 || NB == 2 ? 2 : 4) void k_attn_
 }
 
 template <int D, int NB>
-int wgs_of(int num_cu) { return num_cu * (D == 256 || NB == 2 ? 1 : 2); }
+int wgs_of(int num_cu) { return num_cu; }
 
 template <int D, int NB>
 hipError_t launch_nb(const AttnArgs &a, int bf16, int num_cu, hipStream_t stream) {
