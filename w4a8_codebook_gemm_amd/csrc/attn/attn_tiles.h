@@ -87,16 +87,26 @@ __device__ __forceinline__ int fresh(int x) {
     return x;
 }
 
-__device__ __forceinline__ int64_t uniform64(int64_t x) {
-    return (int64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)x) | (int64_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32;
+// Lane l's value (l uniform) as a uniform one.
+__device__ __forceinline__ int lane_value(int x, int l) { return __builtin_amdgcn_readlane(x, l); }
+__device__ __forceinline__ int64_t lane_value(int64_t x, int l) {
+    return (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)x, l) | (int64_t)__builtin_amdgcn_readlane((int)(x >> 32), l) << 32;
 }
 
-__device__ __forceinline__ int64_t scan64(int64_t x, int lane) {
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-        const int64_t o = __shfl_up((long long)x, s);
-        if (lane >= s) x += o;
-    }
+// Inclusive prefix sum over the wave's lanes: shifts within rows of 16, then the rows' ends to the rows after.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ int64_t moved64(int64_t x) {
+    const int lo = __builtin_amdgcn_update_dpp(0, (int)x, kCtrl, kRows, 0xF, false);
+    const int hi = __builtin_amdgcn_update_dpp(0, (int)(x >> 32), kCtrl, kRows, 0xF, false);
+    return (int64_t)(uint32_t)lo | (int64_t)hi << 32;
+}
+__device__ __forceinline__ int64_t scan64(int64_t x) {
+    x += moved64<0x111, 0xF>(x);  // row_shr:1, 2, 4, 8
+    x += moved64<0x112, 0xF>(x);
+    x += moved64<0x114, 0xF>(x);
+    x += moved64<0x118, 0xF>(x);
+    x += moved64<0x142, 0xA>(x);  // row_bcast:15, 31
+    x += moved64<0x143, 0xC>(x);
     return x;
 }
 

@@ -77,12 +77,11 @@ __device__ __forceinline__ int64_t seq_tiles(const AttnArgs &a, int64_t b0, int 
     for (int64_t i = 0; i < (blocks <= 4 ? blocks : 0); i++) tiles += block_tiles<D, BF16>(a, q, i, x);
     for (uint64_t many = __ballot(blocks > 4); many; many &= many - 1) {
         const int src = __ffsll((unsigned long long)many) - 1;
-        const Seq r = {0, __shfl(q.n, src), __shfl(q.len, src), __shfl(q.pos0, src)};
+        const Seq r = {0, lane_value(q.n, src), lane_value(q.len, src), lane_value(q.pos0, src)};
         const int64_t rb = blocks_of<D, BF16>(a, r);
         int64_t sum = 0;
         for (int64_t i = lane; i < rb; i += 64) sum += block_tiles<D, BF16>(a, r, i, x);
-#pragma unroll
-        for (int s = 1; s < 64; s <<= 1) sum += __shfl_xor((long long)sum, s);
+        sum = lane_value(scan64(sum), 63);
         if (lane == src) tiles = sum;
     }
     return tiles * a.c.kv_heads;
@@ -124,14 +123,13 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
 
     int64_t line = 0;
     for (int64_t b0 = 0; b0 < a.s.B; b0 += 64) {
-        const int64_t mine = seq_tiles<D, BF16>(a, b0, lane), incl = scan64(mine, lane);
-        line += __shfl((long long)incl, 63);
+        const int64_t mine = seq_tiles<D, BF16>(a, b0, lane), incl = scan64(mine);
+        line += lane_value(incl, 63);
         if (a.s.B <= 64) {  // every wave writes the same and reads its own
             s_mine[lane] = mine;
             s_incl[lane] = incl;
         }
     }
-    line = uniform64(line);
     if (line == 0) return;
     int64_t used = (line + kMinTiles - 1) / kMinTiles;
     if (used > wgs) used = wgs;
@@ -146,22 +144,18 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
         int64_t base = 0, b = 0, per_head = 0;
         for (int64_t b0 = 0; b0 < a.s.B; b0 += 64) {
             const int64_t mine = a.s.B <= 64 ? s_mine[lane] : seq_tiles<D, BF16>(a, b0, lane);
-            const int64_t incl = a.s.B <= 64 ? s_incl[lane] : scan64(mine, lane);
-            const int64_t sum = uniform64(__shfl((long long)incl, 63));
+            const int64_t incl = a.s.B <= 64 ? s_incl[lane] : scan64(mine);
+            const int64_t sum = lane_value(incl, 63);
             if (at < base + sum) {
                 const int src = __ffsll((unsigned long long)__ballot(at - base < incl)) - 1;
                 b = b0 + src;
-                base += uniform64(__shfl((long long)(incl - mine), src));
-                per_head = div64(uniform64(__shfl((long long)mine, src)), a.c.kv_heads);
+                base += lane_value(incl - mine, src);
+                per_head = div64(lane_value(mine, src), a.c.kv_heads);
                 break;
             }
             base += sum;
         }
-        Seq q = load_seq(a.s, a.M, a.page_shift, b);
-        q.first = uniform64(q.first);
-        q.n = __builtin_amdgcn_readfirstlane(q.n);
-        q.len = __builtin_amdgcn_readfirstlane(q.len);
-        q.pos0 = q.len - q.n;
+        const Seq q = load_seq(a.s, a.M, a.page_shift, b);
         const int64_t blocks = blocks_of<D, BF16>(a, q);
         const int h = (int)div64(at - base, per_head);
         int64_t unit0 = base + h * per_head, rb = 0;  // the unit's first tile on the line
@@ -169,13 +163,13 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
         for (int64_t r = 0; r < blocks; r += 64) {
             int f = 0, c = 0;
             if (r + lane < blocks) c = block_tiles<D, BF16>(a, q, r + lane, f);
-            const int64_t incl = scan64(c, lane), sum = uniform64(__shfl((long long)incl, 63));
+            const int64_t incl = scan64(c), sum = lane_value(incl, 63);
             if (at < unit0 + sum) {
                 const int src = __ffsll((unsigned long long)__ballot(at - unit0 < incl)) - 1;
-                unit0 += uniform64(__shfl((long long)(incl - c), src));
+                unit0 += lane_value(incl - c, src);
                 rb = r + src;
-                first_tile = __builtin_amdgcn_readfirstlane(__shfl(f, src));
-                tiles = __builtin_amdgcn_readfirstlane(__shfl(c, src));
+                first_tile = lane_value(f, src);
+                tiles = lane_value(c, src);
                 break;
             }
             unit0 += sum;

@@ -26,7 +26,7 @@
 namespace w4a8 {
 namespace {
 
-constexpr int kWaves = 8;
+constexpr int kWaves = 4;         // two workgroups on a compute unit: one streams while the other joins
 constexpr int kThreads = 64 * kWaves;
 
 template <int D>
@@ -41,31 +41,34 @@ constexpr int kRadix = 16;       // pieces that join at a time
 struct Work {
     Seq q;
     int lo, tiles;   // first tile, tiles of each unit
-    int64_t total;   // tiles of all its units
+    int64_t units;
 };
 
 template <int RB, int T>
 __device__ __forceinline__ Work seq_work(const AttnArgs &a, int64_t b) {
-    Work w;
+    Work w{};
+    if (b >= a.s.B) return w;
     w.q = load_seq(a.s, a.M, a.page_shift, b);
-    w.lo = w.tiles = 0;
-    w.total = 0;
     if (w.q.n > 0) {
         if (a.window && (int64_t)w.q.pos0 - a.window + 1 > 0) w.lo = (int)(w.q.pos0 - a.window + 1) / T;
         w.tiles = (w.q.len + T - 1) / T - w.lo;
         if (w.tiles < 1) w.tiles = 1;  // rows that see nothing are still written
-        const int64_t blocks = ((int64_t)w.q.n * a.group + RB - 1) / RB;
-        w.total = blocks * a.c.kv_heads * w.tiles;
+        w.units = ((int64_t)w.q.n * a.group + RB - 1) / RB * a.c.kv_heads;
     }
     return w;
 }
 
-constexpr int kSumRows = 8;  // rows that join at a time
+// A unit's tiles on the line: where workgroups are many, as a whole number of their shares.
+__device__ __forceinline__ int on_line(int tiles, int share) { return share ? (tiles + share - 1) / share * share : tiles; }
+
+constexpr int kMaxShare = 4 * kWaves;
 
 template <int D, int NB>
 struct Layout {
     static constexpr int RB = 16 * NB;
-    static constexpr int kRecord = RB / 8 * 2 * kThreads * 4;  // floats of a piece: each thread's values and their state
+    static constexpr int kSumRows = 4 * kThreads / D;   // rows that join at a time, four values of one a thread
+    static constexpr int kItems = RB / kSumRows;
+    static constexpr int kRecord = kItems * 2 * kThreads * 4;  // floats of a piece: each thread's values and their state
     static constexpr int kRow = D + 4;                  // LDS row, padded
     static constexpr int kLds = kWaves * kSumRows * kRow;  // floats
 };
@@ -82,56 +85,68 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_split(AttnArgs a, int wgs)
     __shared__ __attribute__((aligned(16))) float s_o[Lay::kLds];
     __shared__ half8_t s_q[NB * kParts * 2 * kC * 64];
     __shared__ float s_m[kWaves][RB], s_e[kWaves][RB], s_l[kWaves][RB];
+    __shared__ float4 s_all[RB];
     __shared__ int s_flag;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
     uint32_t *counters = static_cast<uint32_t *>(a.ws);
     float *pieces = reinterpret_cast<float *>(static_cast<char *>(a.ws) + kAttnCounterBytes);
 
     // the line's length, and this workgroup's part of it
-    int64_t line = 0;
-    for (int64_t b0 = 0; b0 < a.s.B; b0 += 64)
-        line += __shfl((long long)scan64(b0 + lane < a.s.B ? seq_work<RB, T>(a, b0 + lane).total : 0, lane), 63);
-    line = uniform64(line);
+    // Even parts may end inside a unit, and a workgroup that has parts of two pays twice for starting
+    // and joining.  While a part is not more than kMaxShare tiles, units are cut into whole shares of
+    // that many tiles instead, each a workgroup's, if there are workgroups enough.
+    Work x = seq_work<RB, T>(a, lane);
+    auto total = [&](int share) {
+        int64_t sum = 0;
+        for (int64_t b0 = 0; b0 < a.s.B; b0 += 64) {
+            if (a.s.B > 64) x = seq_work<RB, T>(a, b0 + lane);
+            sum += lane_value(scan64(x.units * on_line(x.tiles, share)), 63);
+        }
+        return sum;
+    };
+    int64_t line = total(0);
     if (line == 0) return;
-    int64_t used = (line + kWaves - 1) / kWaves;  // at least a tile for each wave
-    if (used > wgs) used = wgs;
+    int share = 0;
+    for (int64_t c = div64(line + (int64_t)wgs * kWaves - 1, (int64_t)wgs * kWaves) * kWaves; c <= kMaxShare && share == 0; c += kWaves) {
+        const int64_t sum = total((int)c);
+        if (sum <= (int64_t)wgs * c) {
+            share = (int)c;
+            line = sum;
+        }
+    }
+    const int64_t used = share ? div64(line, share) : wgs;
     const int64_t w = blockIdx.x;
     if (w >= used) return;
-    const int64_t t0 = div64(w * line, used), t1 = div64((w + 1) * line, used);
+    const int64_t t0 = share ? w * share : div64(w * line, used), t1 = share ? t0 + share : div64((w + 1) * line, used);
 
     for (int64_t at = t0; at < t1;) {
         // the sequence and unit that tile `at` is in
         int64_t base = 0, b = 0;
-        Work wk{};
+        int lo_tile = 0, tiles = 1;
         for (int64_t b0 = 0; b0 < a.s.B; b0 += 64) {
-            Work x{};
-            if (b0 + lane < a.s.B) x = seq_work<RB, T>(a, b0 + lane);
-            const int64_t incl = scan64(x.total, lane);
-            const int64_t sum = uniform64(__shfl((long long)incl, 63));
+            if (a.s.B > 64) x = seq_work<RB, T>(a, b0 + lane);
+            const int64_t mine = x.units * on_line(x.tiles, share), incl = scan64(mine), sum = lane_value(incl, 63);
             if (at < base + sum) {
-                const uint64_t hit = __ballot(at - base < incl);
-                const int src = __ffsll((unsigned long long)hit) - 1;
+                const int src = __ffsll((unsigned long long)__ballot(at - base < incl)) - 1;
                 b = b0 + src;
-                base += uniform64(__shfl((long long)(incl - x.total), src));
-                wk.q.first = uniform64(__shfl((long long)x.q.first, src));
-                wk.q.n = __builtin_amdgcn_readfirstlane(__shfl(x.q.n, src));
-                wk.q.len = __builtin_amdgcn_readfirstlane(__shfl(x.q.len, src));
-                wk.q.pos0 = wk.q.len - wk.q.n;
-                wk.lo = __builtin_amdgcn_readfirstlane(__shfl(x.lo, src));
-                wk.tiles = __builtin_amdgcn_readfirstlane(__shfl(x.tiles, src));
+                base += lane_value(incl - mine, src);
+                lo_tile = lane_value(x.lo, src);
+                tiles = lane_value(x.tiles, src);
                 break;
             }
             base += sum;
         }
-        const int64_t unit = div64(at - base, wk.tiles);
-        const int64_t unit0 = base + unit * wk.tiles;       // the unit's first tile on the line
+        const Seq q = load_seq(a.s, a.M, a.page_shift, b);
+        const int length = on_line(tiles, share);
+        const int64_t unit = div64(at - base, length);
+        const int64_t unit0 = base + unit * length;         // the unit's first tile on the line
         const int tile0 = (int)(at - unit0);
-        const int take = (int)(wk.tiles - tile0 < t1 - at ? wk.tiles - tile0 : t1 - at);
+        const int take = (int)(tiles - tile0 < t1 - at ? tiles - tile0 : t1 - at);
         const int64_t rblock = div64(unit, a.c.kv_heads);
         const int h = (int)(unit - rblock * a.c.kv_heads);
 
         // this lane's rows
-        const int64_t rows = (int64_t)wk.q.n * a.group;
+        const int64_t rows = (int64_t)q.n * a.group;
         const int64_t r0 = rblock * RB;
         const int nrows = (int)(rows - r0 < RB ? rows - r0 : RB);
         int lo[NB], hi[NB];
@@ -148,12 +163,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_split(AttnArgs a, int wgs)
             int hd;
             row_at(0, t_first, hd);
             row_at(nrows - 1, t_last, hd);
-            sees(a, wk.q, t_first, any_lo, all_hi);
-            sees(a, wk.q, t_last, all_lo, any_hi);
+            sees(a, q, t_first, any_lo, all_hi);
+            sees(a, q, t_last, all_lo, any_hi);
         }
 
-        const int end = wk.lo + tile0 + take;
-        int first = wk.lo + tile0 + wave;
+        const int end = lo_tile + tile0 + take;
+        int first = lo_tile + tile0 + wave;
         if (first < any_lo / T) first += (any_lo / T - first + kWaves - 1) / kWaves * kWaves;
         const int stop = end < (any_hi + T - 1) / T ? end : (any_hi + T - 1) / T;
         const int P = a.c.page_size, pm = P - 1;
@@ -161,7 +176,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_split(AttnArgs a, int wgs)
         const int32_t *table = a.s.page_table + b * a.s.table_width;
 
         auto page_of = [&](int t) {  // page of position t, -1 past the end
-            return t < wk.q.len ? table[t >> a.page_shift] : -1;
+            return t < q.len ? table[t >> a.page_shift] : -1;
         };
         auto block_of = [&](int page) {  // its block of this head; a page that is not there reads page 0, masked
             return (int64_t)((uint32_t)page < (uint32_t)a.c.num_pages ? page : 0) * a.c.kv_heads + h;
@@ -228,14 +243,14 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_split(AttnArgs a, int wgs)
             hi[nb] = 0;
             if (r < nrows) {
                 row_at(r, token, head);
-                sees(a, wk.q, token, lo[nb], hi[nb]);
+                sees(a, q, token, lo[nb], hi[nb]);
             }
 #pragma unroll
             for (int c = 0; c < kC; c++)
 #pragma unroll
                 for (int u = 0; u < 2; u++) {
                     if (r < nrows) {
-                        load_q8<BF16>(a.q, (wk.q.first + token) * a.q_stride + head * D + 64 * c + 16 * g + 8 * u, v[c][u]);
+                        load_q8<BF16>(a.q, (q.first + token) * a.q_stride + head * D + 64 * c + 16 * g + 8 * u, v[c][u]);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 8; i++) v[c][u][i] = 0.0f;
@@ -429,22 +444,23 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_split(AttnArgs a, int wgs)
             }
         }
         __syncthreads();
-        float mj[NB], ej[NB];
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
             const int r = 16 * nb + n;
             float mm = s_m[0][r], ee = kLow;
             for (int x = 1; x < kWaves; x++) mm = fmaxf(mm, s_m[x][r]);
             for (int x = 0; x < kWaves; x++) ee = fmaxf(ee, s_e[x][r] + (s_m[x][r] - mm));
-            mj[nb] = mm;
-            ej[nb] = ee;
+            if (wave == nb && g == 0) {
+                float l = 0.0f;
+                for (int x = 0; x < kWaves; x++) l += s_l[x][r] * pow2_down(s_m[x][r] - mm);
+                s_all[r] = make_float4(mm, ee, l, 0.0f);
+            }
             const float q = pow2_down((m[nb] - mm) + (E[nb] - ee));
 #pragma unroll
             for (int i = 0; i < kT; i++) o[nb][i] *= q;
         }
         // sum over the waves, kSumRows rows at a time; a thread ends with four values of a row of each
-        constexpr int kItems = RB / kSumRows;
-        constexpr bool kAll = kSumRows * (D / 4) == kThreads;
+        constexpr int kItems = Lay::kItems, kSumRows = Lay::kSumRows;
         const int ir = tid / (D / 4), id = 4 * (tid % (D / 4));
         float v[kItems][4];
         State st[kItems];
@@ -467,26 +483,20 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_split(AttnArgs a, int wgs)
             }
             __syncthreads();
             v[x][0] = v[x][1] = v[x][2] = v[x][3] = 0.0f;
-            st[x] = State{kLow, 0.0f, 0.0f};
-            if (kAll || ir < kSumRows) {
+            {
 #pragma unroll
                 for (int y = 0; y < kWaves; y++) {
                     const float4 f = *reinterpret_cast<const float4 *>(s_o + (y * kSumRows + ir) * Lay::kRow + id);
                     v[x][0] += f.x; v[x][1] += f.y; v[x][2] += f.z; v[x][3] += f.w;
                 }
-                const int r = q0 + ir;
-                for (int y = 0; y < kWaves; y++) st[x].m = fmaxf(st[x].m, s_m[y][r]);
-                st[x].E = kLow;
-                for (int y = 0; y < kWaves; y++) {
-                    st[x].E = fmaxf(st[x].E, s_e[y][r] + (s_m[y][r] - st[x].m));
-                    st[x].L += s_l[y][r] * pow2_down(s_m[y][r] - st[x].m);
-                }
+                const float4 f = s_all[q0 + ir];
+                st[x] = State{f.x, f.y, f.z};
             }
             __syncthreads();
         }
         bool write = true;
-        if (take < wk.tiles) {
-            const int64_t w_first = div64((unit0 + 1) * used - 1, line), w_end = div64((unit0 + wk.tiles) * used - 1, line);
+        if (take < tiles) {
+            const int64_t w_first = div64((unit0 + 1) * used - 1, line), w_end = div64((unit0 + length) * used - 1, line);
             auto slot = [&](unsigned x) { return shared_piece(pieces + (2 * (w_first + x) + (x == 0 ? 1 : 0)) * Lay::kRecord, 4 * Lay::kRecord); };
             write = join_pieces<kRadix>(counters, w_first, w, w_end, &s_flag, [&](unsigned y) {
                 const __amdgpu_buffer_rsrc_t p = slot(y);
@@ -527,14 +537,14 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_split(AttnArgs a, int wgs)
 #pragma unroll
             for (int x = 0; x < kItems; x++) {
                 const int r = x * kSumRows + ir;
-                if ((kAll || ir < kSumRows) && r < nrows) {
+                if (r < nrows) {
                     const float inv = st[x].L > 0.0f ? 1.0f / st[x].L : 0.0f;
 #pragma unroll
                     for (int i = 0; i < 4; i++) v[x][i] = ldexpf(v[x][i] * inv, (int)st[x].E + kCodeExp - kProbExp);
                     int64_t token;
                     int head;
                     row_at(r, token, head);
-                    const int64_t off = ((wk.q.first + token) * a.hq + head) * D + id;
+                    const int64_t off = ((q.first + token) * a.hq + head) * D + id;
                     if constexpr (BF16) {
                         uint2 u;
                         u.x = (uint32_t)f32_to_bf16_rne(v[x][0]) | (uint32_t)f32_to_bf16_rne(v[x][1]) << 16;
@@ -546,12 +556,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_split(AttnArgs a, int wgs)
                 }
             }
         }
-        at += take;
+        at = unit0 + length < t1 ? unit0 + length : t1;
     }
 }
 
 template <int D, int NB>
-int wgs_of(int num_cu) { return num_cu; }
+int wgs_of(int num_cu) { return 2 * num_cu; }
 
 template <int D, int NB>
 hipError_t launch_nb(const AttnArgs &a, int bf16, int num_cu, hipStream_t stream) {
