@@ -21,6 +21,8 @@
 // Split: the tiles of all units form one line that is cut evenly over the workgroups whatever the
 // lengths are; a workgroup's waves take its tiles in turn and join in LDS.  The pieces of a unit
 // that is cut are joined through the workspace (join_pieces).
+#include <type_traits>
+
 #include "attn_tiles.h"
 
 namespace w4a8 {
@@ -29,13 +31,23 @@ namespace {
 constexpr int kWaves = 4;         // two workgroups on a compute unit: one streams while the other joins
 constexpr int kThreads = 64 * kWaves;
 
+// Values are read by one lane once: past the caches.
+template <class V>
+__device__ __forceinline__ V load_once(const int8_t *p) {
+    typedef uint32_t type __attribute__((ext_vector_type(sizeof(V) / 4)));
+    return __builtin_bit_cast(V, __builtin_nontemporal_load(reinterpret_cast<const type *>(p)));
+}
+
 template <int D>
 struct VLoad;
 template <> struct VLoad<256> { typedef uint4 type; };
 template <> struct VLoad<128> { typedef uint2 type; };
 template <> struct VLoad<64> { typedef uint32_t type; };
 
-constexpr int kRadix = 16;       // pieces that join at a time
+// Workgroups on a compute unit: blocks of 32 rows need the registers of two.
+template <int NB>
+constexpr int kPerCu = NB == 2 ? 1 : 2;
+constexpr int kRadix = 8;        // pieces that join at a node
 
 // How a sequence contributes to the line of tiles.
 struct Work {
@@ -68,13 +80,13 @@ struct Layout {
     static constexpr int RB = 16 * NB;
     static constexpr int kSumRows = 4 * kThreads / D;   // rows that join at a time, four values of one a thread
     static constexpr int kItems = RB / kSumRows;
-    static constexpr int kRecord = kItems * 2 * kThreads * 4;  // floats of a piece: each thread's values and their state
+    static constexpr int kRecord = kItems * kThreads * 4 + RB * 4;  // floats of a piece: each thread's values, each row's state
     static constexpr int kRow = D + 4;                  // LDS row, padded
     static constexpr int kLds = kWaves * kSumRows * kRow;  // floats
 };
 
 template <int D, int NB, bool BF16>
-__global__ __launch_bounds__(kThreads, 2) void k_attn_split(AttnArgs a, int wgs) {
+__global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_attn_split(AttnArgs a, int wgs) {
     using Lay = Layout<D, NB>;
     using VT = typename VLoad<D>::type;
     constexpr int RB = Lay::RB;
@@ -211,7 +223,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_split(AttnArgs a, int wgs)
             for (int x = 0; x < U; x++) {
                 const int8_t *p = a.c.v + (block_of(ps[x]) * P + ((tile * T + 32 * x + (l >> 4) * 8) & pm)) * D + (l & 15) * (D / 16);
 #pragma unroll
-                for (int j = 0; j < 8; j++) vr[x][j] = *reinterpret_cast<const VT *>(p + j * D);
+                for (int j = 0; j < 8; j++) vr[x][j] = load_once<VT>(p + j * D);
             }
         };
         // value scale -1 where the page is not there
@@ -501,35 +513,40 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_split(AttnArgs a, int wgs)
             write = join_pieces<kRadix>(counters, w_first, w, w_end, &s_flag, [&](unsigned y) {
                 const __amdgpu_buffer_rsrc_t p = slot(y);
 #pragma unroll
-                for (int x = 0; x < kItems; x++)
-                    if (x * kSumRows < nrows) {
-                        put_shared4(p, (x * 2 + 0) * kThreads * 16 + tid * 16, v[x][0], v[x][1], v[x][2], v[x][3]);
-                        put_shared4(p, (x * 2 + 1) * kThreads * 16 + tid * 16, st[x].m, st[x].E, st[x].L, 0.0f);
+                for (int x = 0; x < kItems; x++) {
+                    const int r = x * kSumRows + ir;
+                    if (r < nrows) {
+                        put_shared4(p, (x * kThreads + tid) * 16, v[x][0], v[x][1], v[x][2], v[x][3]);
+                        if (id == 0) put_shared4(p, (kItems * kThreads + r) * 16, st[x].m, st[x].E, st[x].L, 0.0f);
                     }
+                }
             }, [&](unsigned y0, unsigned step, unsigned pieces_here) {
 #pragma unroll
                 for (int x = 0; x < kItems; x++) {
-                    if (x * kSumRows >= nrows) break;
+                    const int r = x * kSumRows + ir;
+                    if (r >= nrows) break;
                     st[x] = State{kLow, 0.0f, 0.0f};
                     v[x][0] = v[x][1] = v[x][2] = v[x][3] = 0.0f;
-                    for (unsigned y = 0; y < pieces_here; y += 4) {  // four slots' loads in flight
-                        floatx4 f[4][2];
+                    auto some = [&](auto count, unsigned y) {  // so many slots from y on, their loads together
+                        constexpr int kCount = decltype(count)::value;
+                        floatx4 f[kCount], t[kCount];
 #pragma unroll
-                        for (unsigned z = 0; z < 4; z++) {
-                            // past the last slot: the last one, not used
-                            const __amdgpu_buffer_rsrc_t p = slot(y0 + (y + z < pieces_here ? y + z : pieces_here - 1) * step);
-                            f[z][0] = get_shared4(p, (x * 2 + 0) * kThreads * 16 + tid * 16);
-                            f[z][1] = get_shared4(p, (x * 2 + 1) * kThreads * 16 + tid * 16);
+                        for (int z = 0; z < kCount; z++) {
+                            const __amdgpu_buffer_rsrc_t p = slot(y0 + (y + z) * step);
+                            f[z] = get_shared4(p, (x * kThreads + tid) * 16);
+                            t[z] = get_shared4(p, (kItems * kThreads + r) * 16);
                         }
 #pragma unroll
-                        for (unsigned z = 0; z < 4; z++) {
-                            if (y + z >= pieces_here) break;
+                        for (int z = 0; z < kCount; z++) {
                             float qa, qb;
-                            st[x] = join(st[x], State{f[z][1][0], f[z][1][1], f[z][1][2]}, qa, qb);
+                            st[x] = join(st[x], State{t[z][0], t[z][1], t[z][2]}, qa, qb);
 #pragma unroll
-                            for (int i = 0; i < 4; i++) v[x][i] = v[x][i] * qa + f[z][0][i] * qb;
+                            for (int i = 0; i < 4; i++) v[x][i] = v[x][i] * qa + f[z][i] * qb;
                         }
-                    }
+                    };
+                    unsigned y = 0;
+                    for (; y + 4 <= pieces_here; y += 4) some(std::integral_constant<int, 4>(), y);
+                    for (; y < pieces_here; y++) some(std::integral_constant<int, 1>(), y);
                 }
             });
         }
@@ -561,7 +578,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_split(AttnArgs a, int wgs)
 }
 
 template <int D, int NB>
-int wgs_of(int num_cu) { return 2 * num_cu; }
+int wgs_of(int num_cu) { return kPerCu<NB> * num_cu; }
 
 template <int D, int NB>
 hipError_t launch_nb(const AttnArgs &a, int bf16, int num_cu, hipStream_t stream) {
