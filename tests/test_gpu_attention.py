@@ -268,6 +268,23 @@ def test_attention(A, new, lens, Hq, Hkv, D, page, dtype, causal, window):
     check_attention(A, q, b, codes, scales, cache, causal, window)
 
 
+@pytest.mark.parametrize("new,lo,hi,count,Hq,Hkv,D,dtype", [
+    (1, 500, 6000, 40, 24, 4, 256, BF),       # several units and parts of units for a workgroup, blocks of 16 rows
+    (1, 20, 1500, 300, 8, 8, 64, F32),        # more sequences than a wave has lanes
+    (7, 300, 2500, 40, 12, 3, 128, BF),       # blocks of 32 rows
+    (60, 60, 1200, 70, 8, 2, 128, BF),        # many rows, more sequences than lanes
+    (90, 90, 900, 10, 8, 2, 256, F32),
+])
+def test_attention_of_many_units(A, new, lo, hi, count, Hq, Hkv, D, dtype):
+    """Batches large enough that a workgroup has several units, cut anywhere."""
+    rng = np.random.default_rng(D + count)
+    lens = rng.integers(lo, hi, count)
+    b = Batch(A, rng, [new] * count, list(lens), 16)
+    codes, scales, cache = random_cache(A, rng, b.pages, Hkv, 16, D)
+    q = dev(rng.standard_normal((b.M, Hq, D)).astype(np.float32), dtype)
+    check_attention(A, q, b, codes, scales, cache)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("new", [[1, 1, 1], [40, 90, 20]])
 def test_attention_pages_given_up(A, dtype, new):

@@ -573,7 +573,7 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_attn_split(AttnArgs a,
                 }
             }
         }
-        at = unit0 + length < t1 ? unit0 + length : t1;
+        at = unit0 + length;
     }
 }
 
