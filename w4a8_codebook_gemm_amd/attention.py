@@ -18,7 +18,7 @@ from dataclasses import dataclass, field
 
 import torch
 
-from . import BF16, F32, STATUS, _dev, _fdtype
+from . import BF16, F32, STATUS, _dev
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libw4a8_attn.so")
@@ -87,22 +87,27 @@ def _check(status: int, what: str):
         raise AttentionError(status, what)
 
 
-class _on:
-    """The tensors' device as the current one; a no-op where it is already."""
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
-    def __init__(self, device):
-        self._index = device.index
-        self._guard = None
 
-    def __enter__(self):
-        if torch.cuda.current_device() != self._index:
-            self._guard = torch.cuda.device(self._index)
-            self._guard.__enter__()
-        return torch._C._cuda_getCurrentRawStream(self._index)
+def _launch(dev: torch.device, what: str, f, *args):
+    """f(*args, stream) with the tensors' device as the current one and its current stream."""
+    i = dev.index
+    if _current_device() == i:
+        st = f(*args, _raw_stream(i))
+    else:
+        with torch.cuda.device(i):
+            st = f(*args, _raw_stream(i))
+    if st != 0:
+        raise AttentionError(st, what)
 
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+
+def _ptr(t, name: str, dtype, shape, dev) -> int:
+    """_dev for one dtype, its tests in the order of a good call: the message is made only for a bad one."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    return _dev(t, name, (dtype,), shape, dev)
 
 
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
@@ -139,26 +144,30 @@ def _rows(t: torch.Tensor, name: str, dtypes, heads=None, dim=None, device=None)
     return t.data_ptr(), st if m > 1 else h * d
 
 
-def _heads(t, name, weight, wname, out_dtype, out, m, d, device, dtype):
-    if t.device.type != "cuda" or (device is not None and t.device != device):
-        raise ValueError(f"{name} is on {t.device}, expected {device or 'a GPU device'}")
-    if t.dtype not in _FLOATS or (dtype is not None and t.dtype != dtype):
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype or _FLOATS}")
-    if t.dim() != 3 or t.shape[0] != m or t.shape[2] != d:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{m}, heads, {d}]")
+def _heads(t, name, weight, out_dtype, out, m, d, dev, dtype):
+    """w4a8_heads of one operand, and its output."""
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != m or shape[2] != d:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [{m}, heads, {d}]")
+    h = shape[1]
     st, sh, sd = t.stride()
-    h = t.shape[1]
     if sd != 1:
         raise ValueError(f"{name}: the values of a head must be consecutive, strides are {t.stride()}")
     if m == 1:
         st = 0
-    elif st < 0 or (st < d and st != 0):
+    elif st < d and st != 0:
         raise ValueError(f"{name}: tokens overlap, strides are {t.stride()}")
     if out is None:
-        out = torch.empty((m, h, d), dtype=out_dtype, device=t.device)
-    wp = 0 if weight is None else _dev(weight, wname, (torch.float32,), (d,), t.device)
-    return CHeads(t.data_ptr(), st, sh if h > 1 else d, h, wp,
-                  _dev(out, f"{name}'s output", (out_dtype,), (m, h, d), t.device)), out
+        out = t.new_empty((m, h, d), dtype=out_dtype)
+        op = out.data_ptr()
+    else:
+        op = _ptr(out, name + "'s output", out_dtype, (m, h, d), dev)
+    wp = 0 if weight is None else _ptr(weight, name + "_weight", torch.float32, (d,), dev)
+    return CHeads(t.data_ptr(), st, sh if h > 1 else d, h, wp, op), out
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_freq: torch.Tensor, *,
@@ -174,26 +183,28 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tenso
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be 3-D [tokens, heads, head_dim]")
     m, _, d = q.shape
-    dev = q.device
-    out_dtype = q.dtype if out_dtype is None else out_dtype
-    if out_dtype not in _FLOATS:
+    dev, dtype = q.device, q.dtype
+    if dev.type != "cuda":
+        raise ValueError(f"q must be on a GPU device, got {dev}")
+    if dtype not in _FLOATS:
+        raise TypeError(f"q has dtype {dtype}, expected one of {_FLOATS}")
+    if out_dtype is None:
+        out_dtype = dtype
+    elif out_dtype not in _FLOATS:
         raise TypeError(f"out_dtype {out_dtype}, expected one of {_FLOATS}")
     q_out, k_out = out if out is not None else (None, None)
-    ch, q_out = _heads(q, "q", q_weight, "q_weight", out_dtype, q_out, m, d, None, None)
+    ch, q_out = _heads(q, "q", q_weight, out_dtype, q_out, m, d, dev, dtype)
     kp = 0
     if k is not None:
-        ck, k_out = _heads(k, "k", k_weight, "k_weight", out_dtype, k_out, m, d, dev, q.dtype)
+        ck, k_out = _heads(k, "k", k_weight, out_dtype, k_out, m, d, dev, dtype)
         kp = C.addressof(ck)
     else:
         k_out = None
-    if inv_freq.dim() != 1:
-        raise ValueError("inv_freq must be 1-D [rotary_dim / 2]")
-    pp = _dev(positions, "positions", (torch.int32,), (m,), dev)
-    fp = _dev(inv_freq, "inv_freq", (torch.float64,), None, dev)
-    with _on(dev) as stream:
-        _check(lib().w4a8_qk_norm_rope(C.addressof(ch), kp, m, d, _fdtype(q), BF16 if out_dtype is torch.bfloat16 else F32,
-                                       pp, fp, 2 * inv_freq.shape[0], int(interleaved), attn_factor, eps, weight_offset,
-                                       stream), "w4a8_qk_norm_rope")
+    half = inv_freq.numel()
+    _launch(dev, "w4a8_qk_norm_rope", lib().w4a8_qk_norm_rope, C.addressof(ch), kp, m, d, BF16 if dtype is torch.bfloat16 else F32,
+            BF16 if out_dtype is torch.bfloat16 else F32, _ptr(positions, "positions", torch.int32, (m,), dev),
+            _ptr(inv_freq, "inv_freq", torch.float64, (half,), dev), 2 * half, 1 if interleaved else 0, attn_factor, eps,
+            weight_offset)
     return q_out, k_out
 
 
@@ -245,9 +256,9 @@ class Sequences:
             _dev(self.seq_lens, "seq_lens", (torch.int32,), (b,), dev), b, w))
 
 
-def _same_device(x: torch.Tensor, cache: KVCache, seqs: Sequences):
-    if cache.k.device != x.device or seqs.page_table.device != x.device:
-        raise ValueError(f"tokens on {x.device}, cache on {cache.k.device}, sequences on {seqs.page_table.device}")
+def _same_device(dev: torch.device, cache: KVCache, seqs: Sequences):
+    if cache.k.device != dev or seqs.page_table.device != dev:
+        raise ValueError(f"tokens on {dev}, cache on {cache.k.device}, sequences on {seqs.page_table.device}")
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, seqs: Sequences) -> None:
@@ -256,13 +267,14 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, seqs: Sequences)
     append to."""
     cc = cache.c
     kp, ks = _rows(k, "k", _FLOATS, cc.kv_heads, cc.head_dim)
-    vp, vs = _rows(v, "v", (k.dtype,), cc.kv_heads, cc.head_dim, k.device)
-    if v.shape[0] != k.shape[0]:
-        raise ValueError(f"k has {k.shape[0]} tokens, v {v.shape[0]}")
-    _same_device(k, cache, seqs)
-    with _on(k.device) as stream:
-        _check(lib().w4a8_kv_append(kp, ks, vp, vs, _fdtype(k), k.shape[0], C.addressof(cc), C.addressof(seqs.c), stream),
-               "w4a8_kv_append")
+    dev = k.device
+    vp, vs = _rows(v, "v", (k.dtype,), cc.kv_heads, cc.head_dim, dev)
+    m = k.shape[0]
+    if v.shape[0] != m:
+        raise ValueError(f"k has {m} tokens, v {v.shape[0]}")
+    _same_device(dev, cache, seqs)
+    _launch(dev, "w4a8_kv_append", lib().w4a8_kv_append, kp, ks, vp, vs, BF16 if k.dtype is torch.bfloat16 else F32, m,
+            C.addressof(cc), C.addressof(seqs.c))
 
 
 def kv_attention_workspace_bytes(tokens: int, sequences: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
@@ -292,17 +304,18 @@ def kv_attention(q: torch.Tensor, cache: KVCache, seqs: Sequences, *, scale: flo
     cc, sc = cache.c, seqs.c
     qp, qs = _rows(q, "q", _FLOATS, None, cc.head_dim)
     m, hq, d = q.shape
-    _same_device(q, cache, seqs)
+    dev, dtype = q.device, q.dtype
+    _same_device(dev, cache, seqs)
     if workspace is None:
-        workspace = kv_attention_workspace(max(m, 1), sc.B, hq, cc.kv_heads, d, q.device)
-    elif workspace.device != q.device or not workspace.is_contiguous():
+        workspace = kv_attention_workspace(max(m, 1), sc.B, hq, cc.kv_heads, d, dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the device of q")
     if out is None:
-        out = torch.empty((m, hq, d), dtype=q.dtype, device=q.device)
-    op = _dev(out, "out", (q.dtype,), (m, hq, d), q.device)
-    with _on(q.device) as stream:
-        _check(lib().w4a8_kv_attention(qp, qs, _fdtype(q), m, hq, C.addressof(cc), C.addressof(sc),
-                                       d ** -0.5 if scale is None else scale, int(causal), window, op,
-                                       workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream),
-               "w4a8_kv_attention")
+        out = q.new_empty((m, hq, d))
+        op = out.data_ptr()
+    else:
+        op = _ptr(out, "out", dtype, (m, hq, d), dev)
+    _launch(dev, "w4a8_kv_attention", lib().w4a8_kv_attention, qp, qs, BF16 if dtype is torch.bfloat16 else F32, m, hq,
+            C.addressof(cc), C.addressof(sc), d ** -0.5 if scale is None else scale, 1 if causal else 0, window, op,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out
