@@ -169,12 +169,13 @@ int w4a8_kv_append(const void *k, int64_t k_stride, const void *v, int64_t v_str
 }
 
 // Rows (new tokens x query heads of a cache head) a sequence has on average decide the kernel:
-// to 16 they are the split kernel's block of 16, to 32 its block of 32, above that the prompt kernel.
+// to 16 they are the split kernel's block of 16, to 64 its blocks of 32, above that the prompt kernel.
+constexpr int64_t kSplitRows = 64;
 static int64_t rows_per_sequence(int64_t M, int64_t B, int group) { return (M * group + B - 1) / B; }
 
 // The pieces of cut units that the kernel for this shape leaves behind the counters.
 static int64_t attn_bytes(int64_t M, int64_t B, int group, int head_dim, int num_cu) {
-    return w4a8::kAttnCounterBytes + (rows_per_sequence(M, B, group) <= 32 ? w4a8::attn_split_bytes(head_dim, num_cu)
+    return w4a8::kAttnCounterBytes + (rows_per_sequence(M, B, group) <= kSplitRows ? w4a8::attn_split_bytes(head_dim, num_cu)
                                                                            : w4a8::attn_prompt_bytes(head_dim, num_cu));
 }
 
@@ -194,7 +195,7 @@ int64_t w4a8_kv_attention_workspace_bytes(int64_t M, int64_t B, int q_heads, int
     if (st != W4A8_OK) return -st;
     // a call of fewer tokens or sequences may take either kernel
     const int64_t split = w4a8::attn_split_bytes(head_dim, num_cu), prompt = w4a8::attn_prompt_bytes(head_dim, num_cu);
-    return w4a8::kAttnCounterBytes + (M * (q_heads / kv_heads) <= 32 || split > prompt ? split : prompt);
+    return w4a8::kAttnCounterBytes + (M * (q_heads / kv_heads) <= kSplitRows || split > prompt ? split : prompt);
 }
 
 int w4a8_kv_attention(const void *q, int64_t q_stride, int dtype, int64_t M, int q_heads, const w4a8_kv_cache *cache,
@@ -223,7 +224,7 @@ int w4a8_kv_attention(const void *q, int64_t q_stride, int dtype, int64_t M, int
                      workspace};
     hipStream_t st2 = static_cast<hipStream_t>(stream);
     const int64_t rows = rows_per_sequence(M, seqs->B, group);
-    return status_of(rows <= 32 ? w4a8::launch_attn_split(a, dtype == W4A8_BF16, rows <= 16 ? 1 : 2, num_cu, st2)
+    return status_of(rows <= kSplitRows ? w4a8::launch_attn_split(a, dtype == W4A8_BF16, rows <= 16 ? 1 : 2, num_cu, st2)
                                 : w4a8::launch_attn_prompt(a, dtype == W4A8_BF16, num_cu, st2));
 }
 

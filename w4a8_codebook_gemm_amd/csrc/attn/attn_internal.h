@@ -50,6 +50,13 @@ hipError_t launch_attn_split(const AttnArgs &a, int bf16, int blocks, int num_cu
 int64_t attn_prompt_bytes(int head_dim, int num_cu);
 hipError_t launch_attn_prompt(const AttnArgs &a, int bf16, int num_cu, hipStream_t stream);
 
+// Two values as bf16, to nearest even (one instruction on gfx950).
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    const bf16x2_t v = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
 // One sequence as the kernels see it, every number held to its range: rows first .. first + n - 1,
 // length, and the position of the first row (negative where the length is shorter than n).
 struct Seq {

@@ -69,6 +69,38 @@ __device__ __forceinline__ float pow2_down(float x) { return __builtin_amdgcn_ex
 constexpr int kZeroExp = -300;       // exponent of a value scale of zero
 constexpr float kLow = -3.0e38f;  // "no score yet"
 
+// Eight consecutive query values as they lie in memory, and as fp32.
+template <bool BF16>
+struct RawQ {
+    uint4 a, b;  // b: fp32 only
+    __device__ __forceinline__ void load(const void *q, int64_t off) {
+        if constexpr (BF16) {
+            a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(q) + off);
+        } else {
+            const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(q) + off);
+            a = p[0];
+            b = p[1];
+        }
+    }
+    __device__ __forceinline__ void values(float v[8]) const {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+        if constexpr (BF16) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            }
+        } else {
+            const uint32_t x[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                v[i] = __uint_as_float(w[i]);
+                v[4 + i] = __uint_as_float(x[i]);
+            }
+        }
+    }
+};
+
 // The larger of x and that of lane ^ 32 or lane ^ 16: with both operands x, the swap of half waves
 // (of the odd 16-lane rows with the even ones) leaves the two in its two results.
 typedef uint32_t uintx2 __attribute__((ext_vector_type(2)));

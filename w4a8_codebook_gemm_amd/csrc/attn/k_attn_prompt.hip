@@ -203,26 +203,33 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
             int64_t token = 0;
             int head = 0;
             if (nrows) row_of(token, head);
+            // (a wave without rows reads the first row of its sequence, for nothing)
             const int64_t off = (q.first + token) * a.q_stride + (int64_t)head * D + 8 * hh;
+            // all of the row's values at once, as they lie
+            RawQ<BF16> raw[kSteps];
+#pragma unroll
+            for (int s = 0; s < kSteps; s++) raw[s].load(a.q, off + 16 * s);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int s = 0; s < kSteps; s++) {
-                float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                if (n < nrows) load_q8<BF16>(a.q, off + 16 * s, v);
+                float v[8];
+                raw[s].values(v);
 #pragma unroll
                 for (int i = 0; i < 8; i++) top = fmaxf(top, fabsf(v[i]));
             }
-            top = fmaxf(top, __shfl_xor(top, 32));
+            if (n >= nrows) top = 0.0f;
+            top = max_xor32(top);
             // the row's largest value at 2^13 .. 2^14, as in the split kernel
             int ex = 0;
             if (top > 0.0f) frexpf(top, &ex);
             fac = ldexpf(fabsf(a.scale) * kLog2e, ex - 14);
 #pragma unroll
             for (int s = 0; s < kSteps; s++) {
-                float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                if (n < nrows) load_q8<BF16>(a.q, off + 16 * s, v);
+                float v[8];
+                raw[s].values(v);
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
-                    v[i] = ldexpf(a.scale < 0.0f ? -v[i] : v[i], 14 - ex);
+                    v[i] = n < nrows ? ldexpf(a.scale < 0.0f ? -v[i] : v[i], 14 - ex) : 0.0f;
                     if (s < kSteps - kQLds) {
                         qf[0][s][i] = (_Float16)v[i];
                         if constexpr (kParts == 2) qf[1][s][i] = (_Float16)(v[i] - (float)(_Float16)v[i]);
@@ -520,8 +527,8 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
                 const int64_t d = off + 4 * (x + 4 * hh);
                 if constexpr (BF16) {
                     uint2 u;
-                    u.x = (uint32_t)f32_to_bf16_rne(v[0]) | (uint32_t)f32_to_bf16_rne(v[1]) << 16;
-                    u.y = (uint32_t)f32_to_bf16_rne(v[2]) | (uint32_t)f32_to_bf16_rne(v[3]) << 16;
+                    u.x = pack_bf16(v[0], v[1]);
+                    u.y = pack_bf16(v[2], v[3]);
                     *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.o) + d) = u;
                 } else {
                     *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + d) = make_float4(v[0], v[1], v[2], v[3]);

@@ -564,8 +564,8 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_attn_split(AttnArgs a,
                     const int64_t off = ((q.first + token) * a.hq + head) * D + id;
                     if constexpr (BF16) {
                         uint2 u;
-                        u.x = (uint32_t)f32_to_bf16_rne(v[x][0]) | (uint32_t)f32_to_bf16_rne(v[x][1]) << 16;
-                        u.y = (uint32_t)f32_to_bf16_rne(v[x][2]) | (uint32_t)f32_to_bf16_rne(v[x][3]) << 16;
+                        u.x = pack_bf16(v[x][0], v[x][1]);
+                        u.y = pack_bf16(v[x][2], v[x][3]);
                         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.o) + off) = u;
                     } else {
                         *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + off) = make_float4(v[x][0], v[x][1], v[x][2], v[x][3]);
