@@ -30,6 +30,9 @@ namespace {
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 
 constexpr int kQFar = 2;
+// What the compiler may move over the steps of the second product: vector and scalar arithmetic, so that
+// one half's weights fill the matrix core's time on the other's.
+constexpr int kSchedPV = 0x406;
 constexpr float kNoPage = 1e9f;
 constexpr int kMinTiles = 4;  // tiles a workgroup is worth cutting for
 
@@ -103,12 +106,16 @@ struct Tile {
     static __device__ __forceinline__ int v_at(int row, int slot) { return row * vRow + slot * 16; }
 };
 
-template <int D, bool BF16>
+// kSmall: pages of 16 positions, else of 32 or more.
+template <int D, bool BF16, bool kSmall>
 __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_attn_prompt(AttnArgs a, int wgs) {
     using S = Shape<D, BF16>;
     constexpr int kAhead = D == 128 ? 4 : 2;  // V fragments in flight
     constexpr int T = S::T, kParts = BF16 ? 1 : 2, kSteps = D / 16, kTiles = D / 32;
     constexpr int kQLds = D == 256 && BF16 ? kQFar : 0;  // query fragments that stay in LDS
+    constexpr int kSubs = D == 256 ? 1 : 2, kWide = 32 * kSubs;   // positions of a softmax step: registers
+    constexpr int kSpan = kSmall ? 16 : 32;                       // positions that surely share a page
+    constexpr int kScales = kWide / kSpan, kOf = kSpan / 2;       // pages of a step; a lane's scores of one
     constexpr int kItems = 512 / S::kThreads;  // staging items of a thread: 256 of keys, 256 of values
     using L8 = Tile<D>;
     __shared__ __attribute__((aligned(16))) char s_k[2][L8::kBytes], s_v[2][L8::vBytes];
@@ -346,30 +353,39 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
                 for (int i = 0; i < kItems; i++) page[i] = tile + 2 < end ? find_page(tile + 2, i) : -1;
             }
 #pragma unroll 1
-            for (int sub = 0; sub < T / 32; sub++) {
-                const int p0 = tile * T + 32 * sub;
-                if (p0 >= any_hi || p0 + 32 <= any_lo) continue;  // uniform over the wave
-                const float4 sc[2] = {s_sc[buf][2 * sub], s_sc[buf][2 * sub + 1]};
+            for (int step = 0; step < T / kWide; step++) {
+                const int p0 = tile * T + kWide * step;
+                if (p0 >= any_hi || p0 + kWide <= any_lo) continue;  // uniform over the wave
+                float4 sc[kScales];
+#pragma unroll
+                for (int u = 0; u < kScales; u++) sc[u] = s_sc[buf][step * (kWide / 16) + u * (kSpan / 16)];
                 const int ln = fresh(lane);
-                const char *kp = s_k[buf] + L8::k_at(32 * sub + (ln & 31), ln >> 5), *vp = s_v[buf] + L8::v_at(ln & 31, 4 * sub + (ln >> 5));
-                auto v_frag = [&](int x) {  // fragment x: values 32 (x / 2) .., group x % 2
-                    return *reinterpret_cast<const half8_t *>(vp + L8::v_at(32 * (x >> 1), 2 * (x & 1)));
+                const char *kp = s_k[buf] + L8::k_at(kWide * step + (ln & 31), ln >> 5);
+                const char *vp = s_v[buf] + L8::v_at(ln & 31, 2 * (kWide / 16) * step + (ln >> 5));
+                auto k_frag = [&](int x) {  // step x % kSteps of positions 32 (x / kSteps) ..
+                    return *reinterpret_cast<const half8_t *>(kp + L8::k_at(32 * (x / kSteps), 0) + 16 * (x % kSteps));
                 };
-                floatx16 s = floatx16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+                auto v_frag = [&](int x) {  // values 32 (x % kTiles) .., positions 16 (x / kTiles) ..
+                    return *reinterpret_cast<const half8_t *>(vp + L8::v_at(32 * (x % kTiles), 2 * (x / kTiles)));
+                };
+                floatx16 s[kSubs];
+#pragma unroll
+                for (int y = 0; y < kSubs; y++) s[y] = floatx16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
                 half8_t kf[kAhead];
 #pragma unroll
-                for (int x = 0; x < kAhead; x++) kf[x] = *reinterpret_cast<const half8_t *>(kp + 16 * x);
+                for (int x = 0; x < kAhead; x++) kf[x] = k_frag(x);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int i = 0; i < kSteps; i++) {
-                    const half8_t k = kf[i % kAhead];
-                    if (i + kAhead < kSteps) kf[i % kAhead] = *reinterpret_cast<const half8_t *>(kp + 16 * (i + kAhead));
+                for (int x = 0; x < kSubs * kSteps; x++) {
+                    const half8_t k = kf[x % kAhead];
+                    if (x + kAhead < kSubs * kSteps) kf[x % kAhead] = k_frag(x + kAhead);
+                    const int i = x % kSteps, y = x / kSteps;
                     if (i >= kSteps - kQLds) {
                         const half8_t qx = *reinterpret_cast<const half8_t *>(s_q + (i - (kSteps - kQLds)) * S::kThreads * 16 + tid * 16);
-                        s = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, qx, s, 0, 0, 0);
+                        s[y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, qx, s[y], 0, 0, 0);
                     } else {
 #pragma unroll
-                        for (int pt = 0; pt < kParts; pt++) s = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, qf[pt][i < kSteps - kQLds ? i : 0], s, 0, 0, 0);
+                        for (int pt = 0; pt < kParts; pt++) s[y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, qf[pt][i < kSteps - kQLds ? i : 0], s[y], 0, 0, 0);
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -377,70 +393,41 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
 #pragma unroll
                 for (int x = 0; x < kAhead; x++) vf[x] = v_frag(x);
                 __builtin_amdgcn_sched_barrier(0);
-                // the two groups of 16 positions: s[0..7], s[8..15]
-                if (!(p0 >= all_lo && p0 + 32 <= all_hi && fmaxf(sc[0].w, sc[1].w) < kNoPage)) {
-                    const int to = hi - p0 - 4 * (ln >> 5), from = a.window ? to - (int)a.window : -p0 - 32;
+                // scores of one page are s[y][kOf v] .. of it: kOf of them in a lane
+                float worst = sc[0].w;
 #pragma unroll
-                    for (int j = 0; j < 16; j++) {
+                for (int u = 1; u < kScales; u++) worst = fmaxf(worst, sc[u].w);
+                if (!(p0 >= all_lo && p0 + kWide <= all_hi && worst < kNoPage)) {
+                    const int to = hi - p0 - 4 * (ln >> 5), from = a.window ? to - (int)a.window : -p0 - kWide;
+#pragma unroll
+                    for (int j = 0; j < 16 * kSubs; j++) {
                         const int t = 8 * (j >> 2) + (j & 3);
-                        const bool see = (t >= from) & (t < to) & (sc[j >> 3].w < kNoPage);
-                        s[j] = see ? s[j] : -INFINITY;
+                        const bool see = (t >= from) & (t < to) & (sc[j / kOf].w < kNoPage);
+                        s[j >> 4][j & 15] = see ? s[j >> 4][j & 15] : -INFINITY;
                     }
                 }
-                float f[2], top[2], e[2];
+                float f[kScales], top[kScales], e[kScales], mn = m;
 #pragma unroll
-                for (int u = 0; u < 2; u++) {
-                    float x = fmaxf(fmaxf(s[8 * u], s[8 * u + 1]), s[8 * u + 2]);
-                    x = fmaxf(fmaxf(x, s[8 * u + 3]), s[8 * u + 4]);
-                    x = fmaxf(fmaxf(x, s[8 * u + 5]), fmaxf(s[8 * u + 6], s[8 * u + 7]));
+                for (int u = 0; u < kScales; u++) {
+                    float x = s[u * kOf >> 4][u * kOf & 15];
+#pragma unroll
+                    for (int j = 1; j < kOf; j++) x = fmaxf(x, s[(u * kOf + j) >> 4][(u * kOf + j) & 15]);
                     x = max_xor32(x);
                     // a masked score is -inf whatever the page's scale holds
                     f[u] = fmaxf(fac * sc[u].x, 0x1p-126f);
                     top[u] = ceilf(x * f[u]);
                     e[u] = x == -INFINITY ? (float)kZeroExp : sc[u].w;
+                    mn = fmaxf(mn, top[u]);
                 }
-                const float mn = fmaxf(m, fmaxf(top[0], top[1]));
                 const float down = m - mn;
                 // E grows by more than it has to, so that it seldom does; not where the products are
                 // wanted to fp32's precision, 2^-25 of the largest then
-                const float need = fmaxf((top[0] - mn) + e[0], (top[1] - mn) + e[1]);
+                float need = (top[0] - mn) + e[0];
+#pragma unroll
+                for (int u = 1; u < kScales; u++) need = fmaxf(need, (top[u] - mn) + e[u]);
                 const float En = need > E + down ? need + (BF16 ? 4.0f : 0.0f) : E + down;
                 const float turn = down + (E - En);
                 L *= pow2_down(down);
-                half8_t pf[2][kParts];
-                if constexpr (BF16) {
-                    const half2_t most = {(_Float16)32768.0f, (_Float16)32768.0f};
-#pragma unroll
-                    for (int u = 0; u < 2; u++) {
-                        // a page whose values are not seen may hold any scale
-                        const float lw = e[u] > (float)kZeroExp ? fmaxf(sc[u].z + ((float)kProbExp - En), -60.0f) : -60.0f;
-                        const float c = lw - mn;
-                        float sum = 0.0f;
-                        uint32_t r[4];
-#pragma unroll
-                        for (int j = 0; j < 8; j += 2) {
-                            const float p0x = __builtin_amdgcn_exp2f(fmaf(s[8 * u + j], f[u], c));
-                            const float p1x = __builtin_amdgcn_exp2f(fmaf(s[8 * u + j + 1], f[u], c));
-                            sum += p0x + p1x;
-                            r[j / 2] = __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(half2_t, pack_half(p0x, p1x)), most));
-                        }
-                        pf[u][0] = __builtin_bit_cast(half8_t, make_uint4(r[0], r[1], r[2], r[3]));
-                        L = fmaf(sum, __builtin_amdgcn_exp2f(-lw), L);
-                    }
-                } else {
-#pragma unroll
-                    for (int u = 0; u < 2; u++) {
-                        const float w = e[u] > (float)kZeroExp ? fminf(ldexpf(sc[u].y, (int)((float)kProbExp - En)), 0x1p100f) : 0.0f;
-#pragma unroll
-                        for (int j = 0; j < 8; j++) {
-                            const float p = __builtin_amdgcn_exp2f(fmaf(s[8 * u + j], f[u], -mn));
-                            L += p;
-                            const float x = fminf(p * w, 32768.0f);
-                            pf[u][0][j] = (_Float16)x;
-                            pf[u][kParts - 1][j] = (_Float16)(x - (float)(_Float16)x);
-                        }
-                    }
-                }
                 if (__any(turn < 0.0f)) {
                     const float x = pow2_down(turn);
 #pragma unroll
@@ -448,15 +435,56 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
                 }
                 m = mn;
                 E = En;
-                __builtin_amdgcn_sched_barrier(0);
+                half8_t pf[2 * kSubs][kParts];  // positions 16 x .. of the step
+                auto weights = [&](int u) {     // of page u of the step
+                    uint32_t r[kOf / 2];
+                    float sum = 0.0f;
+                    if constexpr (BF16) {
+                        const half2_t most = {(_Float16)32768.0f, (_Float16)32768.0f};
+                        // a page whose values are not seen may hold any scale
+                        const float lw = e[u] > (float)kZeroExp ? fmaxf(sc[u].z + ((float)kProbExp - En), -60.0f) : -60.0f;
+                        const float c = lw - mn;
 #pragma unroll
-                for (int x = 0; x < 2 * kTiles; x++) {
+                        for (int j = 0; j < kOf; j += 2) {
+                            const int k = u * kOf + j;
+                            const float p0x = __builtin_amdgcn_exp2f(fmaf(s[k >> 4][k & 15], f[u], c));
+                            const float p1x = __builtin_amdgcn_exp2f(fmaf(s[k >> 4][(k & 15) + 1], f[u], c));
+                            sum += p0x + p1x;
+                            r[j / 2] = __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(half2_t, pack_half(p0x, p1x)), most));
+                        }
+                        L = fmaf(sum, __builtin_amdgcn_exp2f(-lw), L);
+#pragma unroll
+                        for (int x = 0; x < kOf / 8; x++)
+                            pf[u * (kOf / 8) + x][0] = __builtin_bit_cast(half8_t, make_uint4(r[4 * x], r[4 * x + 1], r[4 * x + 2], r[4 * x + 3]));
+                    } else {
+                        const float w = e[u] > (float)kZeroExp ? fminf(ldexpf(sc[u].y, (int)((float)kProbExp - En)), 0x1p100f) : 0.0f;
+#pragma unroll
+                        for (int j = 0; j < kOf; j++) {
+                            const int k = u * kOf + j;
+                            const float p = __builtin_amdgcn_exp2f(fmaf(s[k >> 4][k & 15], f[u], -mn));
+                            sum += p;
+                            const float x = fminf(p * w, 32768.0f);
+                            pf[k >> 3][0][k & 7] = (_Float16)x;
+                            pf[k >> 3][kParts - 1][k & 7] = (_Float16)(x - (float)(_Float16)x);
+                        }
+                        L += sum;
+                    }
+                };
+#pragma unroll
+                for (int u = 0; u < kScales / kSubs; u++) weights(u);
+                __builtin_amdgcn_sched_barrier(kSchedPV);
+#pragma unroll
+                for (int x = 0; x < 2 * kSubs * kTiles; x++) {
+                    if (kSubs == 2 && x == 2 * kTiles) {
+#pragma unroll
+                        for (int u = kScales / kSubs; u < kScales; u++) weights(u);
+                    }
                     const half8_t v = vf[x % kAhead];
-                    if (x + kAhead < 2 * kTiles) vf[x % kAhead] = v_frag(x + kAhead);
+                    if (x + kAhead < 2 * kSubs * kTiles) vf[x % kAhead] = v_frag(x + kAhead);
 #pragma unroll
                     for (int pt = 0; pt < kParts; pt++)
-                        o[x >> 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, pf[x & 1][pt], o[x >> 1], 0, 0, 0);
-                    __builtin_amdgcn_sched_barrier(0);
+                        o[x % kTiles] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, pf[x / kTiles][pt], o[x % kTiles], 0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(kSchedPV);
                 }
             }
             if (tile + 1 < end) store(buf ^ 1);
@@ -541,7 +569,8 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
 
 template <int D, bool BF16>
 hipError_t launch_t(const AttnArgs &a, int num_cu, hipStream_t stream) {
-    k_attn_prompt<D, BF16><<<num_cu, Shape<D, BF16>::kThreads, 0, stream>>>(a, num_cu);
+    if (a.c.page_size == 16) k_attn_prompt<D, BF16, true><<<num_cu, Shape<D, BF16>::kThreads, 0, stream>>>(a, num_cu);
+    else k_attn_prompt<D, BF16, false><<<num_cu, Shape<D, BF16>::kThreads, 0, stream>>>(a, num_cu);
     return hipGetLastError();
 }
 
