@@ -170,6 +170,34 @@ __device__ __forceinline__ floatx4 get_shared4(__amdgpu_buffer_rsrc_t r, int off
     return __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 16));
 }
 
+// How the line of tiles is cut.  A unit lies on it with `over` places in front of its tiles, what starting
+// and joining it costs, and workgroup w's part begins at place w line / used.  A beginning among a
+// unit's first `over` places is moved to the unit's, one less than `tail` places before its end
+// to its end: what is left inside a unit is a cut, at the tile that lies there.
+struct Line {
+    int64_t length, used;
+    int over, tail;
+    __device__ __forceinline__ int64_t begin(int64_t w) const { return div64(w * length, used); }
+    // this part [at, t1) of the unit of `tiles` tiles at u0, which begins at or before `at`: its tiles
+    // from .. to - 1; false where it has none
+    __device__ __forceinline__ bool part(int64_t at, int64_t t1, int64_t u0, int64_t u1, int tiles, int &from, int &to) const {
+        from = 0;
+        to = tiles;
+        if (at > u0 + over) {
+            if (at > u1 - tail) return false;
+            from = (int)(at - u0 - over);
+        }
+        if (t1 < u1) {
+            if (t1 <= u0 + over) return false;
+            if (t1 <= u1 - tail && t1 - u0 - over < tiles) to = (int)(t1 - u0 - over);
+        }
+        return true;
+    }
+    // the workgroups that have pieces of the unit [u0, u1)
+    __device__ __forceinline__ int64_t first(int64_t u0) const { return div64((u0 + over + 1) * used + length - 1, length) - 1; }
+    __device__ __forceinline__ int64_t last(int64_t u1) const { return div64((u1 - tail + 1) * used - 1, length); }
+};
+
 // A running softmax: maximum m, exponent E of the weighted sum, sum L of the probabilities.  Joining
 // two of them returns the factors for their weighted sums.
 struct State {

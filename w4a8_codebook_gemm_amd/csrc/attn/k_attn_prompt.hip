@@ -44,6 +44,8 @@ struct Shape {
     static constexpr int RB = 32 * kWaves;
     static constexpr int T = 8192 / D;       // positions of a tile
     static constexpr int kGroups = T / 16;
+    // see Line: a unit's start and end cost some 7 us, a tile 2 (D 256: 1.3)
+    static constexpr int kOver = D == 256 ? 5 : 3, kTail = D == 256 ? 3 : 2;
     static constexpr int kRegs = D / 2;      // floats of O^T in a lane
     static constexpr int kWaveRecord = 64 * (kRegs + 4);    // a wave's piece: O^T, then m, E, L
     static constexpr int kRecord = kWaves * kWaveRecord;
@@ -68,7 +70,7 @@ __device__ __forceinline__ int64_t blocks_of(const AttnArgs &a, const Seq &q) {
     return div64((int64_t)q.n * a.group + Shape<D, BF16>::RB - 1, Shape<D, BF16>::RB);
 }
 
-// Tiles of sequence b0 + lane on the line.  Called by whole waves: sequences of many blocks are
+// Places of sequence b0 + lane on the line.  Called by whole waves: sequences of many blocks are
 // summed by all lanes together.
 template <int D, bool BF16>
 __device__ __forceinline__ int64_t seq_tiles(const AttnArgs &a, int64_t b0, int lane) {
@@ -77,13 +79,13 @@ __device__ __forceinline__ int64_t seq_tiles(const AttnArgs &a, int64_t b0, int 
     const int64_t blocks = blocks_of<D, BF16>(a, q);
     int64_t tiles = 0;
     int x;
-    for (int64_t i = 0; i < (blocks <= 4 ? blocks : 0); i++) tiles += block_tiles<D, BF16>(a, q, i, x);
+    for (int64_t i = 0; i < (blocks <= 4 ? blocks : 0); i++) tiles += block_tiles<D, BF16>(a, q, i, x) + Shape<D, BF16>::kOver;
     for (uint64_t many = __ballot(blocks > 4); many; many &= many - 1) {
         const int src = __ffsll((unsigned long long)many) - 1;
         const Seq r = {0, lane_value(q.n, src), lane_value(q.len, src), lane_value(q.pos0, src)};
         const int64_t rb = blocks_of<D, BF16>(a, r);
         int64_t sum = 0;
-        for (int64_t i = lane; i < rb; i += 64) sum += block_tiles<D, BF16>(a, r, i, x);
+        for (int64_t i = lane; i < rb; i += 64) sum += block_tiles<D, BF16>(a, r, i, x) + Shape<D, BF16>::kOver;
         sum = lane_value(scan64(sum), 63);
         if (lane == src) tiles = sum;
     }
@@ -144,9 +146,10 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
     int64_t w = blockIdx.x;
     if (used == wgs && wgs % 8 == 0) w = w % 8 * (wgs / 8) + w / 8;
     if (w >= used) return;
-    const int64_t t0 = div64(w * line, used), t1 = div64((w + 1) * line, used);
+    const Line cut{line, used, S::kOver, S::kTail};
+    const int64_t t1 = cut.begin(w + 1);
 
-    for (int64_t at = t0; at < t1;) {
+    for (int64_t at = cut.begin(w); at < t1;) {
         // the sequence, cache head and row block that tile `at` is in
         int64_t base = 0, b = 0, per_head = 0;
         for (int64_t b0 = 0; b0 < a.s.B; b0 += 64) {
@@ -170,10 +173,11 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
         for (int64_t r = 0; r < blocks; r += 64) {
             int f = 0, c = 0;
             if (r + lane < blocks) c = block_tiles<D, BF16>(a, q, r + lane, f);
-            const int64_t incl = scan64(c), sum = lane_value(incl, 63);
+            const int64_t place = r + lane < blocks ? c + S::kOver : 0;
+            const int64_t incl = scan64(place), sum = lane_value(incl, 63);
             if (at < unit0 + sum) {
                 const int src = __ffsll((unsigned long long)__ballot(at - unit0 < incl)) - 1;
-                unit0 += lane_value(incl - c, src);
+                unit0 += lane_value(incl - place, src);
                 rb = r + src;
                 first_tile = lane_value(f, src);
                 tiles = lane_value(c, src);
@@ -181,8 +185,12 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
             }
             unit0 += sum;
         }
-        const int tile0 = (int)(at - unit0);
-        const int take = (int)(tiles - tile0 < t1 - at ? tiles - tile0 : t1 - at);
+        const int64_t unit1 = unit0 + S::kOver + tiles;
+        int tile0, tile1;
+        if (!cut.part(at, t1, unit0, unit1, tiles, tile0, tile1)) {
+            at = unit1;
+            continue;
+        }
 
         // this wave's rows
         const int64_t rows = (int64_t)q.n * a.group, r0 = rb * S::RB + 32 * wave;
@@ -337,7 +345,7 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
             }
         };
 
-        const int begin = first_tile + tile0, end = begin + take;
+        const int begin = first_tile + tile0, end = first_tile + tile1;
 #pragma unroll
         for (int i = 0; i < kItems; i++) page[i] = find_page(begin, i);
         load(begin);
@@ -493,8 +501,8 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
         L += __shfl_xor(L, 32);
 
         bool write = true;
-        if (take < tiles) {
-            const int64_t w_first = div64((unit0 + 1) * used - 1, line), w_end = div64((unit0 + tiles) * used - 1, line);
+        if (tile1 - tile0 < tiles) {
+            const int64_t w_first = cut.first(unit0), w_end = cut.last(unit1);
             auto slot = [&](unsigned x) {
                 return shared_piece(pieces + (2 * (w_first + x) + (x == 0 ? 1 : 0)) * S::kRecord + wave * S::kWaveRecord, 4 * S::kWaveRecord);
             };
@@ -563,7 +571,7 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
                 }
             }
         }
-        at += take;
+        at = unit1;
     }
 }
 

@@ -70,10 +70,12 @@ __device__ __forceinline__ Work seq_work(const AttnArgs &a, int64_t b) {
     return w;
 }
 
-// A unit's tiles on the line: where workgroups are many, as a whole number of their shares.
-__device__ __forceinline__ int on_line(int tiles, int share) { return share ? (tiles + share - 1) / share * share : tiles; }
-
 constexpr int kMaxShare = 4 * kWaves;
+constexpr int kOver = 8, kTail = 3;  // see Line: a unit's start and end cost some 8 us, four tiles 4
+
+// A unit's places on the line: its tiles and what it costs beside them, or where workgroups are many a
+// whole number of their shares.
+__device__ __forceinline__ int on_line(int tiles, int share) { return share ? (tiles + share - 1) / share * share : tiles + kOver; }
 
 template <int D, int NB>
 struct Layout {
@@ -129,9 +131,10 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_attn_split(AttnArgs a,
     const int64_t used = share ? div64(line, share) : wgs;
     const int64_t w = blockIdx.x;
     if (w >= used) return;
-    const int64_t t0 = share ? w * share : div64(w * line, used), t1 = share ? t0 + share : div64((w + 1) * line, used);
+    const Line cut{line, used, share ? 0 : kOver, share ? 1 : kTail};
+    const int64_t t1 = cut.begin(w + 1);
 
-    for (int64_t at = t0; at < t1;) {
+    for (int64_t at = cut.begin(w); at < t1;) {
         // the sequence and unit that tile `at` is in
         int64_t base = 0, b = 0;
         int lo_tile = 0, tiles = 1;
@@ -152,8 +155,12 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_attn_split(AttnArgs a,
         const int length = on_line(tiles, share);
         const int64_t unit = div64(at - base, length);
         const int64_t unit0 = base + unit * length;         // the unit's first tile on the line
-        const int tile0 = (int)(at - unit0);
-        const int take = (int)(tiles - tile0 < t1 - at ? tiles - tile0 : t1 - at);
+        const int64_t unit1 = unit0 + length;
+        int tile0, tile1;
+        if (!cut.part(at, t1, unit0, unit1, tiles, tile0, tile1)) {
+            at = unit1;
+            continue;
+        }
         const int64_t rblock = div64(unit, a.c.kv_heads);
         const int h = (int)(unit - rblock * a.c.kv_heads);
 
@@ -179,7 +186,7 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_attn_split(AttnArgs a,
             sees(a, q, t_last, all_lo, any_hi);
         }
 
-        const int end = lo_tile + tile0 + take;
+        const int end = lo_tile + tile1;
         int first = lo_tile + tile0 + wave;
         if (first < any_lo / T) first += (any_lo / T - first + kWaves - 1) / kWaves * kWaves;
         const int stop = end < (any_hi + T - 1) / T ? end : (any_hi + T - 1) / T;
@@ -507,8 +514,8 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_attn_split(AttnArgs a,
             __syncthreads();
         }
         bool write = true;
-        if (take < tiles) {
-            const int64_t w_first = div64((unit0 + 1) * used - 1, line), w_end = div64((unit0 + length) * used - 1, line);
+        if (tile1 - tile0 < tiles) {
+            const int64_t w_first = cut.first(unit0), w_end = cut.last(unit1);
             auto slot = [&](unsigned x) { return shared_piece(pieces + (2 * (w_first + x) + (x == 0 ? 1 : 0)) * Lay::kRecord, 4 * Lay::kRecord); };
             write = join_pieces<kRadix>(counters, w_first, w, w_end, &s_flag, [&](unsigned y) {
                 const __amdgpu_buffer_rsrc_t p = slot(y);
@@ -573,7 +580,7 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_attn_split(AttnArgs a,
                 }
             }
         }
-        at = unit0 + length;
+        at = unit1;
     }
 }
 
