@@ -44,25 +44,6 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
     return __builtin_bit_cast(uint32_t, h);
 }
 
-// Eight consecutive query values.
-template <bool BF16>
-__device__ __forceinline__ void load_q8(const void *q, int64_t off, float v[8]) {
-    if constexpr (BF16) {
-        const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(q) + off);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    } else {
-        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(q) + off);
-        const float4 a = p[0], b = p[1];
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    }
-}
-
 // 2^x for a whole-numbered x <= 0 of any size (0 below fp32's range).
 __device__ __forceinline__ float pow2_down(float x) { return __builtin_amdgcn_exp2f(x); }
 

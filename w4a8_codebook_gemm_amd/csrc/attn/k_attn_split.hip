@@ -71,11 +71,15 @@ __device__ __forceinline__ Work seq_work(const AttnArgs &a, int64_t b) {
 }
 
 constexpr int kMaxShare = 4 * kWaves;
-constexpr int kOver = 8, kTail = 3;  // see Line: a unit's start and end cost some 8 us, four tiles 4
+// See Line: a unit's start and end cost some 8 us, a workgroup's tile 1 (blocks of 16 rows) or 2.
+template <int NB>
+constexpr int kOver = NB == 2 ? 4 : 8;
+constexpr int kTail = 3;
 
 // A unit's places on the line: its tiles and what it costs beside them, or where workgroups are many a
 // whole number of their shares.
-__device__ __forceinline__ int on_line(int tiles, int share) { return share ? (tiles + share - 1) / share * share : tiles + kOver; }
+template <int NB>
+__device__ __forceinline__ int on_line(int tiles, int share) { return share ? (tiles + share - 1) / share * share : tiles + kOver<NB>; }
 
 template <int D, int NB>
 struct Layout {
@@ -114,7 +118,7 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_attn_split(AttnArgs a,
         int64_t sum = 0;
         for (int64_t b0 = 0; b0 < a.s.B; b0 += 64) {
             if (a.s.B > 64) x = seq_work<RB, T>(a, b0 + lane);
-            sum += lane_value(scan64(x.units * on_line(x.tiles, share)), 63);
+            sum += lane_value(scan64(x.units * on_line<NB>(x.tiles, share)), 63);
         }
         return sum;
     };
@@ -131,28 +135,32 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_attn_split(AttnArgs a,
     const int64_t used = share ? div64(line, share) : wgs;
     const int64_t w = blockIdx.x;
     if (w >= used) return;
-    const Line cut{line, used, share ? 0 : kOver, share ? 1 : kTail};
+    const Line cut{line, used, share ? 0 : kOver<NB>, share ? 1 : kTail};
     const int64_t t1 = cut.begin(w + 1);
 
     for (int64_t at = cut.begin(w); at < t1;) {
         // the sequence and unit that tile `at` is in
         int64_t base = 0, b = 0;
         int lo_tile = 0, tiles = 1;
+        Seq q{0, 0, 0, 0};
         for (int64_t b0 = 0; b0 < a.s.B; b0 += 64) {
             if (a.s.B > 64) x = seq_work<RB, T>(a, b0 + lane);
-            const int64_t mine = x.units * on_line(x.tiles, share), incl = scan64(mine), sum = lane_value(incl, 63);
+            const int64_t mine = x.units * on_line<NB>(x.tiles, share), incl = scan64(mine), sum = lane_value(incl, 63);
             if (at < base + sum) {
                 const int src = __ffsll((unsigned long long)__ballot(at - base < incl)) - 1;
                 b = b0 + src;
                 base += lane_value(incl - mine, src);
                 lo_tile = lane_value(x.lo, src);
                 tiles = lane_value(x.tiles, src);
+                q.first = lane_value(x.q.first, src);
+                q.n = lane_value(x.q.n, src);
+                q.len = lane_value(x.q.len, src);
+                q.pos0 = q.len - q.n;
                 break;
             }
             base += sum;
         }
-        const Seq q = load_seq(a.s, a.M, a.page_shift, b);
-        const int length = on_line(tiles, share);
+        const int length = on_line<NB>(tiles, share);
         const int64_t unit = div64(at - base, length);
         const int64_t unit0 = base + unit * length;         // the unit's first tile on the line
         const int64_t unit1 = unit0 + length;
@@ -161,25 +169,37 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_attn_split(AttnArgs a,
             at = unit1;
             continue;
         }
-        const int64_t rblock = div64(unit, a.c.kv_heads);
-        const int h = (int)(unit - rblock * a.c.kv_heads);
+        const int rblock = (int)div64(unit, a.c.kv_heads);
+        const int h = (int)(unit - (int64_t)rblock * a.c.kv_heads);
 
-        // this lane's rows
-        const int64_t rows = (int64_t)q.n * a.group;
-        const int64_t r0 = rblock * RB;
-        const int nrows = (int)(rows - r0 < RB ? rows - r0 : RB);
+        // this lane's rows; a sequence's rows are fewer than 2^31
+        const int r0 = rblock * RB;
+        const int nrows = q.n * a.group - r0 < RB ? q.n * a.group - r0 : RB;
         int lo[NB], hi[NB];
         float fac[NB];
-        auto row_at = [&](int r, int64_t &token, int &head) {  // row r < nrows of the block
-            const int64_t i = div64(r0 + r, a.group);
-            token = i;
-            head = h * a.group + (int)(r0 + r - i * a.group);
+        auto row_at = [&](int r, int &token, int &head) {  // row r < nrows of the block
+            token = (uint32_t)(r0 + r) / (uint32_t)a.group;
+            head = h * a.group + (r0 + r - token * a.group);
         };
+        // queries, all of a row's values of this lane at once, before the codes are asked for
+        RawQ<BF16> raw[NB][2 * kC];
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++) {
+            const int r = 16 * nb + n < nrows ? 16 * nb + n : nrows - 1;
+            int token, head;
+            row_at(r, token, head);
+            sees(a, q, token, lo[nb], hi[nb]);
+            if (r != 16 * nb + n) hi[nb] = 0;
+            const int64_t off = (q.first + token) * a.q_stride + head * D + 16 * g;
+#pragma unroll
+            for (int c = 0; c < kC; c++)
+#pragma unroll
+                for (int u = 0; u < 2; u++) raw[nb][2 * c + u].load(a.q, off + 64 * c + 8 * u);
+        }
         // positions that all rows of the block see, and that any does
         int all_lo, all_hi, any_lo, any_hi;
         {
-            int64_t t_first, t_last;
-            int hd;
+            int t_first, t_last, hd;
             row_at(0, t_first, hd);
             row_at(nrows - 1, t_last, hd);
             sees(a, q, t_first, any_lo, all_hi);
@@ -250,33 +270,18 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_attn_split(AttnArgs a,
             if (first + kWaves < stop) find_pages(first + kWaves);
         }
 
-        // queries as fp16, into LDS: fragment (block, part, step) as its lanes read it
+        // queries as fp16, into LDS: fragment (block, part, step) as its lanes read it; zeros behind the rows
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
-            const int r = 16 * nb + n;
-            float v[kC][2][8];
             float top = 0.0f;
-            int64_t token = 0;
-            int head = 0;
-            lo[nb] = 0;
-            hi[nb] = 0;
-            if (r < nrows) {
-                row_at(r, token, head);
-                sees(a, q, token, lo[nb], hi[nb]);
+#pragma unroll
+            for (int c = 0; c < 2 * kC; c++) {
+                float v[8];
+                raw[nb][c].values(v);
+#pragma unroll
+                for (int i = 0; i < 8; i++) top = fmaxf(top, fabsf(v[i]));
             }
-#pragma unroll
-            for (int c = 0; c < kC; c++)
-#pragma unroll
-                for (int u = 0; u < 2; u++) {
-                    if (r < nrows) {
-                        load_q8<BF16>(a.q, (q.first + token) * a.q_stride + head * D + 64 * c + 16 * g + 8 * u, v[c][u]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; i++) v[c][u][i] = 0.0f;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; i++) top = fmaxf(top, fabsf(v[c][u][i]));
-                }
+            if (16 * nb + n >= nrows) top = 0.0f;
             top = max_xor32(max_xor16(top));
             // the row's largest value at 2^13 .. 2^14: bf16 values are then exact in fp16 down
             // to 2^-28 of it (fp32 as two fp16 numbers to 2^-22 relative), below off by 2^-39
@@ -285,19 +290,19 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_attn_split(AttnArgs a,
             fac[nb] = ldexpf(fabsf(a.scale) * kLog2e, ex - 14);
             if (wave == nb) {
 #pragma unroll
-                for (int c = 0; c < kC; c++)
+                for (int c = 0; c < 2 * kC; c++) {
+                    half8_t q0, q1;
+                    float v[8];
+                    raw[nb][c].values(v);
 #pragma unroll
-                    for (int u = 0; u < 2; u++) {
-                        half8_t q0, q1;
-#pragma unroll
-                        for (int i = 0; i < 8; i++) {
-                            const float x = ldexpf(a.scale < 0.0f ? -v[c][u][i] : v[c][u][i], 14 - ex);
-                            q0[i] = (_Float16)x;
-                            q1[i] = (_Float16)(x - (float)(_Float16)x);
-                        }
-                        s_q[(nb * kParts * 2 * kC + 2 * c + u) * 64 + lane] = q0;
-                        if constexpr (kParts == 2) s_q[((nb * kParts + 1) * 2 * kC + 2 * c + u) * 64 + lane] = q1;
+                    for (int i = 0; i < 8; i++) {
+                        const float x = 16 * nb + n < nrows ? ldexpf(a.scale < 0.0f ? -v[i] : v[i], 14 - ex) : 0.0f;
+                        q0[i] = (_Float16)x;
+                        q1[i] = (_Float16)(x - (float)(_Float16)x);
                     }
+                    s_q[(nb * kParts * 2 * kC + c) * 64 + lane] = q0;
+                    if constexpr (kParts == 2) s_q[((nb * kParts + 1) * 2 * kC + c) * 64 + lane] = q1;
+                }
             }
         }
         __syncthreads();
@@ -565,8 +570,7 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_attn_split(AttnArgs a,
                     const float inv = st[x].L > 0.0f ? 1.0f / st[x].L : 0.0f;
 #pragma unroll
                     for (int i = 0; i < 4; i++) v[x][i] = ldexpf(v[x][i] * inv, (int)st[x].E + kCodeExp - kProbExp);
-                    int64_t token;
-                    int head;
+                    int token, head;
                     row_at(r, token, head);
                     const int64_t off = ((q.first + token) * a.hq + head) * D + id;
                     if constexpr (BF16) {
