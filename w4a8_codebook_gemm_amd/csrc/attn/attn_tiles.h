@@ -27,16 +27,18 @@ __device__ __forceinline__ half8_t codes_natural(uint32_t w0, uint32_t w1) {
     return __builtin_bit_cast(half8_t, make_uint4(r[0], r[1], r[2], r[3]));
 }
 
-// Byte J of two tokens' dwords (already ^ kSign4) as two fp16 numbers code * 2^-24, exact: the
-// byte code + 128 alone is the subnormal (code + 128) 2^-24.  Picking the bytes and turning
-// token rows into a fragment of consecutive tokens are the same permute.
+// Byte J of two tokens' dwords (already ^ kSign4) as two fp16 numbers code * 2^-9, exact: the
+// byte code + 128 alone is the subnormal (code + 128) 2^-24, which one packed multiply-add takes to
+// 2^15 of it less 128 * 2^-9.  Picking the bytes and turning token rows into a fragment of
+// consecutive tokens are the same permute.  (Subnormal operands themselves cost the matrix core's
+// sums precision: next to weights of a wide range 16 bits of the largest product are left, not 22.)
 template <int J>
 __device__ __forceinline__ uint32_t codes_pair(uint32_t first, uint32_t second) {
-    const half2_t bias = __builtin_bit_cast(half2_t, 0x00800080u);  // 128 * 2^-24
+    const half2_t up = {(_Float16)32768.0f, (_Float16)32768.0f}, bias = {(_Float16)-0.25f, (_Float16)-0.25f};
     const uint32_t u = __builtin_amdgcn_perm(second, first, 0x0C000C00u | (uint32_t)J | (uint32_t)(4 + J) << 16);
-    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, u) - bias);
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(half2_t, u), up, bias));
 }
-constexpr int kCodeExp = 24;   // codes_pair's values are code * 2^-kCodeExp
+constexpr int kCodeExp = 9;    // codes_pair's values are code * 2^-kCodeExp
 constexpr int kProbExp = 14;   // probabilities enter the second product as p * 2^kProbExp
 
 __device__ __forceinline__ uint32_t pack_half(float a, float b) {

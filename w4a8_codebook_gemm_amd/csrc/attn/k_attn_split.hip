@@ -16,7 +16,7 @@
 // The running maximum m and the exponent E are whole numbers: with e the exponent of a page's
 // value scale sv < 2^e, a probability enters the second product as p sv 2^(14 - E), E the
 // largest (m_page - m) + e so far, so it is below 2^14 whatever the pages' scales, and every
-// rescaling is by a power of two, exact.  o = O 2^(24 - 14 + E) / sum p.
+// rescaling is by a power of two, exact.  o = O 2^(9 - 14 + E) / sum p (codes are 2^9 less).
 //
 // Split: the tiles of all units form one line that is cut evenly over the workgroups whatever the
 // lengths are; a workgroup's waves take its tiles in turn and join in LDS.  The pieces of a unit
