@@ -78,8 +78,7 @@ constexpr int kTail = 3;
 
 // A unit's places on the line: its tiles and what it costs beside them, or where workgroups are many a
 // whole number of their shares.
-template <int NB>
-__device__ __forceinline__ int on_line(int tiles, int share) { return share ? (tiles + share - 1) / share * share : tiles + kOver<NB>; }
+__device__ __forceinline__ int on_line(int tiles, int share, int over) { return share ? (tiles + share - 1) / share * share : tiles + over; }
 
 template <int D, int NB>
 struct Layout {
@@ -114,28 +113,36 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_attn_split(AttnArgs a,
     // and joining.  While a part is not more than kMaxShare tiles, units are cut into whole shares of
     // that many tiles instead, each a workgroup's, if there are workgroups enough.
     Work x = seq_work<RB, T>(a, lane);
-    auto total = [&](int share) {
+    auto total = [&](int share, int over, int64_t &units) {
         int64_t sum = 0;
+        units = 0;
         for (int64_t b0 = 0; b0 < a.s.B; b0 += 64) {
             if (a.s.B > 64) x = seq_work<RB, T>(a, b0 + lane);
-            sum += lane_value(scan64(x.units * on_line<NB>(x.tiles, share)), 63);
+            sum += lane_value(scan64(x.units * on_line(x.tiles, share, over)), 63);
+            units += lane_value(scan64(x.units), 63);
         }
         return sum;
     };
-    int64_t line = total(0);
+    int64_t units, none;
+    int64_t line = total(0, 0, units);
     if (line == 0) return;
     int share = 0;
     for (int64_t c = div64(line + (int64_t)wgs * kWaves - 1, (int64_t)wgs * kWaves) * kWaves; c <= kMaxShare && share == 0; c += kWaves) {
-        const int64_t sum = total((int)c);
+        const int64_t sum = total((int)c, 0, none);
         if (sum <= (int64_t)wgs * c) {
             share = (int)c;
             line = sum;
         }
     }
+    // with fewer units than workgroups nearly every part is one piece and pays the same: blocks of 32 rows are
+    // then better cut evenly (16 x 8 tokens on 4k 46 us, 49 with kOver); blocks of 16 are not (32 ragged
+    // sequences 114 us evenly, 112 with kOver, 4 long ones 184 and 181)
+    const int over = share == 0 && (NB == 1 || units >= wgs) ? kOver<NB> : 0;
+    line += over * units;
     const int64_t used = share ? div64(line, share) : wgs;
     const int64_t w = blockIdx.x;
     if (w >= used) return;
-    const Line cut{line, used, share ? 0 : kOver<NB>, share ? 1 : kTail};
+    const Line cut{line, used, over, share ? 1 : kTail};
     const int64_t t1 = cut.begin(w + 1);
 
     for (int64_t at = cut.begin(w); at < t1;) {
@@ -145,7 +152,7 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_attn_split(AttnArgs a,
         Seq q{0, 0, 0, 0};
         for (int64_t b0 = 0; b0 < a.s.B; b0 += 64) {
             if (a.s.B > 64) x = seq_work<RB, T>(a, b0 + lane);
-            const int64_t mine = x.units * on_line<NB>(x.tiles, share), incl = scan64(mine), sum = lane_value(incl, 63);
+            const int64_t mine = x.units * on_line(x.tiles, share, over), incl = scan64(mine), sum = lane_value(incl, 63);
             if (at < base + sum) {
                 const int src = __ffsll((unsigned long long)__ballot(at - base < incl)) - 1;
                 b = b0 + src;
@@ -160,7 +167,7 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_attn_split(AttnArgs a,
             }
             base += sum;
         }
-        const int length = on_line<NB>(tiles, share);
+        const int length = on_line(tiles, share, over);
         const int64_t unit = div64(at - base, length);
         const int64_t unit0 = base + unit * length;         // the unit's first tile on the line
         const int64_t unit1 = unit0 + length;
