@@ -151,6 +151,9 @@ APPEND = [
     ([300, 300], [300, 333], 2, 128, 256, F32, 500.0),
     ([5, 9], [3, 9], 1, 64, 16, F32, 1.0),          # a length shorter than its new tokens
     ([1, 1], [1000, 20], 2, 128, 128, BF, 1e4),      # page past the table's width: held to it
+    ([0] * 59 + [200], [7] * 59 + [230], 3, 256, 256, F32, 2.0),  # few tokens a sequence, all of them one's
+    ([0] * 149 + [290, 290], [0] * 149 + [290, 320], 1, 128, 256, BF, 2.0),
+    ([2] * 130, [2 + i % 40 for i in range(130)], 5, 64, 64, BF, 1.0),
 ]
 
 

@@ -1,15 +1,23 @@
 // Append of keys and values into the int8 paged cache.
 //
-// A job is one page of one sequence that gets new tokens; a workgroup does one job for one
+// A job is one page of one sequence that gets new tokens; a team of threads does one job for one
 // head of keys or of values: the largest magnitude of its tokens, the page's scale, the
-// earlier codes where the scale grew, the new codes.  HBM bound (2 or 4 bytes read and one
-// written a value) with long prompts, latency bound with single tokens.  A row of
-// head_dim values is held by head_dim / 16 lanes, 16 consecutive values a lane: 32 or 64
-// bytes read, one 16-byte store.  Up to 4 passes over the job's rows (64 rows at head_dim 256,
-// 256 at 64) stay in registers between the maximum and the codes; longer jobs read their rows
-// twice, the second time from L2.
+// earlier codes where the scale grew, the new codes.  A row of head_dim values is held by
+// head_dim / 16 lanes, 16 consecutive values a lane: 32 or 64 bytes read, one 16-byte store.
+// Up to 4 passes over the job's rows stay in registers between the maximum and the codes, as they
+// lie in memory; longer jobs read their rows twice, the second time from L2.
 //
-// Which page a workgroup has is found on the device, where the lengths are: every wave runs
+// The team is one wave where that holds a page in its 4 passes (pages of 4096 / head_dim tokens or fewer) or
+// where a sequence has 4 new tokens on average or fewer, and the workgroup elsewhere.  A workgroup a page was
+// 16.7 us for 256 sequences x 1 token (8 heads of 128) and 59.5 us for 16384 tokens in pages of 16, mostly
+// workgroups starting; a wave a page is 7.8 us and 30.2 us.  Pages of 64 at head_dim 128 take 15.5 us for
+// 8 x 1024 tokens with a workgroup, and would read every row twice with a wave.
+//
+// Bound by HBM with long prompts: 2 or 4 bytes read and one written a value, 3.3 TB/s over a launch of 50 to
+// 100 MB.  Bound by latency with single tokens: 4.5 us for 61 sequences, of them the chain of reads from the
+// sequence to its page, the scale and the token.
+//
+// Which page a team has is found on the device, where the lengths are: every wave runs
 // the sequences' page counts through a prefix sum, 64 at a time, until its job's is reached.
 #include "attn_internal.h"
 
@@ -65,15 +73,52 @@ __device__ __forceinline__ Job find_job(const AppendArgs &a, int64_t job) {
     return out;
 }
 
-template <int D, bool BF16>
+// 16 values of a row as they lie in memory: a bf16 pair stays one register.
+template <bool BF16>
+struct Raw {
+    static constexpr int kWords = BF16 ? 8 : 16;
+    uint4 w[kWords / 4];
+    __device__ __forceinline__ void load(const void *x, int64_t off) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(x) + off * (BF16 ? 2 : 4));
+#pragma unroll
+        for (int i = 0; i < kWords / 4; i++) w[i] = p[i];
+    }
+    __device__ __forceinline__ void values(float v[16]) const {
+#pragma unroll
+        for (int i = 0; i < kWords / 4; i++) {
+            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                if constexpr (BF16) {
+                    v[8 * i + 2 * j] = __uint_as_float(u[j] << 16);
+                    v[8 * i + 2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+                } else {
+                    v[4 * i + j] = __uint_as_float(u[j]);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ float top() const {
+        float v[16], t = 0.0f;
+        values(v);
+#pragma unroll
+        for (int i = 0; i < 16; i++) t = fmaxf(t, fabsf(v[i]));
+        return t;
+    }
+};
+
+// TEAM threads (one wave, or the workgroup) have one page, head and side.
+template <int D, bool BF16, int TEAM>
 __global__ __launch_bounds__(kThreads) void k_kv_append(AppendArgs a) {
     constexpr int kLanes = D / 16;
-    constexpr int kRows = kThreads / kLanes;  // rows a pass
+    constexpr int kRows = TEAM / kLanes;  // rows a pass
     __shared__ float s_max[kThreads / 64];
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x % TEAM;
+    const int side = (int)((blockIdx.y * blockDim.x + threadIdx.x) / TEAM);
+    if (side >= 2 * a.c.kv_heads) return;  // uniform over the team, as the next is
     const Job job = find_job(a, blockIdx.x);
-    if (job.page < 0) return;  // uniform over the workgroup
-    const int head = blockIdx.y, kv = blockIdx.z;
+    if (job.page < 0) return;
+    const int head = side >> 1, kv = side & 1;
     const int64_t ph = (int64_t)job.page * a.c.kv_heads + head;
     float *scale = (kv ? a.c.v_scale : a.c.k_scale) + ph;
     int8_t *codes = (kv ? a.c.v : a.c.k) + ph * a.c.page_size * D;
@@ -81,28 +126,28 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(AppendArgs a) {
     const int r0 = tid / kLanes;
     const float before = job.slot ? *scale : 0.0f;
 
-    float keep[kKeep][16];
-    float top = 0.0f;
+    Raw<BF16> keep[kKeep];
 #pragma unroll
     for (int p = 0; p < kKeep; p++) {
         const int r = r0 + p * kRows;
-        if (r < job.rows) {
-            load16<BF16>(a.x[kv], x0 + r * a.stride[kv], keep[p]);
-#pragma unroll
-            for (int i = 0; i < 16; i++) top = fmaxf(top, fabsf(keep[p][i]));
-        }
+        keep[p] = Raw<BF16>{};
+        if (r < job.rows) keep[p].load(a.x[kv], x0 + r * a.stride[kv]);
     }
-    for (int r = r0 + kKeep * kRows; r < job.rows; r += kRows) {
-        float v[16];
-        load16<BF16>(a.x[kv], x0 + r * a.stride[kv], v);
+    float top = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; i++) top = fmaxf(top, fabsf(v[i]));
+    for (int p = 0; p < kKeep; p++) top = fmaxf(top, keep[p].top());
+    for (int r = r0 + kKeep * kRows; r < job.rows; r += kRows) {
+        Raw<BF16> x;
+        x.load(a.x[kv], x0 + r * a.stride[kv]);
+        top = fmaxf(top, x.top());
     }
 #pragma unroll
     for (int s = 1; s < 64; s <<= 1) top = fmaxf(top, __shfl_xor(top, s));
-    if ((tid & 63) == 0) s_max[tid >> 6] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+    if constexpr (TEAM > 64) {
+        if ((tid & 63) == 0) s_max[tid >> 6] = top;
+        __syncthreads();
+        top = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+    }
 
     float s = top / 127.0f;
     if (before > 0.0f) {
@@ -115,7 +160,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(AppendArgs a) {
         s = ldexpf(before, j);
         if (j > 0) {
             const float down = j < 20 ? ldexpf(1.0f, -j) : 0.0f;  // |code| 2^-8 < 1/2 already
-            for (int i = tid; i < job.slot * (D / 4); i += kThreads) {
+            for (int i = tid; i < job.slot * (D / 4); i += TEAM) {
                 const uint32_t w = reinterpret_cast<const uint32_t *>(codes)[i];
                 uint32_t u = 0;
 #pragma unroll
@@ -128,20 +173,40 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(AppendArgs a) {
     // 1 / s is read by the corrected quotient only for scales that are far from underflow
     const float inv = 1.0f / s;
     int8_t *y = codes + (int64_t)job.slot * D + 16 * (tid % kLanes);
-    auto put = [&](int r, const float v[16]) {
+    auto put = [&](int r, const Raw<BF16> &x) {
+        float v[16];
+        x.values(v);
         *reinterpret_cast<uint4 *>(y + r * D) = s > 0.0f ? quant16_auto(v, s, inv) : make_uint4(0, 0, 0, 0);
     };
 #pragma unroll
     for (int p = 0; p < kKeep; p++) {
         const int r = r0 + p * kRows;
+        if constexpr (BF16) {
+            // widened anew: the widened values kept from above would halve the waves a SIMD holds
+#pragma unroll
+            for (int i = 0; i < Raw<BF16>::kWords / 4; i++)
+                asm("" : "+v"(keep[p].w[i].x), "+v"(keep[p].w[i].y), "+v"(keep[p].w[i].z), "+v"(keep[p].w[i].w));
+        }
         if (r < job.rows) put(r, keep[p]);
     }
     for (int r = r0 + kKeep * kRows; r < job.rows; r += kRows) {
-        float v[16];
-        load16<BF16>(a.x[kv], x0 + r * a.stride[kv], v);
-        put(r, v);
+        Raw<BF16> x;
+        x.load(a.x[kv], x0 + r * a.stride[kv]);
+        put(r, x);
     }
-    if (tid == 0) *scale = s;  // every thread's read of it is before the barrier above
+    if (tid == 0) *scale = s;  // the team has read it: its value went into s
+}
+
+template <int D, int TEAM>
+hipError_t launch_team(const AppendArgs &a, int bf16, int64_t jobs, hipStream_t stream) {
+    const int sides = 2 * a.c.kv_heads;
+    const int threads = sides * TEAM < kThreads ? sides * TEAM : kThreads;
+    const dim3 grid((unsigned)jobs, (unsigned)((sides * TEAM + threads - 1) / threads));
+    if (bf16)
+        k_kv_append<D, true, TEAM><<<grid, threads, 0, stream>>>(a);
+    else
+        k_kv_append<D, false, TEAM><<<grid, threads, 0, stream>>>(a);
+    return hipGetLastError();
 }
 
 template <int D>
@@ -149,12 +214,8 @@ hipError_t launch_d(const AppendArgs &a, int bf16, hipStream_t stream) {
     // pages a call can touch: a sequence's first and last may be partial
     int64_t jobs = (a.M >> a.page_shift) + 2 * a.s.B;
     if (jobs > a.M) jobs = a.M;
-    const dim3 grid((unsigned)jobs, (unsigned)a.c.kv_heads, 2);
-    if (bf16)
-        k_kv_append<D, true><<<grid, kThreads, 0, stream>>>(a);
-    else
-        k_kv_append<D, false><<<grid, kThreads, 0, stream>>>(a);
-    return hipGetLastError();
+    const bool one_wave = a.c.page_size <= kKeep * 1024 / D || a.M <= 4 * a.s.B;
+    return one_wave ? launch_team<D, 64>(a, bf16, jobs, stream) : launch_team<D, kThreads>(a, bf16, jobs, stream);
 }
 
 }  // namespace
