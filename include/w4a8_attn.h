@@ -59,7 +59,8 @@ typedef struct {
     int64_t head_stride;   /* elements, at least head_dim */
     int heads;             /* >= 1 */
     const float *weight;   /* [head_dim] norm weights; NULL: no norm, rotation only */
-    void *out;             /* [M][heads][head_dim], contiguous; may be x where layout and type are the same */
+    void *out;             /* [M][heads][head_dim], contiguous; may be x where layout and type are the same,
+                              and overlaps nothing else of the call */
 } w4a8_heads;
 
 /*
@@ -82,7 +83,8 @@ W4A8_API int w4a8_qk_norm_rope(const w4a8_heads *q, const w4a8_heads *k, int64_t
 /*
  * An int8 cache of keys and values in pages.  A page holds page_size consecutive tokens of
  * one sequence; for each of its heads it has the codes [page_size][head_dim] and one fp32
- * scale for keys and one for values (element = code * scale, codes -127..127).
+ * scale for keys and one for values (element = code * scale, codes -127..127; scales are finite
+ * and not negative, as the append leaves them).
  */
 typedef struct {
     int8_t *k, *v;            /* [num_pages][kv_heads][page_size][head_dim] */
@@ -119,8 +121,10 @@ typedef struct {
  *   often a page grows, an element is then off by at most one step of the final scale.
  *   (Earlier scale 0: scale = max|x| / 127.)
  *   code = clamp(rint(x / scale), -127, 127), IEEE division, ties to even; 0 where scale is 0.
- * Bit-exact and deterministic.  Slots behind the last token keep their bytes.  Two sequences
- * of one call must not append to the same page.
+ * Bit-exact and deterministic for finite values.  A NaN or an infinity leaves its page and head
+ * without a meaning until slot 0 is written again, and no other page or head.  Slots behind the last
+ * token keep their bytes.  A call must not append to a page twice,
+ * from two sequences or at two places of one.
  *
  *  k, v   [M] tokens of kv_heads * head_dim consecutive values, k_stride and v_stride elements
  *         apart (multiples of 8, at least kv_heads * head_dim), element type dtype;  1 <= M <= 2^24
@@ -140,13 +144,14 @@ W4A8_API int64_t w4a8_kv_attention_workspace_bytes(int64_t M, int64_t B, int q_h
  * over the positions t that the query at position p sees: all of the sequence (causal 0), or
  * t <= p, and with window > 0 also t > p - window.  A query that sees nothing gives 0.  Query
  * head h reads cache head h / (q_heads / kv_heads).  Rows of o that belong to no sequence are
- * left as they were.
+ * left as they were.  Where a query is not finite, or a scale of a page that it sees is negative or not
+ * finite, that row of o has no meaning; other rows, and rows that do not see the page, are not touched by it.
  *
  *  q         [M] tokens of q_heads * head_dim consecutive values, q_stride elements apart (a
  *            multiple of 8), element type dtype;  1 <= M <= 2^24, M * q_heads < 2^31
  *  q_heads   a multiple of kv_heads, at most 8192
  *  causal    0 or 1;  window  0 (none) or >= 1, causal only
- *  o         [M][q_heads][head_dim], element type dtype
+ *  o         [M][q_heads][head_dim], element type dtype; overlaps no other operand
  *  workspace device memory of w4a8_kv_attention_workspace_bytes(M, B, ...) bytes or more, zero-filled before its
  *            first use; every call that completes leaves the counters in it at zero, so one
  *            workspace serves later calls of any shape it is large enough for, one at a time:

@@ -345,6 +345,76 @@ def test_attention_extreme_scales(A, new, lens, dtype):
         check_attention(A, q, b, codes, scales, cache, scale=-0.02)
 
 
+@pytest.mark.parametrize("new,lens,D,page,window", [
+    ([3, 1], [130, 40], 128, 16, 0),
+    ([3, 1], [130, 140], 256, 32, 20),
+    ([20, 1], [200, 60], 64, 16, 30),
+    ([90, 40], [290, 60], 128, 16, 0),
+    ([90, 40], [290, 60], 128, 32, 50),
+    ([70, 80], [400, 80], 256, 16, 33),
+    ([300, 2], [300, 9], 64, 64, 0),
+])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attention_of_what_is_not_seen(A, new, lens, D, page, window, dtype):
+    """Pages that a row does not see may hold any scale, and other rows' queries may be anything: its bits stay."""
+    rng = np.random.default_rng(D + window)
+    b = Batch(A, rng, new, lens, page)
+    _, scales, cache = random_cache(A, rng, b.pages, 2, page, D)
+    q = dev(rng.standard_normal((b.M, 6, D)).astype(np.float32), dtype)
+    seqs = b.seqs()
+    want = A.kv_attention(q, cache, seqs, window=window)
+    pos = np.concatenate([np.arange(n - m, n) for m, n in zip(new, lens)])
+    seq = np.repeat(np.arange(len(new)), new)
+    assert bool(torch.isfinite(want).all())
+    for bad in (np.nan, np.inf, -np.inf, -1.0):
+        for s in range(len(new)):
+            for j in sorted({0, (lens[s] - 1) // page, (lens[s] - new[s]) // page}):
+                for side in (cache.k_scale, cache.v_scale):
+                    side[b.table[s, j]] = bad
+                sees = (seq == s) & (pos >= j * page) & ((pos - window + 1 < (j + 1) * page) | (window == 0))
+                got = A.kv_attention(q, cache, seqs, window=window)
+                cache.k_scale.copy_(dev(scales[0]))
+                cache.v_scale.copy_(dev(scales[1]))
+                assert torch.equal(got[dev(~sees)], want[dev(~sees)]), (bad, s, j)
+        x = q.clone()
+        x[::3, 1] = bad
+        got = A.kv_attention(x, cache, seqs, window=window)
+        rest = torch.ones(q.shape[:2], dtype=torch.bool, device=DEV)
+        rest[::3, 1] = False
+        assert torch.equal(got[rest], want[rest]), bad
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 64), (256, 256)])
+def test_append_of_values_that_are_not_finite(A, dtype, D, page):
+    """They spoil their own page and head, until its first slot is written again."""
+    rng = np.random.default_rng(D)
+    b = Batch(A, rng, [20, 40, 1], [30, 40, 5], page)
+    x = rng.standard_normal((b.M, 2, D)).astype(np.float32)
+    caches = []
+    for bad in (None, np.nan, np.inf):
+        cache = A.KVCache.empty(b.pages, 2, page, D, device=DEV)
+        y = x.copy()
+        if bad is not None:
+            y[19, 1, 5] = bad                     # sequence 0's last token, head 1
+        A.kv_append(dev(y, dtype), dev(x, dtype), cache, b.seqs())
+        caches.append(cache)
+    hit = (b.table[0, 29 // page], 1)
+    keep = torch.ones(b.pages, 2, dtype=torch.bool, device=DEV)
+    keep[hit] = False
+    for c in caches[1:]:
+        assert torch.equal(c.v, caches[0].v) and torch.equal(c.v_scale, caches[0].v_scale)
+        assert torch.equal(c.k[keep], caches[0].k[keep]) and torch.equal(c.k_scale[keep], caches[0].k_scale[keep])
+    again = b.seqs()
+    again.seq_lens[0] = 20                        # from position 0 again
+    page0 = b.table[0, 0]
+    for c in caches:
+        A.kv_append(dev(x, dtype), dev(x, dtype), c, again)
+    for c in caches[1:]:
+        assert torch.equal(c.k_scale[page0], caches[0].k_scale[page0])
+        assert torch.equal(c.k[page0, :, :min(20, page)], caches[0].k[page0, :, :min(20, page)])
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_attention_query_magnitudes(A, dtype):
     """Queries from 2^-100 to 2^60 within a row and between rows."""
@@ -393,6 +463,47 @@ def test_attention_is_deterministic_and_leaves_its_workspace(A, new, dtype):
     small = Batch(A, rng, [2], [50], 32)
     check_attention(A, q[:2], small, codes, scales, cache, workspace=ws)
     assert torch.equal(A.kv_attention(q, cache, seqs, workspace=ws), first)
+
+
+def test_sequences_that_share_pages(A):
+    """A prefix in the tables of several sequences, and a page at two places of one."""
+    rng = np.random.default_rng(15)
+    for new in ([1, 1, 3], [30, 60, 45]):
+        b = Batch(A, rng, new, [100, 90, 150], 16)
+        b.table[1, :5] = b.table[0, :5]
+        b.table[2, :3] = b.table[0, 2:5]
+        b.table[2, 7] = b.table[2, 4]
+        codes, scales, cache = random_cache(A, rng, b.pages, 2, 16, 128)
+        q = dev(rng.standard_normal((b.M, 8, 128)).astype(np.float32), BF)
+        check_attention(A, q, b, codes, scales, cache)
+
+
+def test_two_graphs_that_share_a_workspace(A):
+    """Captured calls of quite different shapes on one workspace, replayed in turn with eager calls between."""
+    rng = np.random.default_rng(16)
+    codes, scales, cache = random_cache(A, rng, 400, 2, 32, 128)
+    ws = A.kv_attention_workspace(512, 4, 12, 2, 128, DEV)
+    runs = []
+    for new, lens, dtype in (([1, 1, 1], [3000, 700, 2100], BF), ([300, 40], [1500, 900], BF), ([4, 2], [2500, 30], F32)):
+        b = Batch(A, rng, new, lens, 32)
+        b.table = rng.integers(0, 400, b.table.shape).astype(np.int32)
+        q, seqs = dev(rng.standard_normal((b.M, 12, 128)).astype(np.float32), dtype), b.seqs()
+        runs.append((q, seqs, A.kv_attention(q, cache, seqs), torch.empty_like(q)))
+    torch.cuda.synchronize()
+    graphs = []
+    for q, seqs, _, out in runs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            A.kv_attention(q, cache, seqs, workspace=ws, out=out)
+        graphs.append(g)
+    for turn in range(6):
+        for i in rng.permutation(len(runs)):
+            runs[i][3].fill_(3.0)
+            graphs[i].replay()
+            if turn % 2:
+                q, seqs, want, _ = runs[(i + 1) % len(runs)]
+                assert torch.equal(A.kv_attention(q, cache, seqs, workspace=ws), want)
+            assert torch.equal(runs[i][3], runs[i][2])
 
 
 def test_streams_and_two_calls_at_once(A):

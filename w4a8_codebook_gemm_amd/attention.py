@@ -211,7 +211,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tenso
 @dataclass(frozen=True)
 class KVCache:
     """An int8 cache in pages: codes [pages, kv_heads, page_size, head_dim], a scale for each
-    page and head.  The tensors are checked here, once."""
+    page and head, finite and not negative.  The tensors are checked here, once."""
     k: torch.Tensor         # int8
     v: torch.Tensor         # int8
     k_scale: torch.Tensor   # float32 [pages, kv_heads]
@@ -300,7 +300,7 @@ def kv_attention(q: torch.Tensor, cache: KVCache, seqs: Sequences, *, scale: flo
     scale: of the scores, 1 / sqrt(D) by default.  window: positions a query sees, its own
     included (0: all before it; causal only).  workspace: from kv_attention_workspace; a new one
     is made where it is None.  out [M, Hq, D] contiguous, of q's type; rows that belong to no
-    sequence are left as they were."""
+    sequence are left as they were (in an out made here: not set)."""
     cc, sc = cache.c, seqs.c
     qp, qs = _rows(q, "q", _FLOATS, None, cc.head_dim)
     m, hq, d = q.shape
