@@ -131,15 +131,7 @@ __device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
     return a / b;
 }
 
-// A value that other workgroups read or wrote: past the per-XCD caches.
-__device__ __forceinline__ void put_shared(float *p, float v) {
-    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ float get_shared(const float *p) {
-    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-
-// The same for four values of a piece: `off` bytes from a base that is uniform over the wave, in
+// Four values of a piece, which other workgroups read or wrote, past the per-XCD caches: `off` bytes from a base that is uniform over the wave, in
 // 16-byte accesses at device scope (cache bit sc1).
 typedef uint32_t uintx4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t shared_piece(const float *base, int bytes) {

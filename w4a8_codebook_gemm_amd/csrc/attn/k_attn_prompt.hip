@@ -41,6 +41,7 @@ struct Shape {
     // fp32 rows need twice the registers for their queries: half the waves share a CU
     static constexpr int kWaves = BF16 ? 8 : 4;
     static constexpr int kThreads = 64 * kWaves;
+    static constexpr int kPerCu = !BF16 && D <= 128 ? 2 : 1;  // workgroups on a compute unit
     static constexpr int RB = 32 * kWaves;
     static constexpr int T = 8192 / D;       // positions of a tile
     static constexpr int kGroups = T / 16;
@@ -110,7 +111,7 @@ struct Tile {
 
 // kSmall: pages of 16 positions, else of 32 or more.
 template <int D, bool BF16, bool kSmall>
-__global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_attn_prompt(AttnArgs a, int wgs) {
+__global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : Shape<D, BF16>::kPerCu)) void k_attn_prompt(AttnArgs a, int wgs) {
     using S = Shape<D, BF16>;
     constexpr int kAhead = D == 128 ? 4 : 2;  // V fragments in flight
     constexpr int T = S::T, kParts = BF16 ? 1 : 2, kSteps = D / 16, kTiles = D / 32;
@@ -577,8 +578,9 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : 1)) void k_
 
 template <int D, bool BF16>
 hipError_t launch_t(const AttnArgs &a, int num_cu, hipStream_t stream) {
-    if (a.c.page_size == 16) k_attn_prompt<D, BF16, true><<<num_cu, Shape<D, BF16>::kThreads, 0, stream>>>(a, num_cu);
-    else k_attn_prompt<D, BF16, false><<<num_cu, Shape<D, BF16>::kThreads, 0, stream>>>(a, num_cu);
+    const int wgs = Shape<D, BF16>::kPerCu * num_cu;
+    if (a.c.page_size == 16) k_attn_prompt<D, BF16, true><<<wgs, Shape<D, BF16>::kThreads, 0, stream>>>(a, wgs);
+    else k_attn_prompt<D, BF16, false><<<wgs, Shape<D, BF16>::kThreads, 0, stream>>>(a, wgs);
     return hipGetLastError();
 }
 
