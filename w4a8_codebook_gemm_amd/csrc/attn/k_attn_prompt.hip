@@ -38,10 +38,10 @@ constexpr int kMinTiles = 4;  // tiles a workgroup is worth cutting for
 
 template <int D, bool BF16>
 struct Shape {
-    // fp32 rows need twice the registers for their queries: half the waves share a CU
-    static constexpr int kWaves = BF16 ? 8 : 4;
+    // fp32 rows need twice the registers for their queries: at D 256 half the waves share a CU.  (D 128 with
+    // 4 waves 1299 us for 2 x 2048 tokens on 6k, with two such workgroups 947, with 8 waves 862.)
+    static constexpr int kWaves = BF16 || D <= 128 ? 8 : 4;
     static constexpr int kThreads = 64 * kWaves;
-    static constexpr int kPerCu = !BF16 && D <= 128 ? 2 : 1;  // workgroups on a compute unit
     static constexpr int RB = 32 * kWaves;
     static constexpr int T = 8192 / D;       // positions of a tile
     static constexpr int kGroups = T / 16;
@@ -111,7 +111,7 @@ struct Tile {
 
 // kSmall: pages of 16 positions, else of 32 or more.
 template <int D, bool BF16, bool kSmall>
-__global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : Shape<D, BF16>::kPerCu)) void k_attn_prompt(AttnArgs a, int wgs) {
+__global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves / 4)) void k_attn_prompt(AttnArgs a, int wgs) {
     using S = Shape<D, BF16>;
     constexpr int kAhead = D == 128 ? 4 : 2;  // V fragments in flight
     constexpr int T = S::T, kParts = BF16 ? 1 : 2, kSteps = D / 16, kTiles = D / 32;
@@ -449,7 +449,6 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : Shape<D, BF
                     uint32_t r[kOf / 2];
                     float sum = 0.0f;
                     if constexpr (BF16) {
-                        const half2_t most = {(_Float16)32768.0f, (_Float16)32768.0f};
                         // a page whose values are not seen may hold any scale
                         const float lw = e[u] > (float)kZeroExp ? fmaxf(sc[u].z + ((float)kProbExp - En), -60.0f) : -60.0f;
                         const float c = lw - mn;
@@ -459,22 +458,30 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : Shape<D, BF
                             const float p0x = __builtin_amdgcn_exp2f(fmaf(s[k >> 4][k & 15], f[u], c));
                             const float p1x = __builtin_amdgcn_exp2f(fmaf(s[k >> 4][(k & 15) + 1], f[u], c));
                             sum += p0x + p1x;
-                            r[j / 2] = __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(half2_t, pack_half(p0x, p1x)), most));
+                            r[j / 2] = pack_half(p0x, p1x);   // 2^14 at most, as E is
                         }
                         L = fmaf(sum, __builtin_amdgcn_exp2f(-lw), L);
 #pragma unroll
                         for (int x = 0; x < kOf / 8; x++)
                             pf[u * (kOf / 8) + x][0] = __builtin_bit_cast(half8_t, make_uint4(r[4 * x], r[4 * x + 1], r[4 * x + 2], r[4 * x + 3]));
                     } else {
+                        float minus = -1.0f;
+                        asm("" : "+v"(minus));   // fma takes an fp16 number as it is, a subtraction would widen it first
                         const float w = e[u] > (float)kZeroExp ? fminf(ldexpf(sc[u].y, (int)((float)kProbExp - En)), 0x1p100f) : 0.0f;
 #pragma unroll
-                        for (int j = 0; j < kOf; j++) {
+                        for (int j = 0; j < kOf; j += 2) {
                             const int k = u * kOf + j;
-                            const float p = __builtin_amdgcn_exp2f(fmaf(s[k >> 4][k & 15], f[u], -mn));
-                            sum += p;
-                            const float x = fminf(p * w, 32768.0f);
-                            pf[k >> 3][0][k & 7] = (_Float16)x;
-                            pf[k >> 3][kParts - 1][k & 7] = (_Float16)(x - (float)(_Float16)x);
+                            const float p0x = __builtin_amdgcn_exp2f(fmaf(s[k >> 4][k & 15], f[u], -mn));
+                            const float p1x = __builtin_amdgcn_exp2f(fmaf(s[k >> 4][(k & 15) + 1], f[u], -mn));
+                            sum += p0x + p1x;
+                            const float x0 = p0x * w, x1 = p1x * w;   // 2^14 at most, as E is
+                            uint32_t hw = pack_half(x0, x1);
+                            asm("" : "+v"(hw));                      // once: what is taken off is what was kept
+                            const half2_t h = __builtin_bit_cast(half2_t, hw);
+                            pf[k >> 3][0][k & 7] = h[0];
+                            pf[k >> 3][0][(k & 7) + 1] = h[1];
+                            pf[k >> 3][kParts - 1][k & 7] = (_Float16)fmaf((float)h[0], minus, x0);
+                            pf[k >> 3][kParts - 1][(k & 7) + 1] = (_Float16)fmaf((float)h[1], minus, x1);
                         }
                         L += sum;
                     }
@@ -578,9 +585,8 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (BF16 ? 2 : Shape<D, BF
 
 template <int D, bool BF16>
 hipError_t launch_t(const AttnArgs &a, int num_cu, hipStream_t stream) {
-    const int wgs = Shape<D, BF16>::kPerCu * num_cu;
-    if (a.c.page_size == 16) k_attn_prompt<D, BF16, true><<<wgs, Shape<D, BF16>::kThreads, 0, stream>>>(a, wgs);
-    else k_attn_prompt<D, BF16, false><<<wgs, Shape<D, BF16>::kThreads, 0, stream>>>(a, wgs);
+    if (a.c.page_size == 16) k_attn_prompt<D, BF16, true><<<num_cu, Shape<D, BF16>::kThreads, 0, stream>>>(a, num_cu);
+    else k_attn_prompt<D, BF16, false><<<num_cu, Shape<D, BF16>::kThreads, 0, stream>>>(a, num_cu);
     return hipGetLastError();
 }
 
