@@ -22,6 +22,13 @@
 //
 // Split: as in the split kernel, the tiles of all units form one line that is cut evenly over the
 // workgroups; a cut unit's pieces are joined two and two in a tree.
+//
+// Measured (TFLOP/s of the positions that are seen; the library's large fp16 product reaches 1125): 2 x 2048 tokens on
+// 14000, 24 / 4 heads of 256, 1.50 to 1.55 ms, 920 to 970; 8192 causal tokens, 32 / 8 of 128, 653 us, 842, of 256 (24 / 4)
+// 951 us, 867, of 64 448 us, 614; 8192 of 128 without a mask 1229 us, 894.  fp32 has twice the products: 2 x 2048 on
+// 6000, 32 / 8 of 128, 870 us, 542.  The matrix cores are busy 42% of the cycles at head_dim 256: both products and the
+// softmax between them take turns on a SIMD's two waves, some 5 vector instructions a score; at head_dim 64, where a
+// score has a quarter of the products, these are the limit.
 #include "attn_tiles.h"
 
 namespace w4a8 {

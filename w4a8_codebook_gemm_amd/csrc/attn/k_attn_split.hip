@@ -21,6 +21,12 @@
 // Split: the tiles of all units form one line that is cut evenly over the workgroups whatever the
 // lengths are; a workgroup's waves take its tiles in turn and join in LDS.  The pieces of a unit
 // that is cut are joined through the workspace (join_pieces).
+//
+// Measured (24 / 4 heads of 256, one token a sequence): 4 x 90k to 131k tokens 169 to 173 us, 5.6 TB/s of 6.0 that a
+// plain read reaches here; 32 x 300 to 16000 104 to 107 us, 5.0 TB/s; 64 x 4000 (32 / 8 of 128) 95 us, 5.5 TB/s.
+// Between a workgroup's first tile and its join it streams at 6.3 TB/s; what is lost is starting and joining, some 12 us
+// a call: 1 x 777 tokens is 16.3 us, of them 1.6 the line, 1.4 finding the unit, 3.9 rows, pages and queries (each
+// waits for a read), 1.7 the tiles, 1.8 the waves' join and 2.2 the workgroups'.
 #include <type_traits>
 
 #include "attn_tiles.h"

@@ -10,6 +10,9 @@
 // of angles each, and keeps those of its eight values in registers for all heads it passes
 // over.  The angle is position * inv_freq in turns, reduced to [-1/2, 1/2] in fp64 (at position
 // 2^18 an fp32 product is off by 2^-7 of a radian), its sine and cosine in fp32.
+//
+// Measured: 8192 tokens, 24 + 4 heads of 256, fp32 to bf16, 77.5 us, 4.5 TB/s (a large copy runs at 4.75 here); 1021 tokens,
+// 32 + 8 of 128, fp32, 13.6 us, 3.0 TB/s, of it 4.4 us that a call of one token takes as well.
 #include "attn_internal.h"
 
 namespace w4a8 {
