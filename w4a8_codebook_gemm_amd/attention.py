@@ -162,7 +162,7 @@ def _heads(t, name, weight, out_dtype, out, m, d, dev, dtype):
     elif st < d and st != 0:
         raise ValueError(f"{name}: tokens overlap, strides are {t.stride()}")
     if out is None:
-        out = t.new_empty((m, h, d), dtype=out_dtype)
+        out = t.new_empty(m, h, d) if out_dtype is dtype else t.new_empty((m, h, d), dtype=out_dtype)
         op = out.data_ptr()
     else:
         op = _ptr(out, name + "'s output", out_dtype, (m, h, d), dev)
@@ -311,7 +311,7 @@ def kv_attention(q: torch.Tensor, cache: KVCache, seqs: Sequences, *, scale: flo
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the device of q")
     if out is None:
-        out = q.new_empty((m, hq, d))
+        out = q.new_empty(m, hq, d)
         op = out.data_ptr()
     else:
         op = _ptr(out, "out", dtype, (m, hq, d), dev)
