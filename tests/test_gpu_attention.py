@@ -288,6 +288,32 @@ def test_attention_of_many_units(A, new, lo, hi, count, Hq, Hkv, D, dtype):
     check_attention(A, q, b, codes, scales, cache)
 
 
+@pytest.mark.parametrize("count,lo,hi,Hq,Hkv,D,page,dtype,window", [
+    (300, 1, 60, 16, 8, 64, 16, BF, 0),            # a unit or more for each wave
+    (300, 30, 260, 24, 8, 128, 32, F32, 0),
+    (700, 1, 150, 20, 5, 128, 16, BF, 0),
+    (280, 100, 300, 8, 8, 64, 64, F32, 70),
+    (150, 40, 90, 32, 16, 128, 16, BF, 33),
+])
+@pytest.mark.parametrize("shape", ["alike", "some empty", "one long", "several tokens"])
+def test_attention_of_many_short_sequences(A, count, lo, hi, Hq, Hkv, D, page, dtype, window, shape):
+    """Batches with a unit or more for each wave, and those that the same launch must share out differently."""
+    rng = np.random.default_rng(count + D)
+    new, lens = [1] * count, [int(x) for x in rng.integers(lo, hi, count)]
+    if shape == "some empty":
+        new = [int(x) for x in rng.integers(0, 2, count)]
+    elif shape == "one long":
+        lens[count // 3] = 9000
+    elif shape == "several tokens":
+        new = [min(int(x), 16 * Hkv // Hq) for x in rng.integers(1, 4, count)]
+    b = Batch(A, rng, new, lens, page, rows_behind=3)
+    codes, scales, cache = random_cache(A, rng, b.pages, Hkv, page, D)
+    b.table[5, 0] = -1
+    b.table[7] = -1
+    q = dev(rng.standard_normal((b.M, Hq, D)).astype(np.float32), dtype)
+    check_attention(A, q, b, codes, scales, cache, window=window)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("new", [[1, 1, 1], [40, 90, 20]])
 def test_attention_pages_given_up(A, dtype, new):
