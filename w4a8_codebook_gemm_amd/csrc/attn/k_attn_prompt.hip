@@ -157,15 +157,18 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
     const Line cut{line, used, S::kOver, S::kTail};
     const int64_t t1 = cut.begin(w + 1);
 
+    int64_t from = 0, from_base = 0;  // the 64 sequences that the last unit was in, and their place
     for (int64_t at = cut.begin(w); at < t1;) {
         // the sequence, cache head and row block that tile `at` is in
-        int64_t base = 0, b = 0, per_head = 0;
-        for (int64_t b0 = 0; b0 < a.s.B; b0 += 64) {
+        int64_t base = from_base, b = 0, per_head = 0;
+        for (int64_t b0 = from; b0 < a.s.B; b0 += 64) {
             const int64_t mine = a.s.B <= 64 ? s_mine[lane] : seq_tiles<D, BF16>(a, b0, lane);
             const int64_t incl = a.s.B <= 64 ? s_incl[lane] : scan64(mine);
             const int64_t sum = lane_value(incl, 63);
             if (at < base + sum) {
                 const int src = __ffsll((unsigned long long)__ballot(at - base < incl)) - 1;
+                from = b0;
+                from_base = base;
                 b = b0 + src;
                 base += lane_value(incl - mine, src);
                 per_head = div64(lane_value(mine, src), a.c.kv_heads);

@@ -82,11 +82,11 @@ template <int NB>
 constexpr int kOver = NB == 2 ? 4 : 8;
 constexpr int kTail = 3;
 // Whole units for single waves, which then join nothing: where every wave has one or more, and the longest unit is longer than
-// the average by no more tiles than twice the units of a workgroup.  (A wave that is left with the longest takes some
-// 1.5 us a tile; a workgroup that starts and joins its units one after the other some 4 us each that the other on its compute
-// unit does not fill.)  32 / 8 heads of 128, workgroups' way and waves': 256 x 100 to 300 tokens 60 and 40 us, 256 x 500
-// to 2000 147 and 154, 512 of them 288 and 272, 1024 633 and 510, 256 x 2000 196 and 185.  kSoloOver: as kOver.
-constexpr int kSoloLong = 2, kSoloOver = 2;
+// the average by no more tiles than a workgroup has units.  (A wave that is left with the longest takes some 1.5 us a tile; a
+// workgroup starts and joins its units one after the other.)  32 / 8 heads of 128, workgroups' way and waves': 256 x 100 to 300
+// tokens 54 and 40 us, 256 x 500 to 2000 143 and 154, 512 of them 259 and 272, 1024 510 and 510, 256 x 2000 194 and
+// 185, fp32 512 x 300 to 900 178 and 155.  kSoloOver: as kOver.
+constexpr int kSoloOver = 2;
 
 // A unit's places on the line: its tiles and what it costs beside them, or where workgroups are many a
 // whole number of their shares.
@@ -153,7 +153,7 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_attn_split(AttnArgs a,
             const int o = __shfl_xor(longest, i);
             longest = longest > o ? longest : o;
         }
-        solo = units >= (int64_t)wgs * kWaves && __builtin_amdgcn_readfirstlane(longest) - div64(line, units) <= div64(kSoloLong * units, wgs);
+        solo = units >= (int64_t)wgs * kWaves && __builtin_amdgcn_readfirstlane(longest) - div64(line, units) <= div64(units, wgs);
     }
     auto sync = [&]() {
         if (solo) {
@@ -673,7 +673,7 @@ int wgs_of(int num_cu) { return kPerCu<NB> * num_cu; }
 template <int D, int NB>
 hipError_t launch_nb(const AttnArgs &a, int bf16, int num_cu, hipStream_t stream) {
     const int wgs = wgs_of<D, NB>(num_cu);
-    // at head_dim 256 the registers do not hold what both ways need (512 x 500 tokens 156 us, 137 without)
+    // at head_dim 256 the registers do not hold what both ways need (512 x 500 tokens of 24 / 4 heads 156 us, 128 without)
     if constexpr (NB == 1 && D < 256) {
         if (a.s.B * a.c.kv_heads >= (int64_t)wgs * kWaves) {
             if (bf16) k_attn_split<D, NB, true, true><<<wgs, kThreads, 0, stream>>>(a, wgs);
