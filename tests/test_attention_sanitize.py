@@ -3,11 +3,21 @@ host-side AddressSanitizer and UndefinedBehaviorSanitizer (hipcc, each -fsanitiz
 -Xarch_host), linked with the other sources' objects and driven by tests/attn_abi_check.c."""
 import concurrent.futures as cf
 import os
+import subprocess
 
 import pytest
 
 from conftest import ROOT
-from test_sanitize import CLANG, HIPCC, SAN_ENV, run
+
+HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+CLANG = "/opt/rocm/llvm/bin/clang"
+SAN_ENV = dict(os.environ, ASAN_OPTIONS="detect_leaks=1:abort_on_error=0", UBSAN_OPTIONS="print_stacktrace=1")
+
+
+def run(cmd, **kw):
+    r = subprocess.run(cmd, capture_output=True, text=True, **kw)
+    assert r.returncode == 0, f"{' '.join(map(str, cmd))}\n{r.stdout[-3000:]}\n{r.stderr[-6000:]}"
+    return r
 
 
 @pytest.mark.skipif(not (os.path.exists(HIPCC) and os.path.exists(CLANG)), reason="ROCm compilers not found")
