@@ -131,8 +131,8 @@ __device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
     return a / b;
 }
 
-// Four values of a piece, which other workgroups read or wrote, past the per-XCD caches: `off` bytes from a base that is uniform over the wave, in
-// 16-byte accesses at device scope (cache bit sc1).
+// Four values of a piece, which other workgroups read or wrote, past the per-XCD caches: `off` bytes from a
+// base that is uniform over the wave, in 16-byte accesses at device scope (cache bit sc1).
 typedef uint32_t uintx4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t shared_piece(const float *base, int bytes) {
     return __builtin_amdgcn_make_buffer_rsrc((void *)base, (short)0, bytes, 0x00020000);
