@@ -504,6 +504,27 @@ def test_sequences_that_share_pages(A):
         check_attention(A, q, b, codes, scales, cache)
 
 
+@pytest.mark.parametrize("M,B", [(1, 3), (500, 2), (300, 400)])
+def test_batches_without_a_token_or_a_length(A, M, B):
+    """Rows that belong to no sequence, and rows whose sequences have length zero."""
+    rng = np.random.default_rng(17)
+    codes, scales, cache = random_cache(A, rng, 4, 8, 16, 64)
+    zeros = torch.zeros(B + 1, dtype=torch.int32, device=DEV)
+    table = torch.zeros(B, 2, dtype=torch.int32, device=DEV)
+    q = torch.randn(M, 8, 64, device=DEV)
+    out = torch.full_like(q, 5.0)
+    none = A.Sequences(table, zeros, torch.full((B,), 20, dtype=torch.int32, device=DEV))
+    A.kv_attention(q, cache, none, out=out)
+    A.kv_append(q, q, cache, none)
+    assert bool((out == 5.0).all())
+    cu = torch.clamp(torch.arange(B + 1, device=DEV) * (-(-M // B)), max=M).to(torch.int32)
+    empty = A.Sequences(table, cu, zeros[:B].clone())
+    A.kv_attention(q, cache, empty, out=out)
+    A.kv_append(q, q, cache, empty)
+    assert bool((out == 0).all())
+    assert np.array_equal(cache.k.cpu().numpy(), codes[0]) and np.array_equal(cache.v_scale.cpu().numpy(), scales[1])
+
+
 def test_two_graphs_that_share_a_workspace(A):
     """Captured calls of quite different shapes on one workspace, replayed in turn with eager calls between."""
     rng = np.random.default_rng(16)
