@@ -220,12 +220,13 @@ __device__ __forceinline__ bool join_pieces(uint32_t *counters, int64_t w_first,
     return true;
 }
 
-// The positions [from, to) that new token i of a sequence sees.
+// The positions [from, to) that new token i of a sequence sees: none in front of position 0.  Both ends
+// grow with i, so a block's first token has the least of them and its last token the greatest.
 __device__ __forceinline__ void sees(const AttnArgs &a, const Seq &q, int64_t i, int &from, int &to) {
     const int64_t pos = q.pos0 + i;
     const int64_t f = a.window ? pos - a.window + 1 : 0;
     from = f > 0 ? (int)f : 0;
-    to = a.causal ? (pos + 1 > 0 ? (int)(pos + 1) : 0) : q.len;
+    to = pos < 0 ? 0 : a.causal ? (int)(pos + 1) : q.len;
 }
 
 }  // namespace w4a8
