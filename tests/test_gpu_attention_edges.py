@@ -7,7 +7,7 @@ import torch
 
 import attention_ref as R
 import test_gpu_attention as T
-from test_gpu_attention import A, BF, DEV, F32, Batch, dev, f64, random_cache  # noqa: F401  (A is a fixture)
+from test_gpu_attention import A, BF, DEV, F32, Batch, dev, random_cache  # noqa: F401  (A is a fixture)
 
 pytestmark = pytest.mark.gpu
 plain_attention = R.attention
@@ -41,3 +41,55 @@ def test_tokens_in_front_of_position_0_see_nothing(A, monkeypatch, new, lens, Hq
     q = dev(rng.standard_normal((b.M, Hq, D)).astype(np.float32), dtype)
     monkeypatch.setattr(R, "attention", attention_in_front)
     T.check_attention(A, q, b, codes, scales, cache, causal=causal)
+
+
+class Far:
+    """One sequence whose length is just below 2^31, nearly all of its pages given up, and the same sequence with
+    `cut` positions (a multiple of every tile) taken from its front, where the operators must do the same."""
+
+    def __init__(self, A, rng, new, page, hkv, d, held):
+        self.width = 2 ** 31 // page - 1
+        self.length = self.width * page - 1        # the last slot of the last page stays free
+        self.cut = 2 ** 31 - 4096
+        self.pages = held + 2
+        far = torch.full((1, self.width), -1, dtype=torch.int32, device=DEV)
+        far[0, -held:] = dev(rng.permutation(self.pages)[:held].astype(np.int32))
+        near = far[:, self.cut // page:].contiguous()
+        self.cu = dev(np.array([0, new], np.int32))
+        self.seqs = [A.Sequences(t, self.cu, dev(np.array([n], np.int32)))
+                     for t, n in ((far, self.length), (near, self.length - self.cut))]
+        _, _, self.cache = random_cache(A, rng, self.pages, hkv, page, d)
+
+
+@pytest.mark.parametrize("new,Hq,Hkv,D", [
+    (1, 6, 1, 256), (1, 8, 2, 128), (1, 2, 2, 64),        # blocks of 16 rows
+    (6, 8, 1, 128), (9, 4, 2, 256),                       # blocks of 32 rows
+    (100, 2, 1, 256), (90, 4, 2, 128), (300, 3, 1, 64),   # the prompt kernel
+])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("window", [1, 500, 1500])
+def test_lengths_up_to_2_31_with_a_window(A, new, Hq, Hkv, D, dtype, window):
+    """Tile counts and a tile's end pass 2^31 in signed arithmetic: the same bits as 2^31 - 4096 positions earlier."""
+    rng = np.random.default_rng(new + D)
+    f = Far(A, rng, new, 16, Hkv, D, held=100)
+    q = dev(rng.standard_normal((new, Hq, D)).astype(np.float32), dtype)
+    far, near = (A.kv_attention(q, f.cache, s, window=window) for s in f.seqs)
+    assert bool((near.abs().amax(-1) > 0).all()) and torch.equal(far, near)
+    x = dev(rng.standard_normal((new, Hkv, D)).astype(np.float32), dtype)
+    caches = [A.KVCache(*(t.clone() for t in (f.cache.k, f.cache.v, f.cache.k_scale, f.cache.v_scale))) for _ in f.seqs]
+    for c, s in zip(caches, f.seqs):
+        A.kv_append(x, x, c, s)
+    assert torch.equal(caches[0].k, caches[1].k) and torch.equal(caches[0].v_scale, caches[1].v_scale)
+    assert not torch.equal(caches[0].k, f.cache.k)
+
+
+@pytest.mark.parametrize("new,Hq", [(1, 4), (9, 4), (80, 4)])
+@pytest.mark.parametrize("page,causal,window", [(16, True, 0), (64, True, 0), (16, False, 0), (16, True, 2 ** 31 - 2)])
+def test_lengths_up_to_2_31_without_a_window(A, new, Hq, page, causal, window):
+    """All 2^31 positions are walked.  The pages that are there lie in the last tile, so the sums are the same."""
+    rng = np.random.default_rng(new)
+    f = Far(A, rng, new, page, 1, 64, held=64 // page)
+    q = dev(rng.standard_normal((new, Hq, 64)).astype(np.float32), F32)
+    far, near = (A.kv_attention(q, f.cache, s, causal=causal, window=window) for s in f.seqs)
+    seen = torch.arange(new, device=DEV) >= new - (64 - 1) if causal else torch.ones(new, dtype=torch.bool, device=DEV)
+    assert torch.equal((near.abs().amax((1, 2)) > 0), seen) and torch.equal(far, near)

@@ -125,6 +125,12 @@ __device__ __forceinline__ int64_t scan64(int64_t x) {
     return x;
 }
 
+// Tiles of T positions in front of position `to` >= 0.  Lengths end below 2^31: a signed sum would pass it.
+template <int T>
+__device__ __forceinline__ int tiles_to(int to) {
+    return (int)(((uint32_t)to + (T - 1)) / T);
+}
+
 // a / b for a >= 0, b > 0
 __device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
     if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);

@@ -69,7 +69,7 @@ __device__ __forceinline__ int block_tiles(const AttnArgs &a, const Seq &q, int6
     sees(a, q, div64(r0, a.group), lo, x);
     sees(a, q, div64(last, a.group), x, hi);
     first = lo / S::T;
-    const int n = (hi + S::T - 1) / S::T - first;
+    const int n = tiles_to<S::T>(hi) - first;
     return n < 1 ? 1 : n;  // rows that see nothing are still written
 }
 
@@ -374,7 +374,7 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
 #pragma unroll 1
             for (int step = 0; step < T / kWide; step++) {
                 const int p0 = tile * T + kWide * step;
-                if (p0 >= any_hi || p0 + kWide <= any_lo) continue;  // uniform over the wave
+                if (p0 >= any_hi || any_lo - p0 >= kWide) continue;  // uniform over the wave
                 float4 sc[kScales];
 #pragma unroll
                 for (int u = 0; u < kScales; u++) sc[u] = s_sc[buf][step * (kWide / 16) + u * (kSpan / 16)];
@@ -416,8 +416,8 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
                 float worst = sc[0].w;
 #pragma unroll
                 for (int u = 1; u < kScales; u++) worst = fmaxf(worst, sc[u].w);
-                if (!(p0 >= all_lo && p0 + kWide <= all_hi && worst < kNoPage)) {
-                    const int to = hi - p0 - 4 * (ln >> 5), from = a.window ? to - (int)a.window : -p0 - kWide;
+                if (!(p0 >= all_lo && all_hi - p0 >= kWide && worst < kNoPage)) {
+                    const int to = hi - p0 - 4 * (ln >> 5), from = a.window ? __builtin_elementwise_sub_sat(to, (int)a.window) : -p0 - kWide;
 #pragma unroll
                     for (int j = 0; j < 16 * kSubs; j++) {
                         const int t = 8 * (j >> 2) + (j & 3);

@@ -69,7 +69,7 @@ __device__ __forceinline__ Work seq_work(const AttnArgs &a, int64_t b) {
     w.q = load_seq(a.s, a.M, a.page_shift, b);
     if (w.q.n > 0) {
         if (a.window && (int64_t)w.q.pos0 - a.window + 1 > 0) w.lo = (int)(w.q.pos0 - a.window + 1) / T;
-        w.tiles = (w.q.len + T - 1) / T - w.lo;
+        w.tiles = tiles_to<T>(w.q.len) - w.lo;
         if (w.tiles < 1) w.tiles = 1;  // rows that see nothing are still written
         w.units = ((int64_t)w.q.n * a.group + RB - 1) / RB * a.c.kv_heads;
     }
@@ -262,7 +262,7 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_attn_split(AttnArgs a,
         const int end = lo_tile + tile1;
         int first = lo_tile + tile0 + (solo ? 0 : wave);
         if (first < any_lo / T) first += (any_lo / T - first + step - 1) / step * step;
-        const int stop = end < (any_hi + T - 1) / T ? end : (any_hi + T - 1) / T;
+        const int stop = end < tiles_to<T>(any_hi) ? end : tiles_to<T>(any_hi);
         const int P = a.c.page_size, pm = P - 1;
         const bool small = a.page_shift == 4;  // two pages in 32 positions
         const int32_t *table = a.s.page_table + b * a.s.table_width;
@@ -412,7 +412,7 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_attn_split(AttnArgs a,
                 load_scales();
                 load_k(tile + step);
             }
-            bool whole = tile * T >= all_lo && tile * T + T <= all_hi;
+            bool whole = tile * T >= all_lo && all_hi - tile * T >= T;
 #pragma unroll
             for (int x = 0; x < U; x++) whole = whole && __all(tvs[x] >= 0.0f);
             half8_t pf[NB][U][kParts];
