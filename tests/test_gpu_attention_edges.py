@@ -93,3 +93,29 @@ def test_lengths_up_to_2_31_without_a_window(A, new, Hq, page, causal, window):
     far, near = (A.kv_attention(q, f.cache, s, causal=causal, window=window) for s in f.seqs)
     seen = torch.arange(new, device=DEV) >= new - (64 - 1) if causal else torch.ones(new, dtype=torch.bool, device=DEV)
     assert torch.equal((near.abs().amax((1, 2)) > 0), seen) and torch.equal(far, near)
+
+
+@pytest.mark.parametrize("P,D,n", [(16, 64, 1), (64, 128, 3), (256, 256, 20)])   # a wave a page; the workgroup
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("mags", [
+    [2.0e38, 3.38e38, 1.0e38, 3.38e38],           # the scale doubles, and 127 times it is above fp32's range
+    [3.3895314e38, 3.3895314e38, 1.0, 0.0],       # bf16's largest
+    [1.0e-38, 3.38e38, 3.38e38, 1e-30],
+    [1.8e38, 3.0e38, 3.38e38],
+])
+def test_append_next_to_the_largest_numbers(A, P, D, n, dtype, mags):
+    """127 times a page's scale may be infinite: everything finite has room then, and the scale stays."""
+    cache = A.KVCache.empty(1, 1, P, D, device=DEV)
+    codes, scales = np.zeros((1, 1, P, D), np.int8), np.zeros((1, 1), np.float32)
+    table = np.zeros((1, 1), np.int32)
+    for t, m in enumerate(mags):
+        x = dev((np.linspace(-1, 1, n * D).reshape(n, 1, D) * m).astype(np.float32), dtype)
+        assert bool(torch.isfinite(x).all())
+        cu, lens = np.array([0, n]), np.array([n * (t + 1)])
+        A.kv_append(x, x, cache, A.Sequences(dev(table), dev(cu, torch.int32), dev(lens, torch.int32)))
+        with np.errstate(over="ignore"):
+            R.append(x.float().cpu().numpy(), codes, scales, table, cu, lens, 1)
+        torch.cuda.synchronize()
+        assert np.isfinite(scales).all()
+        assert np.array_equal(cache.k_scale.cpu().numpy(), scales) and np.array_equal(cache.v_scale.cpu().numpy(), scales), t
+        assert np.array_equal(cache.k.cpu().numpy(), codes) and np.array_equal(cache.v.cpu().numpy(), codes), t

@@ -152,7 +152,8 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(AppendArgs a) {
     float s = top / 127.0f;
     if (before > 0.0f) {
         // the smallest j >= 0 with top <= room * 2^j, from the exponents and fractions
-        const float room = 127.0f * before;
+        // (127 times a scale may pass fp32's range: every finite value has room then)
+        const float room = fminf(127.0f * before, 0x1.fffffep127f);
         int et = 0, er = 0;
         const float mt = frexpf(top, &et), mr = frexpf(room, &er);
         int j = top > 0.0f ? et - er + (mt > mr ? 1 : 0) : 0;
