@@ -7,7 +7,7 @@ import torch
 
 import attention_ref as R
 import test_gpu_attention as T
-from test_gpu_attention import A, BF, DEV, F32, Batch, dev, random_cache  # noqa: F401  (A is a fixture)
+from test_gpu_attention import A, BF, DEV, F32, Batch, dev, f64, random_cache  # noqa: F401  (A is a fixture)
 
 pytestmark = pytest.mark.gpu
 plain_attention = R.attention
@@ -119,3 +119,36 @@ def test_append_next_to_the_largest_numbers(A, P, D, n, dtype, mags):
         assert np.isfinite(scales).all()
         assert np.array_equal(cache.k_scale.cpu().numpy(), scales) and np.array_equal(cache.v_scale.cpu().numpy(), scales), t
         assert np.array_equal(cache.k.cpu().numpy(), codes) and np.array_equal(cache.v.cpu().numpy(), codes), t
+
+
+@pytest.mark.parametrize("new,lens,D,page", [([1, 2], [40, 300], 128, 32), ([20], [100], 64, 16), ([90, 40], [290, 60], 64, 16),
+                                             ([100, 3], [150, 70], 128, 64), ([130], [130], 256, 32)])
+@pytest.mark.parametrize("exps", [[-130], [-149, -131], [-126, -127, -128, -140], [-130, -122], [-149, -60, 0]])
+def test_attention_with_subnormal_value_scales(A, new, lens, D, page, exps):
+    """Value scales below fp32's normal range: each page counts with its own.  Codes are 64 to 127, so an output is
+    2^6 of the largest scale or more: a normal fp32 number wherever that scale is 2^-131 or above."""
+    rng = np.random.default_rng(D + len(exps))
+    b = Batch(A, rng, new, lens, page)
+    codes, scales, cache = random_cache(A, rng, b.pages, 2, page, D)
+    codes[1] = rng.integers(64, 128, codes[1].shape).astype(np.int8)
+    scales[1][:] = np.ldexp(np.float32(1), np.array(exps)[np.arange(b.pages) % len(exps)])[:, None]
+    cache.v.copy_(dev(codes[1]))
+    cache.v_scale.copy_(dev(scales[1]))
+    for dtype in (BF, F32):
+        q = dev((0.05 * rng.standard_normal((b.M, 4, D))).astype(np.float32), dtype)   # flat: every page weighs in
+        check_tiny(A, q, b, codes, scales, cache)
+
+
+def check_tiny(A, q, b, codes, scales, cache):
+    """T.check_attention's bound, and half of the type's smallest step for outputs that are subnormal."""
+    out = A.kv_attention(q, cache, b.seqs())
+    ref, size, top, delta = R.attention(f64(q), codes[0], scales[0], codes[1], scales[1], b.table, b.cu, b.lens,
+                                        q.shape[-1] ** -0.5, True, 0)
+    wide = q.dtype == F32
+    length = int(b.lens.max())
+    e = ((q.shape[-1] + 16) * T.U + (2.0 ** -22 if wide else 0)) * delta
+    bound = (2 * e + 8 * T.U + 2 * (length / 32 + 40) * T.U + 70 * T.U + (2.0 ** -21 if wide else 2.0 ** -11)) * size
+    # a weight under fp16's range is off by half its step, 2^-25, of a largest one that stands at 2^8 at least
+    bound = bound + 2.0 ** -33 * top + T.half_step(q.dtype) * (np.abs(ref) + bound) + torch.finfo(q.dtype).smallest_normal * T.half_step(q.dtype) * 2
+    err = np.abs(f64(out) - ref)
+    assert np.all(err <= bound), float((err / bound).max())

@@ -341,9 +341,10 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
                     *reinterpret_cast<uint4 *>(p + L8::v_at(D / 2, 0)) = make_uint4(codes_pair<2>(d[0], d[1]), codes_pair<2>(d[2], d[3]), codes_pair<2>(d[4], d[5]), codes_pair<2>(d[6], d[7]));
                     *reinterpret_cast<uint4 *>(p + L8::v_at(3 * D / 4, 0)) = make_uint4(codes_pair<3>(d[0], d[1]), codes_pair<3>(d[2], d[3]), codes_pair<3>(d[4], d[5]), codes_pair<3>(d[6], d[7]));
                     if (scaler()) {
+                        // (the logarithm is the fraction's: it takes a subnormal scale for 0)
                         int e = kZeroExp;
-                        if (st_vs > 0.0f) frexpf(st_vs, &e);
-                        s_sc[buf][vg >> 1] = make_float4(st_ks, st_vs, __builtin_amdgcn_logf(st_vs), st_ks < 0.0f ? kNoPage : (float)e);
+                        const float part = st_vs > 0.0f ? frexpf(st_vs, &e) : 0.0f;
+                        s_sc[buf][vg >> 1] = make_float4(st_ks, st_vs, (float)e + __builtin_amdgcn_logf(part), st_ks < 0.0f ? kNoPage : (float)e);
                     }
                 } else {
                     int kt, kc;
