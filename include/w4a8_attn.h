@@ -157,9 +157,13 @@ W4A8_API int64_t w4a8_kv_attention_workspace_bytes(int64_t M, int64_t B, int q_h
  *            workspace serves later calls of any shape it is large enough for, one at a time:
  *            calls that may overlap need workspaces of their own.
  *
- * Scores, softmax statistics and sums are fp32.  bf16 queries are exact in the products;
- * probabilities enter the second product as fp16 (relative error 2^-11 each), for fp32 as the
- * sum of two fp16 numbers (2^-22), as fp32 queries do.  Deterministic.
+ * Scores, softmax statistics and sums are fp32: an exponent is off by some 2^-24 of the row's largest
+ * |score|, so scores of 2^13 (in powers of two) cost a probability 2^-11 of itself.  bf16 queries are exact
+ * in the products down to 2^-28 of a row's largest value.  With P the row's largest probability times value
+ * scale, probabilities enter the second product as one fp16 number for bf16: off by 2^-11 of themselves, or by
+ * 2^-33 P where they are below 2^-22 P; for fp32 as the sum of two: 2^-22 of themselves, 2^-37 P below 2^-15 P,
+ * and fp32 queries likewise (2^-38 of the row's largest value below 2^-16 of it).  A score or a sum that
+ * leaves fp32's range leaves the row without a meaning.  Deterministic.
  */
 W4A8_API int w4a8_kv_attention(const void *q, int64_t q_stride, int dtype, int64_t M, int q_heads,
                                const w4a8_kv_cache *cache, const w4a8_sequences *seqs, float sm_scale, int causal,

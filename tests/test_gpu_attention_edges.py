@@ -152,3 +152,34 @@ def check_tiny(A, q, b, codes, scales, cache):
     bound = bound + 2.0 ** -33 * top + T.half_step(q.dtype) * (np.abs(ref) + bound) + torch.finfo(q.dtype).smallest_normal * T.half_step(q.dtype) * 2
     err = np.abs(f64(out) - ref)
     assert np.all(err <= bound), float((err / bound).max())
+
+
+@pytest.mark.parametrize("new,dtype", [(1, BF), (1, F32), (90, BF), (90, F32)])
+@pytest.mark.parametrize("size", [2.0 ** 10, 2.0 ** 13, 2.0 ** 16])
+@pytest.mark.parametrize("page", [16, 64])
+def test_pages_of_equal_large_scores_weigh_the_same(A, new, dtype, size, page):
+    """Every key is the same, so all scores are, to the bit, whatever their size: a query's output is the mean of the
+    values before it.  A probability is off by its fp16 half step (2^-11, for fp32 2^-22) and the rounding of an
+    exponent of that size, 2^-24 size ln 2 (the fp32 kernels subtract equal numbers: none there)."""
+    rng = np.random.default_rng(page)
+    D, length = 128, 400
+    b = Batch(A, rng, [new], [length], page)
+    codes, scales, cache = random_cache(A, rng, b.pages, 1, page, D)
+    codes[0][:] = rng.integers(-127, 128, D)
+    scales[0][:] = 1.0 / 128
+    cache.k.copy_(dev(codes[0]))
+    cache.k_scale.copy_(dev(scales[0]))
+    q = np.sign(codes[0][0, 0, 0].astype(np.float64)) * rng.uniform(0.5, 1, (new, 2, D))
+    dot = (q * codes[0][0, 0, 0]).sum(-1).max() / 128
+    q = dev(q.astype(np.float32), dtype)
+    out = f64(A.kv_attention(q, cache, b.seqs(), scale=float(size / dot / np.log2(np.e))))
+    t = np.arange(length)
+    v = codes[1][b.table[0, t // page], 0, t % page] * scales[1][b.table[0, t // page], 0].astype(np.float64)[:, None]
+    for i in range(new):
+        seen = v[:length - new + i + 1]
+        ref, mass = seen.mean(0), np.abs(seen).mean(0)
+        weight = 2.0 ** -22 if dtype == F32 else 2.0 ** -11 + 2.0 ** -24 * size * np.log(2)
+        # the sum of probabilities carries the exponent's part too; fp32 sums of 400 terms
+        bound = (2 * weight + 2 * (length / 32 + 40) * T.U) * mass
+        bound = bound + T.half_step(dtype) * (np.abs(ref) + bound)
+        assert np.all(np.abs(out[i] - ref) <= bound), (i, float((np.abs(out[i] - ref) / bound).max()))
