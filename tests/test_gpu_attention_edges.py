@@ -183,3 +183,24 @@ def test_pages_of_equal_large_scores_weigh_the_same(A, new, dtype, size, page):
         bound = (2 * weight + 2 * (length / 32 + 40) * T.U) * mass
         bound = bound + T.half_step(dtype) * (np.abs(ref) + bound)
         assert np.all(np.abs(out[i] - ref) <= bound), (i, float((np.abs(out[i] - ref) / bound).max()))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_angles_keep_their_low_bits(A, interleaved):
+    """Heads of pairs (1, 0) become cosines and sines.  Near the half and the quarter turns, where one of the two is
+    small, it has its own relative error: 2 ulp of the function, half of one for what the fp32 angle leaves out, 2^-53
+    of the turn and of the angle on either side."""
+    rng = np.random.default_rng(1)
+    D = 256
+    near = rng.choice([0.5, 0.25, -0.25, -0.5], D // 2) + rng.choice([-1, 1], D // 2) * np.exp(rng.uniform(np.log(1e-7), np.log(0.2), D // 2))
+    freq = 2 * np.pi * near
+    x = torch.zeros(3, 2, D, device=DEV)
+    first = slice(0, D, 2) if interleaved else slice(0, D // 2)
+    second = slice(1, D, 2) if interleaved else slice(D // 2, D)
+    x[..., first] = 1
+    pos = np.array([1, -1, 0], np.int32)
+    y, _ = A.qk_norm_rope(x, None, dev(pos), dev(freq), interleaved=interleaved)
+    angle = pos[:, None, None] * freq
+    for got, ref in ((f64(y[..., first]), np.cos(angle)), (f64(y[..., second]), np.sin(angle))):
+        err, bound = np.abs(got - ref), 2.5 * 2.0 ** -23 * np.abs(ref) + 4 * 2.0 ** -53 * np.pi
+        assert np.all(err <= bound), float((err / bound).max())

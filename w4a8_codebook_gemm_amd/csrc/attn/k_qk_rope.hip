@@ -9,7 +9,8 @@
 // head: a wave takes one token, computes its cosines and sines once, a lane or two lanes' worth
 // of angles each, and keeps those of its eight values in registers for all heads it passes
 // over.  The angle is position * inv_freq in turns, reduced to [-1/2, 1/2] in fp64 (at position
-// 2^18 an fp32 product is off by 2^-7 of a radian), its sine and cosine in fp32.
+// 2^18 an fp32 product is off by 2^-7 of a radian); sine and cosine of its fp32 part are fp32, what that
+// part leaves out is added to both.
 //
 // Measured: 8192 tokens, 24 + 4 heads of 256, fp32 to bf16, 77.5 us, 4.5 TB/s (a large copy runs at 4.75 here); 1021 tokens,
 // 32 + 8 of 128, fp32, 13.6 us, 3.0 TB/s, of it 4.4 us that a call of one token takes as well.
@@ -77,10 +78,13 @@ __global__ __launch_bounds__(kThreads) void k_qk_norm_rope(RopeArgs a, int chunk
         float *cs = s_cs[wave][0], *sn = s_cs[wave][1];
         for (int i = lane; i < half; i += 64) {
             const double turns = pos * (a.inv_freq[i] * 0.15915494309189533577);
+            // what the fp32 angle leaves out, in radians, is small enough for one term
+            const double part = turns - rint(turns);
+            const float near = (float)part, rest = (float)((part - (double)near) * 6.28318530717958647692);
             float sv, cv;
-            sincospif(2.0f * (float)(turns - rint(turns)), &sv, &cv);
-            cs[i] = cv * a.attn_factor;
-            sn[i] = sv * a.attn_factor;
+            sincospif(2.0f * near, &sv, &cv);
+            cs[i] = fmaf(-rest, sv, cv) * a.attn_factor;
+            sn[i] = fmaf(rest, cv, sv) * a.attn_factor;
         }
         // the wave reads what its own lanes wrote
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
