@@ -132,6 +132,9 @@ typedef struct {
 W4A8_API int w4a8_kv_append(const void *k, int64_t k_stride, const void *v, int64_t v_stride, int dtype, int64_t M,
                             const w4a8_kv_cache *cache, const w4a8_sequences *seqs, void *stream);
 
+/* What of a workspace has to be zero before its first use: its first bytes. */
+#define W4A8_KV_ATTENTION_COUNTER_BYTES 8192
+
 /*
  * Workspace bytes w4a8_kv_attention needs for up to M tokens and B sequences on the current
  * device (a negative status for an invalid shape).  Launches nothing.
@@ -152,10 +155,11 @@ W4A8_API int64_t w4a8_kv_attention_workspace_bytes(int64_t M, int64_t B, int q_h
  *  q_heads   a multiple of kv_heads, at most 8192
  *  causal    0 or 1;  window  0 (none) or >= 1, causal only
  *  o         [M][q_heads][head_dim], element type dtype; overlaps no other operand
- *  workspace device memory of w4a8_kv_attention_workspace_bytes(M, B, ...) bytes or more, zero-filled before its
- *            first use; every call that completes leaves the counters in it at zero, so one
- *            workspace serves later calls of any shape it is large enough for, one at a time:
- *            calls that may overlap need workspaces of their own.
+ *  workspace device memory of w4a8_kv_attention_workspace_bytes(M, B, ...) bytes or more, its first
+ *            W4A8_KV_ATTENTION_COUNTER_BYTES zero before its first use (the others may hold anything);
+ *            every call that completes leaves these counters at zero, so one workspace serves later
+ *            calls of any shape it is large enough for, one at a time: calls that may overlap need
+ *            workspaces of their own.
  *
  * Scores, softmax statistics and sums are fp32: an exponent is off by some 2^-24 of the row's largest
  * |score|, so scores of 2^13 (in powers of two) cost a probability 2^-11 of itself.  bf16 queries are exact

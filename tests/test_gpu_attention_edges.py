@@ -204,3 +204,25 @@ def test_rope_angles_keep_their_low_bits(A, interleaved):
     for got, ref in ((f64(y[..., first]), np.cos(angle)), (f64(y[..., second]), np.sin(angle))):
         err, bound = np.abs(got - ref), 2.5 * 2.0 ** -23 * np.abs(ref) + 4 * 2.0 ** -53 * np.pi
         assert np.all(err <= bound), float((err / bound).max())
+
+
+@pytest.mark.parametrize("new,dtype", [([1, 1, 1], BF), ([5, 9, 6], F32), ([300, 20, 150], BF), ([100, 90, 3], F32)])
+def test_workspace_behind_its_counters_may_hold_anything(A, new, dtype):
+    rng = np.random.default_rng(6)
+    b = Batch(A, rng, new, [3000, 700, 2000], 32)
+    _, _, cache = random_cache(A, rng, b.pages, 2, 32, 128)
+    q, seqs = dev(rng.standard_normal((b.M, 8, 128)).astype(np.float32), dtype), b.seqs()
+    shape = (b.M, 3, 8, 2, 128)
+    want = A.kv_attention(q, cache, seqs)
+    filled = torch.full((A.kv_attention_workspace_bytes(*shape),), 255, dtype=torch.uint8, device=DEV)   # NaN as floats
+    at = filled.data_ptr()
+    filled[:A.COUNTER_BYTES] = 0
+    assert torch.equal(A.kv_attention(q, cache, seqs, workspace=filled), want)
+    # a new workspace costs its counters' zeros, not those of the megabytes behind them
+    filled.fill_(255)
+    del filled
+    ws = A.kv_attention_workspace(*shape, DEV)
+    if ws.data_ptr() != at:
+        pytest.skip("the allocator gave other memory")
+    assert int(ws[:A.COUNTER_BYTES].max()) == 0 and int(ws[A.COUNTER_BYTES:].min()) == 255
+    assert torch.equal(A.kv_attention(q, cache, seqs, workspace=ws), want)

@@ -23,6 +23,7 @@ from . import BF16, F32, STATUS, _dev
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libw4a8_attn.so")
 
+COUNTER_BYTES = 8192  # W4A8_KV_ATTENTION_COUNTER_BYTES
 ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = 0, 1, 2, 3
 _SCALINGS = {"plain": ROPE_PLAIN, "linear": ROPE_LINEAR, "ntk": ROPE_NTK, "yarn": ROPE_YARN}
 EXPORTS = ("w4a8_attn_status_string", "w4a8_rope_frequencies", "w4a8_qk_norm_rope", "w4a8_kv_append",
@@ -287,10 +288,12 @@ def kv_attention_workspace_bytes(tokens: int, sequences: int, q_heads: int, kv_h
 
 def kv_attention_workspace(tokens: int, sequences: int, q_heads: int, kv_heads: int, head_dim: int,
                            device="cuda") -> torch.Tensor:
-    """A zero-filled workspace for kv_attention: one for each call that may run at a time."""
+    """A workspace for kv_attention, its counters zero: one for each call that may run at a time."""
     with torch.cuda.device(device):
         n = kv_attention_workspace_bytes(tokens, sequences, q_heads, kv_heads, head_dim)
-        return torch.zeros(n, dtype=torch.uint8, device=device)
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        ws[:COUNTER_BYTES].zero_()
+        return ws
 
 
 def kv_attention(q: torch.Tensor, cache: KVCache, seqs: Sequences, *, scale: float | None = None, causal: bool = True,

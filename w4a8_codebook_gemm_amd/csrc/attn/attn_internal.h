@@ -42,7 +42,7 @@ struct AttnArgs {
     void *o;
     void *ws;
 };
-constexpr int64_t kAttnCounterBytes = 8192;  // arrival counters at the workspace's start
+constexpr int64_t kAttnCounterBytes = W4A8_KV_ATTENTION_COUNTER_BYTES;  // arrival counters at the workspace's start
 // Few rows a sequence: blocks of 16 (blocks 1) or 32 (2) rows.
 int64_t attn_split_bytes(int head_dim, int num_cu);
 hipError_t launch_attn_split(const AttnArgs &a, int bf16, int blocks, int num_cu, hipStream_t stream);
