@@ -88,8 +88,13 @@ def _check(status: int, what: str):
         raise AttentionError(status, what)
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+def _public_raw_stream(i: int) -> int:
+    return torch.cuda.current_stream(i).cuda_stream
+
+
+# the accessors under torch's public ones take less time; a build of torch may lack them
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_raw_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _launch(dev: torch.device, what: str, f, *args):
