@@ -39,3 +39,30 @@ def test_calls_run_with_torchs_public_accessors(monkeypatch):
     monkeypatch.setattr(A, "_current_device", torch.cuda.current_device)
     got, _ = A.qk_norm_rope(x, None, pos, freq)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("far", [1 << 32, -(1 << 32), 1 << 64])
+def test_numbers_past_the_librarys_integers_are_refused(far):
+    """Their low bits alone would pass for a good call."""
+    with pytest.raises(ValueError, match="does not fit"):
+        A.rope_frequencies(far + 16, device="cpu")
+    good = dict(tokens=1, sequences=1, q_heads=8, kv_heads=4, head_dim=128)
+    for name in good:
+        wrap = far if name in ("q_heads", "kv_heads", "head_dim") else 1 << 64
+        with pytest.raises(ValueError, match=name):
+            A.kv_attention_workspace_bytes(**good | {name: good[name] + wrap})
+
+
+@pytest.mark.gpu
+def test_windows_past_the_librarys_integers_are_refused():
+    cache = A.KVCache.empty(2, 1, 16, 64, device="cuda:0")
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda:0")  # noqa: E731
+    s = A.Sequences(i32([0, 1]), i32(0, 2), i32(20))
+    q = torch.randn(2, 2, 64, device="cuda:0")
+    want = A.kv_attention(q, cache, s)
+    assert torch.equal(A.kv_attention(q, cache, s, window=(1 << 63) - 1), want)
+    for window in ((1 << 64) + 3, 1 << 63):
+        with pytest.raises(ValueError, match="window"):
+            A.kv_attention(q, cache, s, window=window)
+    with pytest.raises(A.AttentionError):
+        A.kv_attention(q, cache, s, window=-1)

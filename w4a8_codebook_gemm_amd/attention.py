@@ -116,6 +116,13 @@ def _ptr(t, name: str, dtype, shape, dev) -> int:
     return _dev(t, name, (dtype,), shape, dev)
 
 
+def _fits(bits: int, **numbers):
+    """Refuses integers that the library would see as others: ctypes takes their low bits without a word."""
+    for name, x in numbers.items():
+        if not -(1 << bits - 1) <= x < 1 << bits - 1:
+            raise ValueError(f"{name} {x} does not fit {bits} bits")
+
+
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
                      original_context: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
                      device="cuda") -> tuple[torch.Tensor, float]:
@@ -124,6 +131,7 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "pla
     scaling: "plain", "linear", "ntk" or "yarn" (see w4a8_rope_scaling)."""
     if scaling not in _SCALINGS:
         raise ValueError(f"scaling must be one of {tuple(_SCALINGS)}, got {scaling!r}")
+    _fits(32, rotary_dim=rotary_dim)
     out = torch.empty(max(int(rotary_dim), 0) // 2 + 1, dtype=torch.float64)
     attn = C.c_float(0.0)
     _check(lib().w4a8_rope_frequencies(rotary_dim, base, _SCALINGS[scaling], factor, original_context, beta_fast,
@@ -285,6 +293,8 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, seqs: Sequences)
 
 def kv_attention_workspace_bytes(tokens: int, sequences: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
     """Workspace bytes kv_attention needs for up to `tokens` rows and `sequences` sequences."""
+    _fits(64, tokens=tokens, sequences=sequences)
+    _fits(32, q_heads=q_heads, kv_heads=kv_heads, head_dim=head_dim)
     n = lib().w4a8_kv_attention_workspace_bytes(tokens, sequences, q_heads, kv_heads, head_dim)
     if n < 0:
         _check(-n, "w4a8_kv_attention_workspace_bytes")
@@ -310,6 +320,8 @@ def kv_attention(q: torch.Tensor, cache: KVCache, seqs: Sequences, *, scale: flo
     is made where it is None.  out [M, Hq, D] contiguous, of q's type; rows that belong to no
     sequence are left as they were (in an out made here: not set)."""
     cc, sc = cache.c, seqs.c
+    if window:
+        _fits(64, window=window)
     qp, qs = _rows(q, "q", _FLOATS, None, cc.head_dim)
     m, hq, d = q.shape
     dev, dtype = q.device, q.dtype
