@@ -124,7 +124,8 @@ typedef struct {
  * Bit-exact and deterministic for finite values.  A NaN or an infinity leaves its page and head
  * without a meaning until slot 0 is written again, and no other page or head.  Slots behind the last
  * token keep their bytes.  A call must not append to a page twice,
- * from two sequences or at two places of one.
+ * from two sequences or at two places of one.  Its time grows with the square of the sequences beyond a few
+ * thousand.
  *
  *  k, v   [M] tokens of kv_heads * head_dim consecutive values, k_stride and v_stride elements
  *         apart (multiples of 8, at least kv_heads * head_dim), element type dtype;  1 <= M <= 2^24
@@ -147,7 +148,10 @@ W4A8_API int64_t w4a8_kv_attention_workspace_bytes(int64_t M, int64_t B, int q_h
  * over the positions t that the query at position p sees: all of the sequence (causal 0), or
  * t <= p, and with window > 0 also t > p - window.  A query that sees nothing gives 0.  Query
  * head h reads cache head h / (q_heads / kv_heads).  Rows of o that belong to no sequence are
- * left as they were.  Where a query is not finite, or a scale of a page that it sees is negative or not
+ * left as they were.  One kernel serves a call; which one goes by M * (q_heads / kv_heads) / B, the rows a
+ * sequence has on average.  Any mix of sequences is right, but a batch of single tokens beside a long prompt
+ * takes up to twice the time of two calls, and rows behind the last sequence or many sequences without a
+ * token may choose the slower kernel.  Where a query is not finite, or a scale of a page that it sees is negative or not
  * finite, that row of o has no meaning; other rows, and rows that do not see the page, are not touched by it.
  *
  *  q         [M] tokens of q_heads * head_dim consecutive values, q_stride elements apart (a

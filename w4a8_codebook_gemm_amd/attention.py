@@ -9,6 +9,8 @@ projections (include/w4a8_attn.h).
 
 Argument marshalling only, as in the package itself: placement, dtype and layout are checked
 here, the kernels run on the current stream of the tensors' device, and nothing falls back.
+Every tensor begins at a multiple of 16 bytes (a slice such as positions[3:] does not) and a call
+has at least one token; the library refuses others.
 """
 from __future__ import annotations
 
@@ -317,8 +319,9 @@ def kv_attention(q: torch.Tensor, cache: KVCache, seqs: Sequences, *, scale: flo
 
     scale: of the scores, 1 / sqrt(D) by default.  window: positions a query sees, its own
     included (0: all before it; causal only).  workspace: from kv_attention_workspace; a new one
-    is made where it is None.  out [M, Hq, D] contiguous, of q's type; rows that belong to no
-    sequence are left as they were (in an out made here: not set)."""
+    is made where it is None.  out [M, Hq, D] contiguous, of q's type, apart from the other operands;
+    rows that belong to no sequence are left as they were (in an out made here: not set).  Single tokens
+    beside long prompts are faster as a call of their own (see w4a8_kv_attention)."""
     cc, sc = cache.c, seqs.c
     if window:
         _fits(64, window=window)

@@ -26,11 +26,15 @@
 // workgroups; a cut unit's pieces are joined two and two in a tree.
 //
 // Measured (TFLOP/s of the positions that are seen; the library's large fp16 product reaches 1125): 2 x 2048 tokens on
-// 14000, 24 / 4 heads of 256, 1.50 to 1.55 ms, 920 to 970; 8192 causal tokens, 32 / 8 of 128, 653 us, 842, of 256 (24 / 4)
-// 951 us, 867, of 64 448 us, 614; 8192 of 128 without a mask 1229 us, 894.  fp32 has twice the products: 2 x 2048 on
-// 6000, 32 / 8 of 128, 870 us, 542.  The matrix cores are busy 42% of the cycles at head_dim 256: both products and the
-// softmax between them take turns on a SIMD's two waves, some 5 vector instructions a score; at head_dim 64, where a
-// score has a quarter of the products, these are the limit.
+// 14000, 24 / 4 heads of 256, 1.46 to 1.55 ms, 940 to 1000; 8192 causal tokens, 32 / 8 of 128, 620 to 690 us, 800 to 890, of
+// 256 (24 / 4) 910 to 940 us, 880 to 910, of 64 436 to 494 us, 560 to 630; 8192 of 128 without a mask 1150 to 1220 us, 900
+// to 960.  fp32 has twice the products: 2 x 2048 on 6000, 32 / 8 of 128, 842 to 862 us, 550; 2 x 1024 on 2000, 24 / 4 of
+// 256, 390 us, 320, with one wave a SIMD.  The matrix cores are busy 44% of the cycles at head_dim 256: both products and
+// the softmax between them take turns on a SIMD's two waves, some 5 vector instructions a score.  At head_dim 64 a score
+// has a quarter of the products: a step of 64 positions has some 185 vector instructions and 35 exponentials, 1300 cycles, to 512
+// cycles of products, so 39% is the most that two waves in turn could keep busy.  It is 25%: the waves also wait.
+// At head_dim 256 the bf16 kernels spill 44 to 46 registers (fp32 from 128 on 7 to 13): but for one, read in the loop over
+// tiles, each unit pays once.
 #include "attn_tiles.h"
 
 namespace w4a8 {
@@ -38,12 +42,16 @@ namespace {
 
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 
+// Query fragments of bf16 heads of 256 that stay in LDS.  None, 2 and 4: 2 x 2048 tokens on 14000 1547 to 1581, 1480
+// to 1485 and 1508 to 1512 us.
 constexpr int kQFar = 2;
 // What the compiler may move over the steps of the second product: vector and scalar arithmetic, so that
 // one half's weights fill the matrix core's time on the other's.
 constexpr int kSchedPV = 0x406;
 constexpr float kNoPage = 1e9f;
-constexpr int kMinTiles = 4;  // tiles a workgroup is worth cutting for
+// Tiles a workgroup is worth cutting for.  1, 4 and 8: 100 tokens on 1000 (32 / 8 heads of 128) 31.9, 32.2 and 36.1 us, 8 x 100
+// fresh ones 16.2, 17.5 and 26.2, longer calls alike.
+constexpr int kMinTiles = 4;
 
 template <int D, bool BF16>
 struct Shape {
@@ -54,7 +62,9 @@ struct Shape {
     static constexpr int RB = 32 * kWaves;
     static constexpr int T = 8192 / D;       // positions of a tile
     static constexpr int kGroups = T / 16;
-    // see Line: a unit's start and end cost some 7 us, a tile 2 (D 256: 1.3)
+    // see Line: a unit's start and end cost some 7 us, a tile 2 (D 256: 1.3).  kOver at 0, as it is, and at 10: 4096 tokens of
+    // 24 / 4 heads of 256 384, 284 and 286 us, 8192 of 64 500, 436 and 477, 5 ragged prompts of 128 438, 402 and 415.  kTail at 1, as it is,
+    // and at 6: 8192 of 64 445, 436 and 441, 100 on 1000 of 128 32.0, 32.2 and 36.0, 2 x 2048 on 14000 of 256 1502, 1482 and 1504.
     static constexpr int kOver = D == 256 ? 5 : 3, kTail = D == 256 ? 3 : 2;
     static constexpr int kRegs = D / 2;      // floats of O^T in a lane
     static constexpr int kWaveRecord = 64 * (kRegs + 4);    // a wave's piece: O^T, then m, E, L
@@ -122,7 +132,9 @@ struct Tile {
 template <int D, bool BF16, bool kSmall>
 __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves / 4)) void k_attn_prompt(AttnArgs a, int wgs) {
     using S = Shape<D, BF16>;
-    constexpr int kAhead = D == 128 ? 4 : 2;  // V fragments in flight
+    // K and V fragments in flight.  2 and 4: at D 256 (2 x 2048 tokens on 14000) 1482 and 1660 us, at D 128 (8 x 64 on 2000)
+    // 45.0 and 44.3, at D 64 436 and 436
+    constexpr int kAhead = D == 128 ? 4 : 2;
     constexpr int T = S::T, kParts = BF16 ? 1 : 2, kSteps = D / 16, kTiles = D / 32;
     constexpr int kQLds = D == 256 && BF16 ? kQFar : 0;  // query fragments that stay in LDS
     constexpr int kSubs = D == 256 ? 1 : 2, kWide = 32 * kSubs;   // positions of a softmax step: registers

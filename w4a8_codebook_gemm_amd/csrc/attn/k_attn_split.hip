@@ -9,8 +9,8 @@
 // With S^T's rows taken as the positions 8 (m / 4) + 4 u + m % 4 of tile u, a lane's eight
 // scores are those of eight consecutive positions of its row, which is the fragment the
 // second product wants: probabilities never leave their lane.  Codes become fp16 in
-// registers: K rows by bytes in order, V by a permute that transposes 2 tokens x 1 value, one
-// permute and one packed addition for two codes.  A wave takes 8192 / D positions at a time, the
+// registers: K rows by bytes in order, V by a permute that transposes 2 tokens x 1 value, one permute and
+// one packed addition (keys) or multiply-add (values) for two codes.  A wave takes 8192 / D positions at a time, the
 // next ones' codes (16 KiB) on their way while it works; queries lie in LDS, shared by the waves.
 //
 // The running maximum m and the exponent E are whole numbers: with e the exponent of a page's
@@ -22,8 +22,12 @@
 // lengths are; a workgroup's waves take its tiles in turn and join in LDS.  The pieces of a unit
 // that is cut are joined through the workspace (join_pieces).  Where units are many and alike, waves have whole ones instead.
 //
-// Measured (24 / 4 heads of 256, one token a sequence): 4 x 90k to 131k tokens 169 to 173 us, 5.6 TB/s of 6.0 that a
-// plain read reaches here; 32 x 300 to 16000 104 to 107 us, 5.0 TB/s; 64 x 4000 (32 / 8 of 128) 95 us, 5.5 TB/s.
+// Measured (24 / 4 heads of 256, one token a sequence): 4 x 90k to 131k tokens 170 to 175 us, 5.6 TB/s of 6.0 that a
+// plain read reaches here; 32 x 300 to 16000 103 to 107 us, 5.0 TB/s; 64 x 4000 (32 / 8 of 128) 95 us, 5.5 TB/s; fp32
+// 4 x 30k to 60k 85 us, 4.6 TB/s; blocks of 32 rows, 16 x 8 tokens on 4000 (32 / 8 of 128), 42 us, 3.1 TB/s.
+// Probabilities as two fp16 numbers for bf16 rows too are 2% slower on long contexts and 4 to 8% with more rows
+// (183 and 187 us, 43.8 and 47.0), for outputs that bf16 rounds to 2^-9.  At head_dim 256 the kernels spill
+// 8 to 17 registers, none of them in the loop over tiles: each unit pays for it once.
 // Between a workgroup's first tile and its join it streams at 6.3 TB/s; what is lost is starting and joining, some 12 us
 // a call: 1 x 777 tokens is 16.3 us, of them 1.6 the line, 1.4 finding the unit, 3.9 rows, pages and queries (each
 // waits for a read), 1.7 the tiles, 1.8 the waves' join and 2.2 the workgroups'.
@@ -76,8 +80,13 @@ __device__ __forceinline__ Work seq_work(const AttnArgs &a, int64_t b) {
     return w;
 }
 
+// Measured (us; 0, 16 and 32 tiles): 8 x 500 to 1000 tokens (32 / 8 heads of 128) 17.5, 14.5 and 14.4; 1 x 777 of 24 / 4 of
+// 256 20.6, 18.9 and 18.9; 16 x 8 tokens on 200 to 4000 49.1, 49.1 and 41.6; longer ones take no shares.
 constexpr int kMaxShare = 4 * kWaves;
-// See Line: a unit's start and end cost some 8 us, a workgroup's tile 1 (blocks of 16 rows) or 2.
+// See Line: a unit's start and end cost some 8 us, a workgroup's tile 1 (blocks of 16 rows) or 2.  kOver at 2, as it is, and at
+// 16: 32 ragged sequences 115, 113 and 111 us, 100 x 100 to 3000 tokens (32 / 8 of 128) 83, 77.5 and 80, 4 long ones 186, 183 and
+// 182; blocks of 32 rows, 32 x 16 tokens on 500 to 4000, 115, 106 and 93.  kTail at 1, 3 and 8: 112.5, 112.9 and 112.3 for the
+// ragged ones, 52, 49 and 49 for 16 x 8 tokens, 108, 106 and 104 for 32 x 16.
 template <int NB>
 constexpr int kOver = NB == 2 ? 4 : 8;
 constexpr int kTail = 3;
