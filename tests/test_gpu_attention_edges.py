@@ -226,3 +226,34 @@ def test_workspace_behind_its_counters_may_hold_anything(A, new, dtype):
         pytest.skip("the allocator gave other memory")
     assert int(ws[:A.COUNTER_BYTES].max()) == 0 and int(ws[A.COUNTER_BYTES:].min()) == 255
     assert torch.equal(A.kv_attention(q, cache, seqs, workspace=ws), want)
+
+
+@pytest.mark.parametrize("count,D", [(1, 64), (1, 256), (300, 64), (300, 128)])    # units cut over workgroups; whole ones for waves
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_small_probabilities_of_single_tokens(A, count, D, dtype):
+    """Two positions of a page, the second's probability 2^-18 to 2^-26 of the first's, whose value is 0: the output is the
+    second's value at that weight.  The first's weight stands at 2^12 or more, so the second's has an fp16 half step, 2^-11 of
+    itself or 2^-25: for fp32 queries two fp16 numbers, of which the second has the 2^-25."""
+    rng = np.random.default_rng(D)
+    b = Batch(A, rng, [1] * count, [2] * count, 16)
+    codes = [np.zeros((b.pages, 8, 16, D), np.int8) for _ in range(2)]
+    codes[0][:, :, 0, :64], codes[0][:, :, 1, :64] = 64, -64
+    codes[1][:, :, 1] = rng.integers(64, 128, (b.pages, 8, D))
+    scales = [np.full((b.pages, 8), 2.0 ** -6, np.float32), np.exp(rng.uniform(-2, 2, (b.pages, 8))).astype(np.float32)]
+    cache = A.KVCache(dev(codes[0]), dev(codes[1]), dev(scales[0]), dev(scales[1]))
+    gap = rng.uniform(18, 26, (count, 16)).astype(np.float32)       # in powers of two: 128 q sm_scale log2 e
+    q = dev(np.repeat(gap[:, :, None] / 128, D, 2), dtype)
+    sm = float(np.log(2))
+    out = f64(A.kv_attention(q, cache, b.seqs(), scale=sm))
+    gap = f64(q)[:, :, 0] * 128
+    head = np.repeat(np.arange(8), 2)
+    page = b.table[:, 0]
+    p = 1 / (1 + 2.0 ** gap)
+    value = codes[1][page][:, head, 1].astype(np.float64)
+    sv = scales[1][page][:, head].astype(np.float64)[:, :, None]
+    ref = p[:, :, None] * value * sv
+    relative = (2.0 ** -22 if dtype == F32 else 2.0 ** -11) + (D + 16) * T.U * 27 + 80 * T.U
+    bound = relative * ref + 2.0 ** -37 * value * sv
+    bound = bound + T.half_step(dtype) * (ref + bound)
+    err = np.abs(out - ref)
+    assert np.all(err <= bound), float((err / bound).max())
