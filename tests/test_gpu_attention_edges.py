@@ -257,3 +257,25 @@ def test_small_probabilities_of_single_tokens(A, count, D, dtype):
     bound = bound + T.half_step(dtype) * (ref + bound)
     err = np.abs(out - ref)
     assert np.all(err <= bound), float((err / bound).max())
+
+
+@pytest.mark.parametrize("new,dtype", [([1, 1, 1], BF), ([6, 9, 2], BF), ([200, 30, 90], F32)])
+def test_captured_without_a_workspace_of_its_own(A, new, dtype):
+    """The graph zeroes its counters at every replay and follows lengths that change between them."""
+    rng = np.random.default_rng(8)
+    b = Batch(A, rng, new, [1500, 700, 900], 32, extra_width=0)
+    _, _, cache = random_cache(A, rng, b.pages, 2, 32, 64)
+    q, seqs = dev(rng.standard_normal((b.M, 8, 64)).astype(np.float32), dtype), b.seqs()
+    A.kv_attention(q, cache, seqs)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = A.kv_attention(q, cache, seqs)
+    for turn in range(5):
+        seqs.seq_lens.copy_(dev(rng.integers(1, 690, 3).astype(np.int32)))
+        q.copy_(dev(rng.standard_normal(q.shape).astype(np.float32), dtype))
+        graph.replay()
+        want = A.kv_attention(q, cache, seqs)
+        if turn % 2:
+            torch.cuda.synchronize()
+        assert torch.equal(out, want), turn
