@@ -279,3 +279,19 @@ def test_captured_without_a_workspace_of_its_own(A, new, dtype):
         if turn % 2:
             torch.cuda.synchronize()
         assert torch.equal(out, want), turn
+
+
+@pytest.mark.parametrize("new,lens,rows_behind", [
+    ([1] * 30 + [500], list(range(100, 700, 20)) + [500], 0),          # single tokens in the prompt kernel
+    ([1] * 70 + [300] + [1] * 5, list(range(20, 370, 5)) + [420] + [200] * 5, 7),    # a prompt in blocks of 32 rows
+    ([1] * 90 + [120], [150] * 90 + [120], 0),                         # a prompt in blocks of 16 rows
+    ([40, 0, 0, 0, 3] + [0] * 60, [200, 30, 0, 1, 90] + [0] * 60, 0),  # sequences without a token lower the average
+    ([1, 1, 2], [300, 200, 100], 200),                                 # rows behind them raise it
+])
+@pytest.mark.parametrize("dtype,D", [(BF, 128), (F32, 64), (BF, 256)])
+def test_batches_of_unlike_sequences(A, new, lens, rows_behind, dtype, D):
+    rng = np.random.default_rng(len(new) + D)
+    b = Batch(A, rng, new, lens, 32, rows_behind=rows_behind)
+    codes, scales, cache = random_cache(A, rng, b.pages, 2, 32, D)
+    q = dev((0.3 * rng.standard_normal((b.M, 8, D))).astype(np.float32), dtype)
+    T.check_attention(A, q, b, codes, scales, cache)
