@@ -150,9 +150,10 @@ W4A8_API int64_t w4a8_kv_attention_workspace_bytes(int64_t M, int64_t B, int q_h
  * head h reads cache head h / (q_heads / kv_heads).  Rows of o that belong to no sequence are
  * left as they were.  One kernel serves a call; which one goes by M * (q_heads / kv_heads) / B, the rows a
  * sequence has on average.  Any mix of sequences is right, but a batch of single tokens beside a long prompt
- * takes up to twice the time of two calls, and rows behind the last sequence or many sequences without a
- * token may choose the slower kernel.  Where a query is not finite, or a scale of a page that it sees is negative or not
- * finite, that row of o has no meaning; other rows, and rows that do not see the page, are not touched by it.
+ * may take twice the time of two calls, and rows behind the last sequence or many sequences without a
+ * token may choose the slower kernel.  Where a query is not finite, or a scale of a page that it sees is
+ * negative or not finite, that row of o has no meaning; other rows, and rows that do not see the page, are
+ * not touched by it.
  *
  *  q         [M] tokens of q_heads * head_dim consecutive values, q_stride elements apart (a
  *            multiple of 8), element type dtype;  1 <= M <= 2^24, M * q_heads < 2^31

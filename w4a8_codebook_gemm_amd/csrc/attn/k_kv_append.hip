@@ -15,8 +15,9 @@
 //
 // Bound by HBM with long prompts: 2 or 4 bytes read and one written a value; bf16 3.4 TB/s over launches of 50 and of
 // 100 MB (14 to 15 and 29 us), fp32 4.0 over 84 MB (18.5 to 21 us), where a copy runs at 4.75.  Some 4 us are the start,
-// the rest is each team's chain: its page number is waited for before its tokens are asked for.  Bound by latency with single tokens: 4.5 us for 61 sequences, of them the chain of reads from the
-// sequence to its page, the scale and the token.
+// the rest is each team's chain: its page number is waited for before its tokens are asked for.  Bound by
+// latency with single tokens: 4.5 us for 61 sequences, of them the chain of reads from the sequence to its
+// page, the scale and the token.
 //
 // Which page a team has is found on the device, where the lengths are: every wave runs
 // the sequences' page counts through a prefix sum, 64 at a time, until its job's is reached.  The waves are as many as the
