@@ -228,11 +228,77 @@ __device__ __forceinline__ bool join_pieces(uint32_t *counters, int64_t w_first,
 
 // The positions [from, to) that new token i of a sequence sees: none in front of position 0.  Both ends
 // grow with i, so a block's first token has the least of them and its last token the greatest.
-__device__ __forceinline__ void sees(const AttnArgs &a, const Seq &q, int64_t i, int &from, int &to) {
+template <class Args>
+__device__ __forceinline__ void sees(const Args &a, const Seq &q, int64_t i, int &from, int &to) {
     const int64_t pos = q.pos0 + i;
     const int64_t f = a.window ? pos - a.window + 1 : 0;
     from = f > 0 ? (int)f : 0;
     to = pos < 0 ? 0 : a.causal ? (int)(pos + 1) : q.len;
+}
+
+// How a sequence contributes to the line of tiles where rows are few: blocks of RB of them.
+struct Work {
+    Seq q;
+    int lo, tiles;   // first tile, tiles of each unit
+    int64_t units;
+};
+
+template <int RB, int T, class Args>
+__device__ __forceinline__ Work seq_work(const Args &a, int64_t b) {
+    Work w{};
+    if (b >= a.s.B) return w;
+    w.q = load_seq(a.s, a.M, a.page_shift, b);
+    if (w.q.n > 0) {
+        if (a.window && (int64_t)w.q.pos0 - a.window + 1 > 0) w.lo = (int)(w.q.pos0 - a.window + 1) / T;
+        w.tiles = tiles_to<T>(w.q.len) - w.lo;
+        if (w.tiles < 1) w.tiles = 1;  // rows that see nothing are still written
+        w.units = ((int64_t)w.q.n * a.group + RB - 1) / RB * a.c.kv_heads;
+    }
+    return w;
+}
+
+// A unit's places on the line: its tiles and what it costs beside them, or where workgroups are many a
+// whole number of their shares.
+__device__ __forceinline__ int on_line(int tiles, int share, int over) { return share ? (tiles + share - 1) / share * share : tiles + over; }
+
+// Where rows are many: first tile and tiles of row block rb of a sequence, S a prompt kernel's shape.
+template <class S, class Args>
+__device__ __forceinline__ int block_tiles(const Args &a, const Seq &q, int64_t rb, int &first) {
+    const int64_t rows = (int64_t)q.n * a.group, r0 = rb * S::RB;
+    const int64_t last = (r0 + S::RB < rows ? r0 + S::RB : rows) - 1;
+    int lo, hi, x;
+    sees(a, q, div64(r0, a.group), lo, x);
+    sees(a, q, div64(last, a.group), x, hi);
+    first = lo / S::T;
+    const int n = tiles_to<S::T>(hi) - first;
+    return n < 1 ? 1 : n;  // rows that see nothing are still written
+}
+
+template <class S, class Args>
+__device__ __forceinline__ int64_t blocks_of(const Args &a, const Seq &q) {
+    return div64((int64_t)q.n * a.group + S::RB - 1, S::RB);
+}
+
+// Places of sequence b0 + lane on the line.  Called by whole waves: sequences of many blocks are
+// summed by all lanes together.
+template <class S, class Args>
+__device__ __forceinline__ int64_t seq_tiles(const Args &a, int64_t b0, int lane) {
+    Seq q{0, 0, 0, 0};
+    if (b0 + lane < a.s.B) q = load_seq(a.s, a.M, a.page_shift, b0 + lane);
+    const int64_t blocks = blocks_of<S>(a, q);
+    int64_t tiles = 0;
+    int x;
+    for (int64_t i = 0; i < (blocks <= 4 ? blocks : 0); i++) tiles += block_tiles<S>(a, q, i, x) + S::kOver;
+    for (uint64_t many = __ballot(blocks > 4); many; many &= many - 1) {
+        const int src = __ffsll((unsigned long long)many) - 1;
+        const Seq r = {0, lane_value(q.n, src), lane_value(q.len, src), lane_value(q.pos0, src)};
+        const int64_t rb = blocks_of<S>(a, r);
+        int64_t sum = 0;
+        for (int64_t i = lane; i < rb; i += 64) sum += block_tiles<S>(a, r, i, x) + S::kOver;
+        sum = lane_value(scan64(sum), 63);
+        if (lane == src) tiles = sum;
+    }
+    return tiles * a.c.kv_heads;
 }
 
 }  // namespace w4a8

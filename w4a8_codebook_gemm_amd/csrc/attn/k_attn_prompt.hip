@@ -71,47 +71,6 @@ struct Shape {
     static constexpr int kRecord = kWaves * kWaveRecord;
 };
 
-// First tile and tiles of row block rb of a sequence.
-template <int D, bool BF16>
-__device__ __forceinline__ int block_tiles(const AttnArgs &a, const Seq &q, int64_t rb, int &first) {
-    using S = Shape<D, BF16>;
-    const int64_t rows = (int64_t)q.n * a.group, r0 = rb * S::RB;
-    const int64_t last = (r0 + S::RB < rows ? r0 + S::RB : rows) - 1;
-    int lo, hi, x;
-    sees(a, q, div64(r0, a.group), lo, x);
-    sees(a, q, div64(last, a.group), x, hi);
-    first = lo / S::T;
-    const int n = tiles_to<S::T>(hi) - first;
-    return n < 1 ? 1 : n;  // rows that see nothing are still written
-}
-
-template <int D, bool BF16>
-__device__ __forceinline__ int64_t blocks_of(const AttnArgs &a, const Seq &q) {
-    return div64((int64_t)q.n * a.group + Shape<D, BF16>::RB - 1, Shape<D, BF16>::RB);
-}
-
-// Places of sequence b0 + lane on the line.  Called by whole waves: sequences of many blocks are
-// summed by all lanes together.
-template <int D, bool BF16>
-__device__ __forceinline__ int64_t seq_tiles(const AttnArgs &a, int64_t b0, int lane) {
-    Seq q{0, 0, 0, 0};
-    if (b0 + lane < a.s.B) q = load_seq(a.s, a.M, a.page_shift, b0 + lane);
-    const int64_t blocks = blocks_of<D, BF16>(a, q);
-    int64_t tiles = 0;
-    int x;
-    for (int64_t i = 0; i < (blocks <= 4 ? blocks : 0); i++) tiles += block_tiles<D, BF16>(a, q, i, x) + Shape<D, BF16>::kOver;
-    for (uint64_t many = __ballot(blocks > 4); many; many &= many - 1) {
-        const int src = __ffsll((unsigned long long)many) - 1;
-        const Seq r = {0, lane_value(q.n, src), lane_value(q.len, src), lane_value(q.pos0, src)};
-        const int64_t rb = blocks_of<D, BF16>(a, r);
-        int64_t sum = 0;
-        for (int64_t i = lane; i < rb; i += 64) sum += block_tiles<D, BF16>(a, r, i, x) + Shape<D, BF16>::kOver;
-        sum = lane_value(scan64(sum), 63);
-        if (lane == src) tiles = sum;
-    }
-    return tiles * a.c.kv_heads;
-}
-
 // The tiles in LDS.  Rows are 16 bytes longer than their values, so that the same 16-byte slot of
 // eight consecutive rows touches all banks, and every fragment is one address plus a constant.
 //   K: a row for each position; its 8-value slots even ones first, then odd ones (a staging thread
@@ -154,7 +113,7 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
 
     int64_t line = 0;
     for (int64_t b0 = 0; b0 < a.s.B; b0 += 64) {
-        const int64_t mine = seq_tiles<D, BF16>(a, b0, lane), incl = scan64(mine);
+        const int64_t mine = seq_tiles<S>(a, b0, lane), incl = scan64(mine);
         line += lane_value(incl, 63);
         if (a.s.B <= 64) {  // every wave writes the same and reads its own
             s_mine[lane] = mine;
@@ -176,7 +135,7 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
         // the sequence, cache head and row block that tile `at` is in
         int64_t base = from_base, b = 0, per_head = 0;
         for (int64_t b0 = from; b0 < a.s.B; b0 += 64) {
-            const int64_t mine = a.s.B <= 64 ? s_mine[lane] : seq_tiles<D, BF16>(a, b0, lane);
+            const int64_t mine = a.s.B <= 64 ? s_mine[lane] : seq_tiles<S>(a, b0, lane);
             const int64_t incl = a.s.B <= 64 ? s_incl[lane] : scan64(mine);
             const int64_t sum = lane_value(incl, 63);
             if (at < base + sum) {
@@ -191,13 +150,13 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
             base += sum;
         }
         const Seq q = load_seq(a.s, a.M, a.page_shift, b);
-        const int64_t blocks = blocks_of<D, BF16>(a, q);
+        const int64_t blocks = blocks_of<S>(a, q);
         const int h = (int)div64(at - base, per_head);
         int64_t unit0 = base + h * per_head, rb = 0;  // the unit's first tile on the line
         int first_tile = 0, tiles = 1;
         for (int64_t r = 0; r < blocks; r += 64) {
             int f = 0, c = 0;
-            if (r + lane < blocks) c = block_tiles<D, BF16>(a, q, r + lane, f);
+            if (r + lane < blocks) c = block_tiles<S>(a, q, r + lane, f);
             const int64_t place = r + lane < blocks ? c + S::kOver : 0;
             const int64_t incl = scan64(place), sum = lane_value(incl, 63);
             if (at < unit0 + sum) {

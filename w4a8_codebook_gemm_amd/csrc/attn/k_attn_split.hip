@@ -59,27 +59,6 @@ template <int NB>
 constexpr int kPerCu = NB == 2 ? 1 : 2;
 constexpr int kRadix = 8;        // pieces that join at a node
 
-// How a sequence contributes to the line of tiles.
-struct Work {
-    Seq q;
-    int lo, tiles;   // first tile, tiles of each unit
-    int64_t units;
-};
-
-template <int RB, int T>
-__device__ __forceinline__ Work seq_work(const AttnArgs &a, int64_t b) {
-    Work w{};
-    if (b >= a.s.B) return w;
-    w.q = load_seq(a.s, a.M, a.page_shift, b);
-    if (w.q.n > 0) {
-        if (a.window && (int64_t)w.q.pos0 - a.window + 1 > 0) w.lo = (int)(w.q.pos0 - a.window + 1) / T;
-        w.tiles = tiles_to<T>(w.q.len) - w.lo;
-        if (w.tiles < 1) w.tiles = 1;  // rows that see nothing are still written
-        w.units = ((int64_t)w.q.n * a.group + RB - 1) / RB * a.c.kv_heads;
-    }
-    return w;
-}
-
 // Measured (us; 0, 16 and 32 tiles): 8 x 500 to 1000 tokens (32 / 8 heads of 128) 17.5, 14.5 and 14.4; 1 x 777 of 24 / 4 of
 // 256 20.6, 18.9 and 18.9; 16 x 8 tokens on 200 to 4000 49.1, 49.1 and 41.6; longer ones take no shares.
 constexpr int kMaxShare = 4 * kWaves;
@@ -96,10 +75,6 @@ constexpr int kTail = 3;
 // tokens 54 and 40 us, 256 x 500 to 2000 143 and 154, 512 of them 259 and 272, 1024 510 and 510, 256 x 2000 194 and
 // 185, fp32 512 x 300 to 900 178 and 155.  kSoloOver: as kOver.
 constexpr int kSoloOver = 2;
-
-// A unit's places on the line: its tiles and what it costs beside them, or where workgroups are many a
-// whole number of their shares.
-__device__ __forceinline__ int on_line(int tiles, int share, int over) { return share ? (tiles + share - 1) / share * share : tiles + over; }
 
 template <int D, int NB>
 struct Layout {
