@@ -1,6 +1,7 @@
-"""Compile the HIP sources for gfx950 into two shared libraries: csrc/ into libw4a8.so (the
-quantised layer, exporting the C ABI declared in include/w4a8.h) and csrc/attn/ into
-libw4a8_attn.so (the attention operators, include/w4a8_attn.h).
+"""Compile the HIP sources for gfx950 into three shared libraries: csrc/ into libw4a8.so (the
+quantised layer, exporting the C ABI declared in include/w4a8.h), csrc/attn/ into
+libw4a8_attn.so (the attention operators, include/w4a8_attn.h) and csrc/serve/ into
+libw4a8_serve.so (the serving operators, include/w4a8_serve.h).
 
 Each source is compiled to an object in _build/ (in parallel), then linked.
 """
@@ -19,6 +20,8 @@ BUILD = os.path.join(ROOT, "_build", "w4a8")
 LIB = os.path.join(PKG, "libw4a8.so")
 ATTN_CSRC = os.path.join(CSRC, "attn")
 ATTN_LIB = os.path.join(PKG, "libw4a8_attn.so")
+SERVE_CSRC = os.path.join(CSRC, "serve")
+SERVE_LIB = os.path.join(PKG, "libw4a8_serve.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -40,6 +43,10 @@ def sources():
 
 def attn_sources():
     return sorted(glob.glob(os.path.join(ATTN_CSRC, "*.hip")))
+
+
+def serve_sources():
+    return sorted(glob.glob(os.path.join(SERVE_CSRC, "*.hip")))
 
 
 def _compile(src: str, verbose: bool) -> str:
@@ -66,7 +73,7 @@ def _link(objs, lib: str, verbose: bool) -> None:
 
 def build(verbose: bool = False, jobs: int = 8) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    parts = [(sources(), LIB), (attn_sources(), ATTN_LIB)]
+    parts = [(sources(), LIB), (attn_sources(), ATTN_LIB), (serve_sources(), SERVE_LIB)]
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
         futs = [[ex.submit(_compile, s, verbose) for s in srcs] for srcs, _ in parts]
         objs = [[f.result() for f in fs] for fs in futs]

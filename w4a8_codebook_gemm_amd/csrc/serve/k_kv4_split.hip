@@ -1,0 +1,601 @@
+// Attention over the paged cache in 4 bits for few query rows a sequence (decode).
+//
+//   o = sum_t p_t v_t / sum_t p_t,  p_t = exp2(s_t - m),  s_t = scale log2(e) q . k_t
+//
+// HBM bound: 9/16 of a byte a cached value, read once for the few query rows that share its head.
+// Rows, products and their layout are the int8 cache's (k_attn_split.hip): the (token, query
+// head) pairs of one sequence and one cache head are the columns of v_mfma_f32_16x16x32_f16,
+//   S^T [32 positions x 16 rows] = K [positions x D] Q^T,   O^T [D x 16] += V^T P^T,
+// with S^T's rows taken as the positions 8 (m / 4) + 4 u + m % 4 of tile u, so that probabilities
+// never leave their lane.  Fragments are exact (kv4_tiles.h).  A lane has D / 4 consecutive values of
+// a key, so its scale bytes lie together, and D / 16 consecutive values of eight tokens, which are
+// one scale group: its eight scale bytes lie together too.  Two tokens' codes are put side by side
+// before they become fp16, which is what turns rows of tokens into a fragment.
+//
+// The unit of a head is a factor of the scores and of the output, so a row's scores need no factor of
+// their own and the only statistic is the running maximum m, a whole number: rescaling is exact.
+//
+// Split: as in the int8 kernel, the tiles of all units form one line that is cut evenly over the
+// workgroups; a workgroup's waves take its tiles in turn and join in LDS, and pieces of a cut unit
+// through the workspace (join_pieces).
+#include <type_traits>
+
+#include "kv4_tiles.h"
+
+namespace w4a8 {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+template <int NB>
+constexpr int kPerCu = NB == 2 ? 1 : 2;  // workgroups on a compute unit
+constexpr int kRadix = 8;                // pieces that join at a node
+constexpr int kMaxShare = 4 * kWaves;
+template <int NB>
+constexpr int kOver = NB == 2 ? 4 : 8;
+constexpr int kTail = 3;
+
+template <int D, int NB>
+struct Layout {
+    static constexpr int RB = 16 * NB;
+    static constexpr int kSumRows = 4 * kThreads / D;   // rows that join at a time, four values of one a thread
+    static constexpr int kItems = RB / kSumRows;
+    static constexpr int kRecord = kItems * kThreads * 4 + RB * 4;  // floats of a piece: each thread's values, each row's state
+    static constexpr int kRow = D + 4;                  // LDS row, padded
+    static constexpr int kLds = kWaves * kSumRows * kRow;  // floats
+};
+
+// Bytes that a lane reads of a key's scales and of a value's codes.
+template <int N>
+struct Bytes;
+template <> struct Bytes<1> { typedef uint8_t type; };
+template <> struct Bytes<2> { typedef uint16_t type; };
+template <> struct Bytes<4> { typedef uint32_t type; };
+template <> struct Bytes<8> { typedef uint2 type; };
+template <int N>
+__device__ __forceinline__ typename Bytes<N>::type load_bytes(const uint8_t *p) {
+    return *reinterpret_cast<const typename Bytes<N>::type *>(p);
+}
+
+template <int D, int NB, bool BF16>
+__global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a, int wgs) {
+    using Lay = Layout<D, NB>;
+    constexpr int RB = Lay::RB;
+    constexpr int U = D == 64 ? 4 : 2, T = 32 * U;  // 32-position parts of a tile
+    constexpr int kParts = BF16 ? 1 : 2;   // fp16 numbers that make a query value or a probability
+    constexpr int kS = D / 32;             // dwords of a key in a lane, steps of the first product
+    constexpr int kT = D / 16;             // tiles of O^T
+    constexpr int kVB = D / 32;            // bytes of a value row in a lane
+    constexpr int kVW = kVB < 4 ? 1 : kVB / 4;  // dwords they are held in
+    __shared__ __attribute__((aligned(16))) float s_o[Lay::kLds];
+    constexpr int kQ = NB * kParts * kS * 64;  // fragments of a unit's queries
+    __shared__ half8_t s_q[kQ];
+    __shared__ float s_m[kWaves][RB], s_l[kWaves][RB];
+    __shared__ float2 s_all[RB];
+    __shared__ int s_flag;
+    const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4, wave = tid >> 6;
+    uint32_t *counters = static_cast<uint32_t *>(a.ws);
+    float *pieces = reinterpret_cast<float *>(static_cast<char *>(a.ws) + kAttnCounterBytes);
+
+    // the line's length, and this workgroup's part of it: while a part is not more than kMaxShare tiles, units
+    // are cut into whole shares of that many tiles, each a workgroup's, if there are workgroups enough
+    Work x = seq_work<RB, T>(a, lane);
+    auto total = [&](int share, int over, int64_t &units) {
+        int64_t sum = 0;
+        units = 0;
+        for (int64_t b0 = 0; b0 < a.s.B; b0 += 64) {
+            if (a.s.B > 64) x = seq_work<RB, T>(a, b0 + lane);
+            sum += lane_value(scan64(x.units * on_line(x.tiles, share, over)), 63);
+            units += lane_value(scan64(x.units), 63);
+        }
+        return sum;
+    };
+    int64_t units, none;
+    int64_t line = total(0, 0, units);
+    if (line == 0) return;
+    int share = 0;
+    for (int64_t c = div64(line + (int64_t)wgs * kWaves - 1, (int64_t)wgs * kWaves) * kWaves; c <= kMaxShare && share == 0; c += kWaves) {
+        const int64_t sum = total((int)c, 0, none);
+        if (sum <= (int64_t)wgs * c) {
+            share = (int)c;
+            line = sum;
+        }
+    }
+    const int over = share == 0 && (NB == 1 || units >= wgs) ? kOver<NB> : 0;
+    line += over * units;
+    const int64_t used = share ? div64(line, share) : wgs, w = blockIdx.x;
+    if (w >= used) return;
+    const Line cut{line, used, over, share ? 1 : kTail};
+    const int64_t t1 = cut.begin(w + 1);
+
+    int64_t from = 0, from_base = 0, held = -1;  // the 64 sequences that the last unit was in, their place; those in x
+    for (int64_t at = cut.begin(w); at < t1;) {
+        // the sequence and unit that tile `at` is in
+        int64_t base = from_base, b = 0;
+        int lo_tile = 0, tiles = 1;
+        Seq q{0, 0, 0, 0};
+        for (int64_t b0 = from; b0 < a.s.B; b0 += 64) {
+            if (a.s.B > 64 && b0 != held) x = seq_work<RB, T>(a, b0 + lane);
+            held = b0;
+            const int64_t mine = x.units * on_line(x.tiles, share, over), incl = scan64(mine), sum = lane_value(incl, 63);
+            if (at < base + sum) {
+                const int src = __ffsll((unsigned long long)__ballot(at - base < incl)) - 1;
+                from = b0;
+                from_base = base;
+                b = b0 + src;
+                base += lane_value(incl - mine, src);
+                lo_tile = lane_value(x.lo, src);
+                tiles = lane_value(x.tiles, src);
+                q.first = lane_value(x.q.first, src);
+                q.n = lane_value(x.q.n, src);
+                q.len = lane_value(x.q.len, src);
+                q.pos0 = q.len - q.n;
+                break;
+            }
+            base += sum;
+        }
+        const int length = on_line(tiles, share, over);
+        const int64_t unit = div64(at - base, length);
+        const int64_t unit0 = base + unit * length;         // the unit's first tile on the line
+        const int64_t unit1 = unit0 + length;
+        int tile0, tile1;
+        if (!cut.part(at, t1, unit0, unit1, tiles, tile0, tile1)) {
+            at = unit1;
+            continue;
+        }
+        const int rblock = (int)div64(unit, a.c.kv_heads);
+        const int h = (int)(unit - (int64_t)rblock * a.c.kv_heads);
+
+        // this lane's rows; a sequence's rows are fewer than 2^31
+        const int r0 = rblock * RB;
+        const int nrows = q.n * a.group - r0 < RB ? q.n * a.group - r0 : RB;
+        int lo[NB], hi[NB];
+        float fac[NB];
+        auto row_at = [&](int r, int &token, int &head) {  // row r < nrows of the block
+            token = (uint32_t)(r0 + r) / (uint32_t)a.group;
+            head = h * a.group + (r0 + r - token * a.group);
+        };
+        // queries, all of a row's values of this lane at once, before the codes are asked for
+        RawQ<BF16> raw[NB][kS];
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++) {
+            const int r = 16 * nb + n < nrows ? 16 * nb + n : nrows - 1;
+            int token, head;
+            row_at(r, token, head);
+            sees(a, q, token, lo[nb], hi[nb]);
+            if (r != 16 * nb + n) hi[nb] = 0;
+            const int64_t off = (q.first + token) * a.q_stride + head * D + g * (D / 4);
+#pragma unroll
+            for (int c = 0; c < kS; c++) raw[nb][c].load(a.q, off + 8 * c);
+        }
+        // positions that all rows of the block see, and that any does
+        int all_lo, all_hi, any_lo, any_hi;
+        {
+            int t_first, t_last, hd;
+            row_at(0, t_first, hd);
+            row_at(nrows - 1, t_last, hd);
+            sees(a, q, t_first, any_lo, all_hi);
+            sees(a, q, t_last, all_lo, any_hi);
+        }
+
+        const int end = lo_tile + tile1;
+        int first = lo_tile + tile0 + wave;
+        if (first < any_lo / T) first += (any_lo / T - first + kWaves - 1) / kWaves * kWaves;
+        const int stop = end < tiles_to<T>(any_hi) ? end : tiles_to<T>(any_hi);
+        const int P = a.c.page_size, pm = P - 1;
+        const bool small = a.page_shift == 4;  // two pages in 32 positions
+        const int32_t *table = a.s.page_table + b * a.s.table_width;
+
+        auto page_of = [&](int t) {  // page of position t, -1 past the end
+            return t < q.len ? table[t >> a.page_shift] : -1;
+        };
+        auto block_of = [&](int page) {  // its block of this head; a page that is not there reads page 0, masked
+            return (int64_t)((uint32_t)page < (uint32_t)a.c.num_pages ? page : 0) * a.c.kv_heads + h;
+        };
+        uint32_t kr[U][2][kS], kc[U][2], vr[U][8][kVW];
+        uint2 vc[U];
+        int pk[U], ps[U];       // pages of the tile to load next, of this lane's key row and of its positions
+        uint32_t there = 0;     // of the tile in hand: bit x where part x's page of this lane's positions is there
+        auto find_pages = [&](int tile) {
+            const int l = fresh(lane);
+#pragma unroll
+            for (int x = 0; x < U; x++) {
+                const int t = tile * T + 32 * x;
+                pk[x] = page_of(t + (small ? 2 * (l & 8) : 0));
+                ps[x] = page_of(t + (small ? (l & 32) >> 1 : 0));
+            }
+        };
+        auto load_k = [&](int tile) {
+            const int l = fresh(lane);
+#pragma unroll
+            for (int x = 0; x < U; x++) {
+                const int64_t row = block_of(pk[x]) * P + ((tile * T + 32 * x + 2 * (l & 12) + (l & 3)) & pm);
+                const uint8_t *p = a.c.k + row * (D / 2) + (l >> 4) * (D / 8), *s = a.c.k_scale + row * (D / 16) + (l >> 4) * (D / 64);
+#pragma unroll
+                for (int u = 0; u < 2; u++) {
+                    const uint8_t *pu = p + u * 4 * (D / 2);
+                    if constexpr (D >= 128) {
+#pragma unroll
+                        for (int c = 0; c < kS; c += 4) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(pu + 4 * c);
+                            kr[x][u][c] = v.x; kr[x][u][c + 1] = v.y; kr[x][u][c + 2] = v.z; kr[x][u][c + 3] = v.w;
+                        }
+                    } else {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(pu);
+                        kr[x][u][0] = v.x;
+                        kr[x][u][1] = v.y;
+                    }
+                    kc[x][u] = load_bytes<D / 64>(s + u * 4 * (D / 16));
+                }
+            }
+        };
+        auto load_v = [&](int tile) {
+            const int l = fresh(lane);
+#pragma unroll
+            for (int x = 0; x < U; x++) {
+                const int64_t blk = block_of(ps[x]);
+                const int slot = (tile * T + 32 * x + (l >> 4) * 8) & pm;
+                const uint8_t *p = a.c.v + (blk * P + slot) * (D / 2) + (l & 15) * kVB;
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    if constexpr (kVB == 8) {
+                        const uint2 v = load_bytes<8>(p + j * (D / 2));
+                        vr[x][j][0] = v.x;
+                        vr[x][j][kVW - 1] = v.y;
+                    } else {
+                        vr[x][j][0] = load_bytes<kVB>(p + j * (D / 2));
+                    }
+                }
+                vc[x] = load_bytes<8>(a.c.v_scale + (blk * (D / 16) + (l & 15) * (D / 16) / 16) * P + slot);
+            }
+        };
+        auto set_there = [&]() {
+            uint32_t t = 0;
+#pragma unroll
+            for (int x = 0; x < U; x++) t |= (uint32_t)((uint32_t)ps[x] < (uint32_t)a.c.num_pages) << x;
+            return t;
+        };
+        uint32_t next_there = 0;
+        if (first < stop) {
+            find_pages(first);
+            next_there = set_there();
+            load_k(first);
+            load_v(first);
+            if (first + kWaves < stop) find_pages(first + kWaves);
+        }
+
+        // queries as fp16, into LDS: fragment (block, part, step) as its lanes read it; zeros behind the rows
+        int k_exp;
+        const float k_part = frexpf(a.c.k_unit[h], &k_exp);
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++) {
+            float top = 0.0f;
+#pragma unroll
+            for (int c = 0; c < kS; c++) {
+                float v[8];
+                raw[nb][c].values(v);
+#pragma unroll
+                for (int i = 0; i < 8; i++) top = fmaxf(top, fabsf(v[i]));
+            }
+            if (16 * nb + n >= nrows) top = 0.0f;
+            top = max_xor32(max_xor16(top));
+            // the row's largest value at 2^13 .. 2^14: bf16 values are then exact in fp16 down
+            // to 2^-28 of it (fp32 as two fp16 numbers to 2^-22 relative), below off by 2^-39
+            int ex = 0;
+            if (top > 0.0f) frexpf(top, &ex);
+            fac[nb] = fmaxf(ldexpf(fabsf(a.scale) * kLog2e * k_part, ex + k_exp - 14 + kValueExp), 0x1p-126f);
+            if (wave == nb) {
+#pragma unroll
+                for (int c = 0; c < kS; c++) {
+                    half8_t q0, q1;
+                    float v[8];
+                    raw[nb][c].values(v);
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        const float y = 16 * nb + n < nrows ? ldexpf(a.scale < 0.0f ? -v[i] : v[i], 14 - ex) : 0.0f;
+                        q0[i] = (_Float16)y;
+                        q1[i] = (_Float16)(y - (float)(_Float16)y);
+                    }
+                    s_q[(nb * kParts * kS + c) * 64 + lane] = q0;
+                    if constexpr (kParts == 2) s_q[((nb * kParts + 1) * kS + c) * 64 + lane] = q1;
+                }
+            }
+        }
+        __syncthreads();
+
+        floatx4 o[NB][kT];
+        float m[NB], L[NB];
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++) {
+            m[nb] = kLow;
+            L[nb] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kT; i++) o[nb][i] = floatx4{0, 0, 0, 0};
+        }
+        for (int tile = first; tile < stop; tile += kWaves) {
+            const bool more = tile + kWaves < stop;
+            floatx4 s[NB][U][2];
+#pragma unroll
+            for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                for (int x = 0; x < U; x++) s[nb][x][0] = s[nb][x][1] = floatx4{0, 0, 0, 0};
+            const half8_t *qp = s_q + fresh(lane);
+#pragma unroll
+            for (int c = 0; c < kS; c++) {
+                half8_t qf[NB][kParts];
+#pragma unroll
+                for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                    for (int pt = 0; pt < kParts; pt++) qf[nb][pt] = qp[((nb * kParts + pt) * kS + c) * 64];
+#pragma unroll
+                for (int x = 0; x < U; x++)
+#pragma unroll
+                    for (int u = 0; u < 2; u++) {
+                        // 16 values a scale: two dwords
+                        const half2_t sc = c < 2 ? scale_both<0>(kc[x][u]) : c < 4 ? scale_both<1>(kc[x][u]) : c < 6 ? scale_both<2>(kc[x][u]) : scale_both<3>(kc[x][u]);
+                        const half8_t k = values_natural(kr[x][u][c], sc);
+#pragma unroll
+                        for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                            for (int pt = 0; pt < kParts; pt++)
+                                s[nb][x][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qf[nb][pt], s[nb][x][u], 0, 0, 0);
+                    }
+            }
+            there = next_there;
+            if (more) {
+                next_there = set_there();
+                load_k(tile + kWaves);
+            }
+            const bool whole = tile * T >= all_lo && all_hi - tile * T >= T && __all(there == (1u << U) - 1);
+            half8_t pf[NB][U][kParts];
+#pragma unroll
+            for (int nb = 0; nb < NB; nb++) {
+                if (!whole) {
+#pragma unroll
+                    for (int y = 0; y < U; y++) {
+                        const int t = tile * T + 32 * y + 8 * g;
+                        const bool ok = there >> y & 1;
+#pragma unroll
+                        for (int j = 0; j < 8; j++) {
+                            const bool see = ok & (t + j >= lo[nb]) & (t + j < hi[nb]);
+                            s[nb][y][j >> 2][j & 3] = see ? s[nb][y][j >> 2][j & 3] : -INFINITY;
+                        }
+                    }
+                }
+                float all = -INFINITY;
+#pragma unroll
+                for (int y = 0; y < U; y++)
+#pragma unroll
+                    for (int j = 0; j < 8; j++) all = fmaxf(all, s[nb][y][j >> 2][j & 3]);
+                all = max_xor32(max_xor16(all));
+                const float mn = fmaxf(m[nb], ceilf(all * fac[nb]));
+                const float down = m[nb] - mn;             // <= 0
+                const float c = (float)kProbExp - mn;
+                float f = fac[nb], sum = 0.0f;
+                if (__any(far_scores(mn))) {
+#pragma unroll
+                    for (int y = 0; y < U; y++) {
+                        s[nb][y][0] *= f;
+                        s[nb][y][1] *= f;
+                    }
+                    f = 1.0f;
+                }
+#pragma unroll
+                for (int y = 0; y < U; y++) {
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        const float p = __builtin_amdgcn_exp2f(fmaf(s[nb][y][j >> 2][j & 3], f, c));  // 2^14 (1 + 2^-8) at most
+                        sum += p;
+                        const _Float16 p0 = (_Float16)p;
+                        pf[nb][y][0][j] = p0;
+                        if constexpr (kParts == 2) pf[nb][y][1][j] = (_Float16)(p - (float)p0);
+                    }
+                }
+                const float turn = pow2_down(down);
+                L[nb] = L[nb] * turn + sum;
+                if (__any(down < 0.0f)) {
+#pragma unroll
+                    for (int i = 0; i < kT; i++) o[nb][i] *= turn;
+                }
+                m[nb] = mn;
+            }
+#pragma unroll
+            for (int y = 0; y < U; y++) {
+                const half2_t sv[4] = {scale_pair<0>(vc[y].x), scale_pair<2>(vc[y].x), scale_pair<0>(vc[y].y), scale_pair<2>(vc[y].y)};
+#pragma unroll
+                for (int i = 0; i < kVW; i++)
+#pragma unroll
+                    for (int odd = 0; odd < 2; odd++) {
+                        uint32_t d[4];
+#pragma unroll
+                        for (int j = 0; j < 4; j++)
+                            d[j] = odd ? odd_codes(vr[y][2 * j][i], vr[y][2 * j + 1][i]) : even_codes(vr[y][2 * j][i], vr[y][2 * j + 1][i]);
+                        auto tile_of = [&](auto byte) {
+                            constexpr int J = decltype(byte)::value;
+                            const half8_t f = __builtin_bit_cast(half8_t, make_uint4(codes_times<J>(d[0], sv[0]), codes_times<J>(d[1], sv[1]),
+                                                                                     codes_times<J>(d[2], sv[2]), codes_times<J>(d[3], sv[3])));
+                            const int k = 8 * i + 2 * J + odd;
+#pragma unroll
+                            for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+                                for (int pt = 0; pt < kParts; pt++)
+                                    o[nb][k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, pf[nb][y][pt], o[nb][k], 0, 0, 0);
+                        };
+                        tile_of(std::integral_constant<int, 0>());
+                        tile_of(std::integral_constant<int, 1>());
+                        if constexpr (kVB >= 4) {
+                            tile_of(std::integral_constant<int, 2>());
+                            tile_of(std::integral_constant<int, 3>());
+                        }
+                    }
+            }
+            if (more) {
+                load_v(tile + kWaves);
+                if (tile + 2 * kWaves < stop) find_pages(tile + 2 * kWaves);
+            }
+        }
+
+        // join the waves: the column's sum first (a lane has summed its own positions)
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++) {
+            L[nb] += __shfl_xor(L[nb], 16);
+            L[nb] += __shfl_xor(L[nb], 32);
+            if (g == 0) {
+                s_m[wave][16 * nb + n] = m[nb];
+                s_l[wave][16 * nb + n] = L[nb];
+            }
+        }
+        // a wave's rows x kSumRows .. into LDS, in order of their values
+        constexpr int kItems = Lay::kItems, kSumRows = Lay::kSumRows;
+        auto spread = [&](int x) {
+#pragma unroll
+            for (int nb = 0; nb < NB; nb++) {
+                const int r = 16 * nb + n - x * kSumRows;
+                if (r >= 0 && r < kSumRows) {
+                    float *p = s_o + (wave * kSumRows + r) * Lay::kRow;
+#pragma unroll
+                    for (int ii = 0; ii < 4; ii++)
+#pragma unroll
+                        for (int i = 0; i < kT; i += 4)
+                            *reinterpret_cast<float4 *>(p + (4 * g + ii) * kT + i) =
+                                make_float4(o[nb][i][ii], o[nb][i + 1][ii], o[nb][i + 2][ii], o[nb][i + 3][ii]);
+                }
+            }
+        };
+        __syncthreads();
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++) {
+            const int r = 16 * nb + n;
+            float mm = s_m[0][r];
+            for (int x = 1; x < kWaves; x++) mm = fmaxf(mm, s_m[x][r]);
+            if (wave == nb && g == 0) {
+                float l = 0.0f;
+                for (int x = 0; x < kWaves; x++) l += s_l[x][r] * pow2_down(s_m[x][r] - mm);
+                s_all[r] = make_float2(mm, l);
+            }
+            const float y = pow2_down(m[nb] - mm);
+#pragma unroll
+            for (int i = 0; i < kT; i++) o[nb][i] *= y;
+        }
+        // sum over the waves, kSumRows rows at a time; a thread ends with four values of a row of each
+        const int ir = tid / (D / 4), id = 4 * (tid % (D / 4));
+        float v[kItems][4];
+        State st[kItems];
+#pragma unroll
+        for (int x = 0; x < kItems; x++) {
+            const int q0 = x * kSumRows;
+            if (q0 >= nrows) break;
+            spread(x);
+            __syncthreads();
+            v[x][0] = v[x][1] = v[x][2] = v[x][3] = 0.0f;
+            {
+#pragma unroll
+                for (int y = 0; y < kWaves; y++) {
+                    const float4 f = *reinterpret_cast<const float4 *>(s_o + (y * kSumRows + ir) * Lay::kRow + id);
+                    v[x][0] += f.x; v[x][1] += f.y; v[x][2] += f.z; v[x][3] += f.w;
+                }
+                const float2 f = s_all[q0 + ir];
+                st[x] = State{f.x, 0.0f, f.y};
+            }
+            __syncthreads();
+        }
+        bool write = true;
+        if (tile1 - tile0 < tiles) {
+            const int64_t w_first = cut.first(unit0), w_end = cut.last(unit1);
+            auto slot = [&](unsigned x) { return shared_piece(pieces + (2 * (w_first + x) + (x == 0 ? 1 : 0)) * Lay::kRecord, 4 * Lay::kRecord); };
+            write = join_pieces<kRadix>(counters, w_first, w, w_end, &s_flag, [&](unsigned y) {
+                const __amdgpu_buffer_rsrc_t p = slot(y);
+#pragma unroll
+                for (int x = 0; x < kItems; x++) {
+                    const int r = x * kSumRows + ir;
+                    if (r < nrows) {
+                        put_shared4(p, (x * kThreads + tid) * 16, v[x][0], v[x][1], v[x][2], v[x][3]);
+                        if (id == 0) put_shared4(p, (kItems * kThreads + r) * 16, st[x].m, st[x].E, st[x].L, 0.0f);
+                    }
+                }
+            }, [&](unsigned y0, unsigned step, unsigned pieces_here) {
+#pragma unroll
+                for (int x = 0; x < kItems; x++) {
+                    const int r = x * kSumRows + ir;
+                    if (r >= nrows) break;
+                    st[x] = State{kLow, 0.0f, 0.0f};
+                    v[x][0] = v[x][1] = v[x][2] = v[x][3] = 0.0f;
+                    auto some = [&](auto count, unsigned y) {  // so many slots from y on, their loads together
+                        constexpr int kCount = decltype(count)::value;
+                        floatx4 f[kCount], t[kCount];
+#pragma unroll
+                        for (int z = 0; z < kCount; z++) {
+                            const __amdgpu_buffer_rsrc_t p = slot(y0 + (y + z) * step);
+                            f[z] = get_shared4(p, (x * kThreads + tid) * 16);
+                            t[z] = get_shared4(p, (kItems * kThreads + r) * 16);
+                        }
+#pragma unroll
+                        for (int z = 0; z < kCount; z++) {
+                            float qa, qb;
+                            st[x] = join(st[x], State{t[z][0], t[z][1], t[z][2]}, qa, qb);
+#pragma unroll
+                            for (int i = 0; i < 4; i++) v[x][i] = v[x][i] * qa + f[z][i] * qb;
+                        }
+                    };
+                    unsigned y = 0;
+                    for (; y + 4 <= pieces_here; y += 4) some(std::integral_constant<int, 4>(), y);
+                    for (; y < pieces_here; y++) some(std::integral_constant<int, 1>(), y);
+                }
+            });
+        }
+        if (write) {
+            int v_exp;
+            const float v_part = frexpf(a.c.v_unit[h], &v_exp);
+#pragma unroll
+            for (int x = 0; x < kItems; x++) {
+                const int r = x * kSumRows + ir;
+                if (r < nrows) {
+                    // the sum of the probabilities carries the same 2^14 as the products
+                    const float inv = st[x].L > 0.0f ? v_part / st[x].L : 0.0f;
+                    float y[4];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) y[i] = ldexpf(v[x][i] * inv, v_exp + kValueExp);
+                    int token, head;
+                    row_at(r, token, head);
+                    const int64_t off = ((q.first + token) * a.hq + head) * D + id;
+                    if constexpr (BF16)
+                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.o) + off) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+                    else
+                        *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + off) = make_float4(y[0], y[1], y[2], y[3]);
+                }
+            }
+        }
+        at = unit1;
+    }
+}
+
+template <int D, int NB>
+hipError_t launch_nb(const Attn4Args &a, int bf16, int num_cu, hipStream_t stream) {
+    const int wgs = kPerCu<NB> * num_cu;
+    if (bf16) k_kv4_split<D, NB, true><<<wgs, kThreads, 0, stream>>>(a, wgs);
+    else k_kv4_split<D, NB, false><<<wgs, kThreads, 0, stream>>>(a, wgs);
+    return hipGetLastError();
+}
+
+template <int D>
+int64_t bytes_d(int num_cu) {
+    const int64_t one = 2 * (int64_t)kPerCu<1> * num_cu * Layout<D, 1>::kRecord;
+    const int64_t two = 2 * (int64_t)kPerCu<2> * num_cu * Layout<D, 2>::kRecord;
+    return 4 * (one > two ? one : two);
+}
+
+}  // namespace
+
+int64_t kv4_split_bytes(int head_dim, int num_cu) {
+    return head_dim == 64 ? bytes_d<64>(num_cu) : head_dim == 128 ? bytes_d<128>(num_cu) : bytes_d<256>(num_cu);
+}
+
+hipError_t launch_kv4_split(const Attn4Args &a, int bf16, int blocks, int num_cu, hipStream_t stream) {
+    switch (a.c.head_dim) {
+        case 64: return blocks == 1 ? launch_nb<64, 1>(a, bf16, num_cu, stream) : launch_nb<64, 2>(a, bf16, num_cu, stream);
+        case 128: return blocks == 1 ? launch_nb<128, 1>(a, bf16, num_cu, stream) : launch_nb<128, 2>(a, bf16, num_cu, stream);
+        default: return blocks == 1 ? launch_nb<256, 1>(a, bf16, num_cu, stream) : launch_nb<256, 2>(a, bf16, num_cu, stream);
+    }
+}
+
+}  // namespace w4a8

@@ -1,0 +1,206 @@
+// Pages of sequences taken from and given back to a list on the device.
+//
+// Latency bound: a step's numbers are a few kilobytes.  A workgroup takes 1024 sequences at a time, one a
+// thread: prefix sums of their new tokens and new pages, left in LDS, then every token and every
+// page finds its sequence there by bisection.  With more tokens than a workgroup's threads care for, each of
+// many workgroups walks all sequences and takes its share of each 1024's tokens and pages; what such a
+// launch reads it must not write, so lengths and count that are updated in place are a second launch's.
+#include "serve_internal.h"
+#include "../attn/attn_tiles.h"
+
+namespace w4a8 {
+namespace {
+
+constexpr int kThreads = 1024, kWaves = kThreads / 64;
+// Tokens for which one workgroup is enough.
+constexpr int kAlone = 4096;
+constexpr int kPerThread = 4;    // entries of a thread at a time in giving back
+
+// What a launch of assigning writes.
+enum { kTokens = 1, kState = 2 };  // table, offsets, positions, slots; lengths, count
+
+__device__ __forceinline__ int held(int64_t x, int64_t most) { return (int)(x < 0 ? 0 : x > most ? most : x); }
+
+// Exclusive prefix sums of two numbers over the workgroup's threads, and their totals.
+struct Sums {
+    int64_t a, b, all_a, all_b;
+};
+__device__ __forceinline__ Sums scan_threads(int64_t a, int64_t b, int64_t (*s_part)[2]) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t ia = scan64(a), ib = scan64(b);
+    __syncthreads();  // the last ones have been read
+    if (lane == 63) {
+        s_part[wave][0] = ia;
+        s_part[wave][1] = ib;
+    }
+    __syncthreads();
+    const int64_t pa = scan64(lane < kWaves ? s_part[lane & (kWaves - 1)][0] : 0);
+    const int64_t pb = scan64(lane < kWaves ? s_part[lane & (kWaves - 1)][1] : 0);
+    const int before = wave > 0 ? wave - 1 : 0;
+    const int64_t fa = __shfl(pa, before), fb = __shfl(pb, before);
+    return Sums{(wave ? fa : 0) + ia - a, (wave ? fb : 0) + ib - b, lane_value(pa, kWaves - 1), lane_value(pb, kWaves - 1)};
+}
+
+// The last i < n with at[i] <= x, at not decreasing and at[0] <= x.
+template <class T>
+__device__ __forceinline__ int find_last(const T *at, int n, T x) {
+    int lo = 0;
+    for (int step = kThreads / 2; step > 0; step >>= 1)
+        if (lo + step < n && at[lo + step] <= x) lo += step;
+    return lo;
+}
+
+__global__ __launch_bounds__(kThreads) void k_pages_assign(w4a8_pages p, int shift, const int32_t *__restrict__ new_tokens,
+                                                           int64_t M, w4a8_batch out, int what) {
+    __shared__ int64_t s_part[kWaves][2];
+    __shared__ int s_token[kThreads], s_page[kThreads], s_old[kThreads];  // from the 1024 sequences' first on
+    const int tid = threadIdx.x;
+    const int64_t P = int64_t(1) << shift, most = p.table_width << shift;
+    const int count = held(p.free_count[0], p.num_pages);
+    const int64_t share = (int64_t)gridDim.x * kThreads, first = (int64_t)blockIdx.x * kThreads + tid;
+    auto taken = [&](int64_t i) {  // the i-th page off the list
+        return i < count ? p.free_pages[count - 1 - i] : -1;
+    };
+    int64_t token0 = 0, page0 = 0, lacking = 0;  // in front of the 1024 sequences; pages that tables have no room for
+    for (int64_t b0 = 0; b0 < p.B; b0 += kThreads) {
+        const int64_t b = b0 + tid;
+        int old = 0;
+        int64_t n = 0;
+        if (b < p.B) {
+            old = held(p.seq_lens[b], most);
+            n = held(new_tokens[b], M);
+        }
+        // what lies behind row M - 1 is not there: the rows up to a sequence's first are not known before the sum
+        Sums s = scan_threads(n, 0, s_part);
+        const int64_t at = token0 + s.a, row = at < M ? at : M, end = at + n < M ? at + n : M;
+        n = end - row;
+        const int64_t len = old + n < most ? old + n : most;
+        const int have = (int)((old + P - 1) >> shift), need = (int)((len + P - 1) >> shift);
+        const int64_t lack = ((old + n + P - 1) >> shift) - need;
+        const Sums t = scan_threads(need - have, lack, s_part);
+        const int all_tokens = (int)((token0 + s.all_a < M ? token0 + s.all_a : M) - (token0 < M ? token0 : M));
+        const int seqs = (int)(p.B - b0 < kThreads ? p.B - b0 : kThreads);
+        const int64_t base = token0 < M ? token0 : M;
+        s_token[tid] = (int)(row - base);
+        s_page[tid] = (int)t.a;  // (the tokens are M at most)
+        s_old[tid] = old;
+        __syncthreads();
+        if (what & kTokens) {
+            if (blockIdx.x == 0 && b < p.B) {
+                out.cu_tokens[b] = (int)row;
+                if (b == p.B - 1) out.cu_tokens[p.B] = (int)end;
+            }
+            for (int64_t i = first; i < all_tokens; i += share) {
+                const int q = find_last(s_token, seqs, (int)i);
+                const int64_t pos = s_old[q] + (i - s_token[q]);
+                const int64_t entry = pos >> shift, held_pages = (s_old[q] + P - 1) >> shift;
+                int page = -1;
+                if (pos < most)
+                    page = entry < held_pages ? p.page_table[(b0 + q) * p.table_width + entry]
+                                              : taken(page0 + s_page[q] + (entry - held_pages));
+                out.positions[base + i] = (int)(pos < INT32_MAX ? pos : INT32_MAX);
+                out.slots[base + i] = (uint32_t)page < (uint64_t)p.num_pages ? ((int64_t)page << shift) + (pos & (P - 1)) : -1;
+            }
+            for (int64_t i = first; i < t.all_a; i += share) {
+                const int q = find_last(s_page, seqs, (int)i);
+                const int64_t entry = ((s_old[q] + P - 1) >> shift) + (i - s_page[q]);
+                p.page_table[(b0 + q) * p.table_width + entry] = taken(page0 + i);
+            }
+        }
+        if ((what & kState) && blockIdx.x == 0 && b < p.B) out.seq_lens[b] = (int)len;
+        token0 += s.all_a;
+        page0 += t.all_a;
+        lacking += t.all_b;
+        __syncthreads();
+    }
+    if (what & kTokens)
+        for (int64_t i = (token0 < M ? token0 : M) + first; i < M; i += share) {
+            out.positions[i] = 0;
+            out.slots[i] = -1;
+        }
+    if (blockIdx.x == 0 && tid == 0) {
+        // (every thread of this workgroup has read the count in front of a barrier)
+        const int64_t short_of = (page0 > count ? page0 - count : 0) + lacking;
+        if (what & kState) {
+            out.free_count[0] = (int)(page0 < count ? count - page0 : 0);
+            out.missing[0] = (int)(short_of < INT32_MAX ? short_of : INT32_MAX);
+        }
+    }
+}
+
+// From the last sequence to the first, and within one from its last page down.
+__global__ __launch_bounds__(kThreads) void k_pages_release(w4a8_pages p, int shift, const int32_t *__restrict__ keep_lens,
+                                                            int32_t *lens, int32_t *free_count) {
+    __shared__ int64_t s_part[kWaves][2];
+    __shared__ int64_t s_first[kThreads];  // pages behind a sequence's, of the 1024
+    __shared__ int s_have[kThreads];
+    const int tid = threadIdx.x;
+    const int64_t P = int64_t(1) << shift, most = p.table_width << shift;
+    int64_t count = held(p.free_count[0], p.num_pages);
+    for (int64_t b0 = 0; b0 < p.B; b0 += kThreads) {
+        const int64_t b = p.B - 1 - (b0 + tid);  // thread 0 has the last one
+        int have = 0, gone = 0;
+        if (b >= 0) {
+            const int old = held(p.seq_lens[b], most), keep = held(keep_lens[b], old);
+            have = (int)((old + P - 1) >> shift);
+            gone = have - (int)((keep + P - 1) >> shift);
+            lens[b] = keep;
+        }
+        const Sums s = scan_threads(gone, 0, s_part);
+        s_first[tid] = s.a;
+        s_have[tid] = have;
+        __syncthreads();
+        const int seqs = (int)(p.B - b0 < kThreads ? p.B - b0 : kThreads);
+        for (int64_t i0 = 0; i0 < s.all_a; i0 += kThreads * kPerThread) {
+            int page[kPerThread];
+            int n = 0;
+#pragma unroll
+            for (int j = 0; j < kPerThread; j++) {
+                const int64_t i = i0 + tid * kPerThread + j;
+                page[j] = -1;
+                if (i < s.all_a) {
+                    const int q = find_last(s_first, seqs, i);
+                    page[j] = p.page_table[(p.B - 1 - (b0 + q)) * p.table_width + (s_have[q] - 1 - (i - s_first[q]))];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kPerThread; j++) {
+                if (page[j] >= p.num_pages) page[j] = -1;
+                n += page[j] >= 0;
+            }
+            const Sums t = scan_threads(n, 0, s_part);
+            int64_t at = count + t.a;
+#pragma unroll
+            for (int j = 0; j < kPerThread; j++)
+                if (page[j] >= 0) {
+                    if (at < p.num_pages) p.free_pages[at] = page[j];
+                    at++;
+                }
+            count += t.all_a;
+            if (count > p.num_pages) count = p.num_pages;
+        }
+        __syncthreads();
+    }
+    if (tid == 0) free_count[0] = (int)count;
+}
+
+}  // namespace
+
+hipError_t launch_pages_assign(const w4a8_pages &p, int page_shift, const int32_t *new_tokens, int64_t M,
+                               const w4a8_batch &out, hipStream_t stream) {
+    const bool in_place = out.seq_lens == p.seq_lens || out.free_count == p.free_count;
+    int64_t grid = M <= kAlone ? 1 : (M + kThreads - 1) / kThreads;
+    if (grid > 512) grid = 512;
+    const bool two = in_place && grid > 1;
+    k_pages_assign<<<(unsigned)grid, kThreads, 0, stream>>>(p, page_shift, new_tokens, M, out, two ? kTokens : kTokens | kState);
+    if (two) k_pages_assign<<<1, kThreads, 0, stream>>>(p, page_shift, new_tokens, M, out, kState);
+    return hipGetLastError();
+}
+
+hipError_t launch_pages_release(const w4a8_pages &p, int page_shift, const int32_t *keep, int32_t *lens, int32_t *count,
+                                hipStream_t stream) {
+    k_pages_release<<<1, kThreads, 0, stream>>>(p, page_shift, keep, lens, count);
+    return hipGetLastError();
+}
+
+}  // namespace w4a8
