@@ -44,14 +44,13 @@ struct Shape {
 // eight consecutive rows touches all banks, and every fragment is one address plus a constant.
 //   K: a row for each position; its slot of 8 values x is at place x / 4 + (x % 4) (D / 32): a staging
 //      thread writes four slots that follow each other, its neighbour the next four.
-//   V: row d / 4 + (d % 4) (D / 4) for value d (a staging thread writes four values, its neighbour the
-//      next four); place g has the positions 16 (g / 2) + 4 (g % 2) + {0..3, 8..11}.
+//   V: row d / 8 + (d % 8) (D / 8) for value d (a staging thread writes eight values, its neighbour the
+//      next eight); place g has the positions 16 (g / 2) + 4 (g % 2) + {0..3, 8..11}, four a staging thread's.
 template <int D>
 struct Tile {
     static constexpr int kRow = 2 * D + 16, kBytes = 8192 / D * kRow;
     static constexpr int vRow = 16384 / D + 16, vBytes = D * vRow;
     static __device__ __forceinline__ int k_at(int t, int place) { return t * kRow + place * 16; }
-    static __device__ __forceinline__ int v_row(int d) { return (d >> 2) + (d & 3) * (D / 4); }
     static __device__ __forceinline__ int v_at(int row, int place) { return row * vRow + place * 16; }
     // the first value that step s of the first product takes in half hh of the wave: place s + hh (D / 16)
     static __device__ __forceinline__ int q_at(int s, int hh) { return 32 * (s % (D / 32)) + 8 * (s / (D / 32)) + 16 * hh; }
@@ -210,30 +209,30 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
         for (int i = 0; i < kTiles; i++) o[i] = floatx16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
         float m = kLow, L = 0.0f;
 
-        // staging: item i < 256 holds 4 values of 8 positions of V, the others 32 values of a position of K
+        // staging: item i < 256 holds 8 values of 4 positions of V, the others 32 values of a position of K
         const int P = a.c.page_size, pm = P - 1;
         const int32_t *table = a.s.page_table + b * a.s.table_width;
-        uint32_t st[kItems][4], sc[kItems][2];  // codes (V: two positions a dword), scale bytes
+        uint32_t st[kItems][4], sc[kItems];  // codes, scale bytes
         int st_there = 0;
         int page[kItems];
         auto item_v = [&](int i) { return S::kWaves == 8 ? wave < 4 : i == 0; };
-        // V: position group, first value; K: position, chunk
+        // V: group of four positions, eight values; K: position, chunk
         auto place_v = [&](int &vg, int &vd) {
             const int it = fresh(tid) & 255;
-            vg = it / (D / 4);
-            vd = 4 * (it % (D / 4));
+            vg = it / (D / 8);
+            vd = it % (D / 8);
         };
         auto place_k = [&](int &kt, int &kc) {
             const int it = fresh(tid) & 255;
             kt = it / (D / 32);
             kc = it % (D / 32);
         };
-        auto teller = [&]() { return (fresh(tid) & 255) % (D / 2) == 0; };  // says whether a group's page is there
+        auto teller = [&]() { return (fresh(tid) & 255) % (D / 2) == 0; };  // says whether 16 positions' page is there
         auto find_page = [&](int tile, int i) {
             int x, y;
             if (item_v(i)) {
                 place_v(x, y);
-                x = 16 * (x >> 1);
+                x = 4 * x;
             } else {
                 place_k(x, y);
             }
@@ -248,17 +247,11 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
                 if (item_v(i)) {
                     int vg, vd;
                     place_v(vg, vd);
-                    const int slot = ((tile * T + 16 * (vg >> 1)) & pm) + 4 * (vg & 1);
-                    const uint8_t *p = a.c.v + (blk * P + slot) * (D / 2) + vd / 2;
+                    const int slot = (tile * T + 4 * vg) & pm;
+                    const uint8_t *p = a.c.v + (blk * P + slot) * (D / 2) + 4 * vd;
 #pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const int t = ((2 * j) & 3) + 8 * (j >> 1);
-                        st[i][j] = (uint32_t)*reinterpret_cast<const uint16_t *>(p + t * (D / 2)) |
-                                   (uint32_t)*reinterpret_cast<const uint16_t *>(p + (t + 1) * (D / 2)) << 16;
-                    }
-                    const uint8_t *s = a.c.v_scale + (blk * (D / 16) + vd / 16) * P + slot;
-                    sc[i][0] = *reinterpret_cast<const uint32_t *>(s);
-                    sc[i][1] = *reinterpret_cast<const uint32_t *>(s + 8);
+                    for (int j = 0; j < 4; j++) st[i][j] = *reinterpret_cast<const uint32_t *>(p + j * (D / 2));
+                    sc[i] = *reinterpret_cast<const uint32_t *>(a.c.v_scale + (blk * (D / 16) + (vd >> 1)) * P + slot);
                     st_there = ok;
                 } else {
                     int kt, kc;
@@ -266,7 +259,7 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
                     const int64_t row = blk * P + ((tile * T + kt) & pm);
                     const uint4 x = *reinterpret_cast<const uint4 *>(a.c.k + row * (D / 2) + 16 * kc);
                     st[i][0] = x.x; st[i][1] = x.y; st[i][2] = x.z; st[i][3] = x.w;
-                    sc[i][0] = *reinterpret_cast<const uint16_t *>(a.c.k_scale + row * (D / 16) + 2 * kc);
+                    sc[i] = *reinterpret_cast<const uint16_t *>(a.c.k_scale + row * (D / 16) + 2 * kc);
                 }
             }
         };
@@ -276,25 +269,28 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
                 if (item_v(i)) {
                     int vg, vd;
                     place_v(vg, vd);
-                    char *p = s_v[buf] + L4::v_at(L4::v_row(vd), vg);  // values vd + y: y (D / 4) rows on
-                    const half2_t s[4] = {scale_pair<0>(sc[i][0]), scale_pair<2>(sc[i][0]), scale_pair<0>(sc[i][1]), scale_pair<2>(sc[i][1])};
-                    // two positions' four codes each: bytes of both positions' code of values 0, 2 (even) and 1, 3
-                    uint32_t e[4], d[4];
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        e[j] = even_codes(st[i][j], st[i][j] >> 16);
-                        d[j] = odd_codes(st[i][j], st[i][j] >> 16);
-                    }
-                    *reinterpret_cast<uint4 *>(p) = make_uint4(codes_times<0>(e[0], s[0]), codes_times<0>(e[1], s[1]), codes_times<0>(e[2], s[2]), codes_times<0>(e[3], s[3]));
-                    *reinterpret_cast<uint4 *>(p + L4::v_at(D / 4, 0)) = make_uint4(codes_times<0>(d[0], s[0]), codes_times<0>(d[1], s[1]), codes_times<0>(d[2], s[2]), codes_times<0>(d[3], s[3]));
-                    *reinterpret_cast<uint4 *>(p + L4::v_at(D / 2, 0)) = make_uint4(codes_times<1>(e[0], s[0]), codes_times<1>(e[1], s[1]), codes_times<1>(e[2], s[2]), codes_times<1>(e[3], s[3]));
-                    *reinterpret_cast<uint4 *>(p + L4::v_at(3 * D / 4, 0)) = make_uint4(codes_times<1>(d[0], s[0]), codes_times<1>(d[1], s[1]), codes_times<1>(d[2], s[2]), codes_times<1>(d[3], s[3]));
-                    if (teller()) s_there[buf][vg >> 1] = st_there;
+                    // four positions are half a place
+                    char *p = s_v[buf] + L4::v_at(vd, 2 * (vg >> 2) + (vg & 1)) + (vg & 2) * 4;
+                    const half2_t s0 = scale_pair<0>(sc[i]), s1 = scale_pair<2>(sc[i]);
+                    const uint32_t e0 = even_codes(st[i][0], st[i][1]), e1 = even_codes(st[i][2], st[i][3]);
+                    const uint32_t d0 = odd_codes(st[i][0], st[i][1]), d1 = odd_codes(st[i][2], st[i][3]);
+                    auto row = [&](int y, uint32_t first, uint32_t second) {  // value 8 vd + y
+                        *reinterpret_cast<uint2 *>(p + L4::v_at(y * (D / 8), 0)) = make_uint2(first, second);
+                    };
+                    row(0, codes_times<0>(e0, s0), codes_times<0>(e1, s1));
+                    row(1, codes_times<0>(d0, s0), codes_times<0>(d1, s1));
+                    row(2, codes_times<1>(e0, s0), codes_times<1>(e1, s1));
+                    row(3, codes_times<1>(d0, s0), codes_times<1>(d1, s1));
+                    row(4, codes_times<2>(e0, s0), codes_times<2>(e1, s1));
+                    row(5, codes_times<2>(d0, s0), codes_times<2>(d1, s1));
+                    row(6, codes_times<3>(e0, s0), codes_times<3>(e1, s1));
+                    row(7, codes_times<3>(d0, s0), codes_times<3>(d1, s1));
+                    if (teller()) s_there[buf][vg >> 2] = st_there;
                 } else {
                     int kt, kc;
                     place_k(kt, kc);
                     char *p = s_k[buf] + L4::k_at(kt, kc);
-                    const half2_t s0 = scale_both<0>(sc[i][0]), s1 = scale_both<1>(sc[i][0]);
+                    const half2_t s0 = scale_both<0>(sc[i]), s1 = scale_both<1>(sc[i]);
 #pragma unroll
                     for (int x = 0; x < 4; x++)
                         *reinterpret_cast<half8_t *>(p + L4::k_at(0, x * (D / 32))) = values_natural(st[i][x], x < 2 ? s0 : s1);
@@ -374,7 +370,7 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
 #pragma unroll
                 for (int j = 1; j < 16 * kSubs; j++) top = fmaxf(top, s[j >> 4][j & 15]);
                 top = max_xor32(top);
-                const float mn = fmaxf(m, ceilf(top * fac));
+                const float mn = fmaxf(m, whole_above(top * fac));
                 const float down = m - mn;
                 if (__any(down < 0.0f)) {
                     const float x = pow2_down(down);
@@ -384,19 +380,13 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
                 }
                 m = mn;
                 const float c = (float)kProbExp - mn;
-                float f = fac;
-                if (__any(far_scores(mn))) {
-#pragma unroll
-                    for (int y = 0; y < kSubs; y++) s[y] *= f;
-                    f = 1.0f;
-                }
                 half8_t pf[2 * kSubs][kParts];  // positions 16 x .. of the step
                 auto weights = [&](int y) {     // of its 32 positions 32 y ..
                     float sum = 0.0f;
 #pragma unroll
                     for (int j = 0; j < 16; j += 2) {
-                        const float p0x = __builtin_amdgcn_exp2f(fmaf(s[y][j], f, c));   // 2^14 (1 + 2^-8) at most
-                        const float p1x = __builtin_amdgcn_exp2f(fmaf(s[y][j + 1], f, c));
+                        const float p0x = __builtin_amdgcn_exp2f(fmaf(s[y][j], fac, c));   // 2^14 at most
+                        const float p1x = __builtin_amdgcn_exp2f(fmaf(s[y][j + 1], fac, c));
                         sum += p0x + p1x;
                         const int z = 2 * y + (j >> 3);
                         if constexpr (BF16) {
@@ -484,24 +474,24 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
             int head;
             row_of(token, head);
             const int64_t off = ((q.first + token) * a.hq + head) * D;
-            // value 4 x + y is in row x + y (D / 4) of O^T; this lane has the rows 32 i + 8 j + 4 hh + c
+            // value 8 x + y is in row x + y (D / 8) of O^T; this lane has the rows 32 i + 8 j + 4 hh + c
 #pragma unroll
-            for (int z = 0; z < D / 8; z++) {
+            for (int z = 0; z < D / 16; z++) {
                 const int x = (z >> 2) * 8 + (z & 3);   // and + 4 hh
-                float v[4];
+                float v[8];
 #pragma unroll
-                for (int y = 0; y < 4; y++) {
-                    const int row = x + y * (D / 4);
+                for (int y = 0; y < 8; y++) {
+                    const int row = x + y * (D / 8);
                     v[y] = ldexpf(o[row >> 5][((row & 31) >> 3) * 4 + (row & 3)] * inv, v_exp + kValueExp);
                 }
-                const int64_t d = off + 4 * (x + 4 * hh);
+                const int64_t d = off + 8 * (x + 4 * hh);
                 if constexpr (BF16) {
-                    uint2 u;
-                    u.x = pack_bf16(v[0], v[1]);
-                    u.y = pack_bf16(v[2], v[3]);
-                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.o) + d) = u;
+                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o) + d) =
+                        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
                 } else {
-                    *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + d) = make_float4(v[0], v[1], v[2], v[3]);
+                    float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(a.o) + d);
+                    p[0] = make_float4(v[0], v[1], v[2], v[3]);
+                    p[1] = make_float4(v[4], v[5], v[6], v[7]);
                 }
             }
         }

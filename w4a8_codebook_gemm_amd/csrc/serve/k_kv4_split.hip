@@ -368,23 +368,15 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a,
 #pragma unroll
                     for (int j = 0; j < 8; j++) all = fmaxf(all, s[nb][y][j >> 2][j & 3]);
                 all = max_xor32(max_xor16(all));
-                const float mn = fmaxf(m[nb], ceilf(all * fac[nb]));
+                const float mn = fmaxf(m[nb], whole_above(all * fac[nb]));
                 const float down = m[nb] - mn;             // <= 0
                 const float c = (float)kProbExp - mn;
-                float f = fac[nb], sum = 0.0f;
-                if (__any(far_scores(mn))) {
-#pragma unroll
-                    for (int y = 0; y < U; y++) {
-                        s[nb][y][0] *= f;
-                        s[nb][y][1] *= f;
-                    }
-                    f = 1.0f;
-                }
+                float sum = 0.0f;
 #pragma unroll
                 for (int y = 0; y < U; y++) {
 #pragma unroll
                     for (int j = 0; j < 8; j++) {
-                        const float p = __builtin_amdgcn_exp2f(fmaf(s[nb][y][j >> 2][j & 3], f, c));  // 2^14 (1 + 2^-8) at most
+                        const float p = __builtin_amdgcn_exp2f(fmaf(s[nb][y][j >> 2][j & 3], fac[nb], c));  // 2^14 at most
                         sum += p;
                         const _Float16 p0 = (_Float16)p;
                         pf[nb][y][0][j] = p0;

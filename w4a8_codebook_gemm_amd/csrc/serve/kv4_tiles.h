@@ -39,8 +39,10 @@ __device__ __forceinline__ half8_t values_natural(uint32_t w, half2_t s) {
 __device__ __forceinline__ uint32_t even_codes(uint32_t first, uint32_t second) { return (first & 0x0F0F0F0Fu) | ((second << 4) & 0xF0F0F0F0u); }
 __device__ __forceinline__ uint32_t odd_codes(uint32_t first, uint32_t second) { return ((first >> 4) & 0x0F0F0F0Fu) | (second & 0xF0F0F0F0u); }
 
-// Whether a row's exponents s fac - m may not be one multiply-add: it does not round the product, which then
-// may pass a maximum m that was rounded by 2^-24 of itself.  Up to this size that is 2^-8, above it the product is rounded first.
-__device__ __forceinline__ bool far_scores(float m) { return fabsf(m) > 65536.0f && m > kLow; }
+// The running maximum for a largest exponent t = s fac, a whole number.  Exponents are one multiply-add each,
+// s fac - m, which does not round the product as t is rounded: m is 2^-22 of t above it (2 to 4 of its last places),
+// so that none of them passes 0 by rounding.  For |t| up to 2^16 that is 2^-6 before it is rounded up; from 2^26 on it takes a row's
+// weights out of fp16's range.  (Where nothing is seen t is -inf and this no number, which fmaxf passes over.)
+__device__ __forceinline__ float whole_above(float t) { return ceilf(fmaf(fabsf(t), 0x1p-22f, t)); }
 
 }  // namespace w4a8
