@@ -52,16 +52,28 @@ template <> struct Bytes<1> { typedef uint8_t type; };
 template <> struct Bytes<2> { typedef uint16_t type; };
 template <> struct Bytes<4> { typedef uint32_t type; };
 template <> struct Bytes<8> { typedef uint2 type; };
+template <> struct Bytes<16> { typedef uint4 type; };
 template <int N>
 __device__ __forceinline__ typename Bytes<N>::type load_bytes(const uint8_t *p) {
     return *reinterpret_cast<const typename Bytes<N>::type *>(p);
 }
+// Codes are read by one lane once: past the caches.
+template <int N>
+__device__ __forceinline__ typename Bytes<N>::type load_once(const uint8_t *p) {
+    if constexpr (N < 4) {
+        return __builtin_nontemporal_load(reinterpret_cast<const typename Bytes<N>::type *>(p));
+    } else {
+        typedef uint32_t type __attribute__((ext_vector_type(N / 4)));
+        return __builtin_bit_cast(typename Bytes<N>::type, __builtin_nontemporal_load(reinterpret_cast<const type *>(p)));
+    }
+}
 
-template <int D, int NB, bool BF16>
+// kSmall: pages of 16 positions, else of 32 or more: a page for all lanes' part of a tile.
+template <int D, int NB, bool BF16, bool kSmall>
 __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a, int wgs) {
     using Lay = Layout<D, NB>;
     constexpr int RB = Lay::RB;
-    constexpr int U = D == 64 ? 4 : 2, T = 32 * U;  // 32-position parts of a tile
+    constexpr int U = 256 / D, T = 32 * U;  // 32-position parts of a tile
     constexpr int kParts = BF16 ? 1 : 2;   // fp16 numbers that make a query value or a probability
     constexpr int kS = D / 32;             // dwords of a key in a lane, steps of the first product
     constexpr int kT = D / 16;             // tiles of O^T
@@ -73,7 +85,7 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a,
     __shared__ float s_m[kWaves][RB], s_l[kWaves][RB];
     __shared__ float2 s_all[RB];
     __shared__ int s_flag;
-    const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     uint32_t *counters = static_cast<uint32_t *>(a.ws);
     float *pieces = reinterpret_cast<float *>(static_cast<char *>(a.ws) + kAttnCounterBytes);
 
@@ -183,85 +195,92 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a,
         if (first < any_lo / T) first += (any_lo / T - first + kWaves - 1) / kWaves * kWaves;
         const int stop = end < tiles_to<T>(any_hi) ? end : tiles_to<T>(any_hi);
         const int P = a.c.page_size, pm = P - 1;
-        const bool small = a.page_shift == 4;  // two pages in 32 positions
         const int32_t *table = a.s.page_table + b * a.s.table_width;
 
+        // Pages come from 64 entries of the table that the wave's lanes hold: a load of the page itself would be waited for
+        // behind the codes that were asked for before it.
+        int window0 = 0, window = -1;
+        auto find_window = [&](int e) {
+            window0 = e;
+            // (waited for here, not where it is used on the path that does not come by)
+            window = fresh(window0 + lane < a.s.table_width ? table[window0 + lane] : -1);
+        };
         auto page_of = [&](int t) {  // page of position t, -1 past the end
-            return t < q.len ? table[t >> a.page_shift] : -1;
+            const int e = (t >> a.page_shift) - window0, p = kSmall ? __shfl(window, e) : lane_value(window, e);
+            return t < q.len ? p : -1;
         };
-        auto block_of = [&](int page) {  // its block of this head; a page that is not there reads page 0, masked
-            return (int64_t)((uint32_t)page < (uint32_t)a.c.num_pages ? page : 0) * a.c.kv_heads + h;
+        // The slot of position t in a cache of this head's rows; a page that is not there reads page 0, masked.
+        auto slot_of = [&](int t, int page, bool &ok) {
+            ok = (uint32_t)page < (uint32_t)a.c.num_pages;
+            return ((int64_t)(ok ? page : 0) * a.c.kv_heads + h) * P + (t & pm);
         };
-        uint32_t kr[U][2][kS], kc[U][2], vr[U][8][kVW];
-        uint2 vc[U];
-        int pk[U], ps[U];       // pages of the tile to load next, of this lane's key row and of its positions
-        uint32_t there = 0;     // of the tile in hand: bit x where part x's page of this lane's positions is there
-        auto find_pages = [&](int tile) {
-            const int l = fresh(lane);
+        // This lane's places from a part's first position on: in its keys and their scales, its values and theirs.
+        const int k_row = 2 * (lane & 12) + (lane & 3);
+        const uint32_t k_at = k_row * (D / 2) + g * (D / 8), kc_at = k_row * (D / 16) + g * (D / 64);
+        const uint32_t v_at = 8 * g * (D / 2) + n * kVB, vc_at = (uint32_t)(n * (D / 16) / 16) * P + 8 * g;
+        // A tile's codes and scale bytes as they lie; `there`: bit x where part x's page of this lane's positions is there.
+        struct Codes {
+            uint32_t k[U][2][kS], kc[U][2], v[U][8][kVW];
+            uint2 vc[U];
+            uint32_t there;
+        };
+        auto load_k = [&](int tile, Codes &c) {
+            // (a tile's entries begin with its first position's)
+            const int last = (tile * T + (T - 1)) >> a.page_shift;
+            if (last - window0 >= 64) find_window((tile * T) >> a.page_shift);
 #pragma unroll
             for (int x = 0; x < U; x++) {
-                const int t = tile * T + 32 * x;
-                pk[x] = page_of(t + (small ? 2 * (l & 8) : 0));
-                ps[x] = page_of(t + (small ? (l & 32) >> 1 : 0));
-            }
-        };
-        auto load_k = [&](int tile) {
-            const int l = fresh(lane);
-#pragma unroll
-            for (int x = 0; x < U; x++) {
-                const int64_t row = block_of(pk[x]) * P + ((tile * T + 32 * x + 2 * (l & 12) + (l & 3)) & pm);
-                const uint8_t *p = a.c.k + row * (D / 2) + (l >> 4) * (D / 8), *s = a.c.k_scale + row * (D / 16) + (l >> 4) * (D / 64);
+                const int t = tile * T + 32 * x, half = kSmall ? 2 * (lane & 8) : 0;  // (small pages: the row's own)
+                bool ok;
+                const int64_t row = slot_of(t, page_of(t + half), ok);
+                const uint8_t *p = a.c.k + row * (D / 2) + (k_at - half * (D / 2)), *sk = a.c.k_scale + row * (D / 16) + (kc_at - half * (D / 16));
 #pragma unroll
                 for (int u = 0; u < 2; u++) {
                     const uint8_t *pu = p + u * 4 * (D / 2);
                     if constexpr (D >= 128) {
 #pragma unroll
-                        for (int c = 0; c < kS; c += 4) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(pu + 4 * c);
-                            kr[x][u][c] = v.x; kr[x][u][c + 1] = v.y; kr[x][u][c + 2] = v.z; kr[x][u][c + 3] = v.w;
+                        for (int i = 0; i < kS; i += 4) {
+                            const uint4 y = load_once<16>(pu + 4 * i);
+                            c.k[x][u][i] = y.x; c.k[x][u][i + 1] = y.y; c.k[x][u][i + 2] = y.z; c.k[x][u][i + 3] = y.w;
                         }
                     } else {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(pu);
-                        kr[x][u][0] = v.x;
-                        kr[x][u][1] = v.y;
+                        const uint2 y = load_once<8>(pu);
+                        c.k[x][u][0] = y.x;
+                        c.k[x][u][1] = y.y;
                     }
-                    kc[x][u] = load_bytes<D / 64>(s + u * 4 * (D / 16));
+                    c.kc[x][u] = load_bytes<D / 64>(sk + u * 4 * (D / 16));
                 }
             }
         };
-        auto load_v = [&](int tile) {
-            const int l = fresh(lane);
+        auto load_v = [&](int tile, Codes &c) {
+            c.there = 0;
 #pragma unroll
             for (int x = 0; x < U; x++) {
-                const int64_t blk = block_of(ps[x]);
-                const int slot = (tile * T + 32 * x + (l >> 4) * 8) & pm;
-                const uint8_t *p = a.c.v + (blk * P + slot) * (D / 2) + (l & 15) * kVB;
+                const int t = tile * T + 32 * x, half = kSmall ? 8 * (g & 2) : 0;
+                bool ok;
+                const int64_t row = slot_of(t, page_of(t + half), ok);
+                c.there |= (uint32_t)ok << x;
+                const uint8_t *p = a.c.v + row * (D / 2) + (v_at - half * (D / 2));
 #pragma unroll
                 for (int j = 0; j < 8; j++) {
                     if constexpr (kVB == 8) {
-                        const uint2 v = load_bytes<8>(p + j * (D / 2));
-                        vr[x][j][0] = v.x;
-                        vr[x][j][kVW - 1] = v.y;
+                        const uint2 y = load_once<8>(p + j * (D / 2));
+                        c.v[x][j][0] = y.x;
+                        c.v[x][j][kVW - 1] = y.y;
                     } else {
-                        vr[x][j][0] = load_bytes<kVB>(p + j * (D / 2));
+                        c.v[x][j][0] = load_once<kVB>(p + j * (D / 2));
                     }
                 }
-                vc[x] = load_bytes<8>(a.c.v_scale + (blk * (D / 16) + (l & 15) * (D / 16) / 16) * P + slot);
+                // a block's rows of P scale bytes, one for each group
+                const int slot = t & pm;
+                c.vc[x] = load_bytes<8>(a.c.v_scale + (row - slot) * (D / 16) + slot + (vc_at - half));
             }
         };
-        auto set_there = [&]() {
-            uint32_t t = 0;
-#pragma unroll
-            for (int x = 0; x < U; x++) t |= (uint32_t)((uint32_t)ps[x] < (uint32_t)a.c.num_pages) << x;
-            return t;
-        };
-        uint32_t next_there = 0;
+        Codes cd;
+        find_window((first * T) >> a.page_shift);
         if (first < stop) {
-            find_pages(first);
-            next_there = set_there();
-            load_k(first);
-            load_v(first);
-            if (first + kWaves < stop) find_pages(first + kWaves);
+            load_k(first, cd);
+            load_v(first, cd);
         }
 
         // queries as fp16, into LDS: fragment (block, part, step) as its lanes read it; zeros behind the rows
@@ -312,40 +331,46 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a,
 #pragma unroll
             for (int i = 0; i < kT; i++) o[nb][i] = floatx4{0, 0, 0, 0};
         }
-        for (int tile = first; tile < stop; tile += kWaves) {
-            const bool more = tile + kWaves < stop;
+        // a tile's work; kMore: with the next one's loads, without a branch around them, which would have every wait for codes
+        // wait for all that is on its way
+        auto work = [&](int tile, auto next) {
+            constexpr bool kMore = decltype(next)::value;
             floatx4 s[NB][U][2];
 #pragma unroll
             for (int nb = 0; nb < NB; nb++)
 #pragma unroll
                 for (int x = 0; x < U; x++) s[nb][x][0] = s[nb][x][1] = floatx4{0, 0, 0, 0};
             const half8_t *qp = s_q + fresh(lane);
-#pragma unroll
-            for (int c = 0; c < kS; c++) {
-                half8_t qf[NB][kParts];
+            half8_t qf[2][NB][kParts];  // this step's and the next one's
+            auto take_q = [&](int c) {
 #pragma unroll
                 for (int nb = 0; nb < NB; nb++)
 #pragma unroll
-                    for (int pt = 0; pt < kParts; pt++) qf[nb][pt] = qp[((nb * kParts + pt) * kS + c) * 64];
+                    for (int pt = 0; pt < kParts; pt++) qf[c & 1][nb][pt] = qp[((nb * kParts + pt) * kS + c) * 64];
+            };
+            take_q(0);
+#pragma unroll
+            for (int c = 0; c < kS; c++) {
+                if (c + 1 < kS) take_q(c + 1);
 #pragma unroll
                 for (int x = 0; x < U; x++)
 #pragma unroll
                     for (int u = 0; u < 2; u++) {
                         // 16 values a scale: two dwords
-                        const half2_t sc = c < 2 ? scale_both<0>(kc[x][u]) : c < 4 ? scale_both<1>(kc[x][u]) : c < 6 ? scale_both<2>(kc[x][u]) : scale_both<3>(kc[x][u]);
-                        const half8_t k = values_natural(kr[x][u][c], sc);
+                        const uint32_t b = cd.kc[x][u];
+                        const half2_t sc = c < 2 ? scale_both<0>(b) : c < 4 ? scale_both<1>(b) : c < 6 ? scale_both<2>(b) : scale_both<3>(b);
+                        const half8_t k = values_natural(cd.k[x][u][c], sc);
 #pragma unroll
                         for (int nb = 0; nb < NB; nb++)
 #pragma unroll
                             for (int pt = 0; pt < kParts; pt++)
-                                s[nb][x][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qf[nb][pt], s[nb][x][u], 0, 0, 0);
+                                s[nb][x][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qf[c & 1][nb][pt], s[nb][x][u], 0, 0, 0);
                     }
+                __builtin_amdgcn_sched_barrier(0);
             }
-            there = next_there;
-            if (more) {
-                next_there = set_there();
-                load_k(tile + kWaves);
-            }
+            if constexpr (kMore) load_k(tile + kWaves, cd);
+            __builtin_amdgcn_sched_barrier(0);
+            const uint32_t there = cd.there;
             const bool whole = tile * T >= all_lo && all_hi - tile * T >= T && __all(there == (1u << U) - 1);
             half8_t pf[NB][U][kParts];
 #pragma unroll
@@ -391,9 +416,10 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a,
                 }
                 m[nb] = mn;
             }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int y = 0; y < U; y++) {
-                const half2_t sv[4] = {scale_pair<0>(vc[y].x), scale_pair<2>(vc[y].x), scale_pair<0>(vc[y].y), scale_pair<2>(vc[y].y)};
+                const half2_t sv[4] = {scale_pair<0>(cd.vc[y].x), scale_pair<2>(cd.vc[y].x), scale_pair<0>(cd.vc[y].y), scale_pair<2>(cd.vc[y].y)};
 #pragma unroll
                 for (int i = 0; i < kVW; i++)
 #pragma unroll
@@ -401,7 +427,7 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a,
                         uint32_t d[4];
 #pragma unroll
                         for (int j = 0; j < 4; j++)
-                            d[j] = odd ? odd_codes(vr[y][2 * j][i], vr[y][2 * j + 1][i]) : even_codes(vr[y][2 * j][i], vr[y][2 * j + 1][i]);
+                            d[j] = odd ? odd_codes(cd.v[y][2 * j][i], cd.v[y][2 * j + 1][i]) : even_codes(cd.v[y][2 * j][i], cd.v[y][2 * j + 1][i]);
                         auto tile_of = [&](auto byte) {
                             constexpr int J = decltype(byte)::value;
                             const half8_t f = __builtin_bit_cast(half8_t, make_uint4(codes_times<J>(d[0], sv[0]), codes_times<J>(d[1], sv[1]),
@@ -419,12 +445,15 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a,
                             tile_of(std::integral_constant<int, 2>());
                             tile_of(std::integral_constant<int, 3>());
                         }
+                        __builtin_amdgcn_sched_barrier(0);
                     }
             }
-            if (more) {
-                load_v(tile + kWaves);
-                if (tile + 2 * kWaves < stop) find_pages(tile + 2 * kWaves);
-            }
+            if constexpr (kMore) load_v(tile + kWaves, cd);
+        };
+        if (first < stop) {
+            int tile = first;
+            for (; tile + kWaves < stop; tile += kWaves) work(tile, std::true_type());
+            work(tile, std::false_type());
         }
 
         // join the waves: the column's sum first (a lane has summed its own positions)
@@ -564,8 +593,9 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a,
 template <int D, int NB>
 hipError_t launch_nb(const Attn4Args &a, int bf16, int num_cu, hipStream_t stream) {
     const int wgs = kPerCu<NB> * num_cu;
-    if (bf16) k_kv4_split<D, NB, true><<<wgs, kThreads, 0, stream>>>(a, wgs);
-    else k_kv4_split<D, NB, false><<<wgs, kThreads, 0, stream>>>(a, wgs);
+    auto f = a.page_shift == 4 ? (bf16 ? k_kv4_split<D, NB, true, true> : k_kv4_split<D, NB, false, true>)
+                               : (bf16 ? k_kv4_split<D, NB, true, false> : k_kv4_split<D, NB, false, false>);
+    f<<<wgs, kThreads, 0, stream>>>(a, wgs);
     return hipGetLastError();
 }
 
