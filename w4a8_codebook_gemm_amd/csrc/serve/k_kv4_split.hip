@@ -277,8 +277,8 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a,
             }
         };
         Codes cd;
-        find_window((first * T) >> a.page_shift);
-        if (first < stop) {
+        if (first < stop) {  // (a wave without a tile may stand where first * T passes 2^31)
+            find_window((first * T) >> a.page_shift);
             load_k(first, cd);
             load_v(first, cd);
         }
