@@ -91,6 +91,10 @@ NORM = [
     (2, 65536, F32, F32, BF, 0),
     (4099, 256, BF, F32, None, 0),          # more tokens than workgroups
     (2500, 2048, F32, BF, BF, 0),
+    (4097, 5120, F32, BF, BF, 0),           # three blocks a lane group, two tokens a workgroup
+    (4096, 2816, BF, F32, None, 24),        # one wave a token, with a block to spare
+    (4100, 9216, BF, BF, None, 0),          # three waves a token
+    (4099, 1536, F32, F32, None, 0),
 ]
 
 

@@ -2,13 +2,15 @@
 //
 //   h = x + r;  y = h rsqrt(mean h^2 + eps) (w + offset);  int8 of the rotated y, a scale a token
 //
-// HBM bound: every value is read once and written once.  A workgroup holds a token in registers, 16
-// consecutive values a lane as the rotation wants them (fwht256_row16), and passes two barriers: the
-// sum of squares, then the largest rotated magnitude.  The next token's values are on their way
-// meanwhile.  The sum is fp64 (products of fp32 numbers are exact in it), so the factor does not
-// depend on how the sum is split, but for one rounding in some 2^28; it costs one conversion and one multiply-add a value.
-#include <atomic>
-
+// HBM bound: every value is read once and written once.  A token is held in registers, 16 consecutive
+// values a lane and block of 256 as the rotation wants them (fwht256_row16), by W waves of R blocks a
+// group of 16 lanes.  Two numbers need all of a token: the sum of squares, then the largest rotated magnitude.
+// One wave a token exchanges them between lanes alone, so nothing waits for another wave; more waves a token
+// (fewer blocks a lane group) also meet at two barriers, and finish a single token sooner.
+//
+// The sum is fp64 (products of fp32 numbers are exact in it), so the factor does not depend on how the sum is
+// split, but for one rounding in some 2^28.  Its root is the hardware's reciprocal square root (some 2^-28 off) and
+// one Newton step, y + y/2 (1 - a y^2), in fp64: 2^-52, as exact as a division by a root.
 #include "serve_internal.h"
 
 namespace w4a8 {
@@ -16,6 +18,7 @@ namespace {
 
 constexpr int kMaxThreads = 1024;
 constexpr uint32_t kOutside = 0x80000000u;  // buffer offset past any row: reads zero, stores dropped
+constexpr int kMaxWeights = 32768;          // bytes of weights that a workgroup keeps in LDS
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // 16 consecutive values as they lie in memory
@@ -59,19 +62,59 @@ __device__ __forceinline__ void store16(__amdgpu_buffer_rsrc_t r, uint32_t eleme
     }
 }
 
-// Tokens blockIdx.x, blockIdx.x + gridDim.x, ...; R blocks of 256 a group of 16 lanes.
-template <bool XB, bool RB, int R>
-__global__ __launch_bounds__(kMaxThreads) void k_add_norm(NormArgs a) {
+// Sum and maximum (of values >= 0) over a wave's lanes, by shifts within rows of 16, then from row to row; the last
+// lane's, as uniform values.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ uint32_t moved(uint32_t x) { return __builtin_amdgcn_update_dpp(0, (int)x, kCtrl, kRows, 0xF, false); }
+template <int kCtrl, int kRows>
+__device__ __forceinline__ double moved(double x) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    return __builtin_bit_cast(double, (uint64_t)moved<kCtrl, kRows>((uint32_t)b) | (uint64_t)moved<kCtrl, kRows>((uint32_t)(b >> 32)) << 32);
+}
+__device__ __forceinline__ double wave_sum(double x) {
+    x += moved<0x111, 0xF>(x);  // row_shr:1, 2, 4, 8
+    x += moved<0x112, 0xF>(x);
+    x += moved<0x114, 0xF>(x);
+    x += moved<0x118, 0xF>(x);
+    x += moved<0x142, 0xA>(x);  // row_bcast:15, 31
+    x += moved<0x143, 0xC>(x);
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    return __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)b, 63) |
+                                          (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(b >> 32), 63) << 32);
+}
+template <int kCtrl, int kRows>
+__device__ __forceinline__ float max_moved(float x) { return fmaxf(x, __uint_as_float(moved<kCtrl, kRows>(__float_as_uint(x)))); }
+__device__ __forceinline__ float wave_max(float x) {
+    x = max_moved<0x111, 0xF>(x);
+    x = max_moved<0x112, 0xF>(x);
+    x = max_moved<0x114, 0xF>(x);
+    x = max_moved<0x118, 0xF>(x);
+    x = max_moved<0x142, 0xA>(x);
+    x = max_moved<0x143, 0xC>(x);
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), 63));
+}
+
+// 1 / sqrt(a), a > 0, normal and finite
+__device__ __forceinline__ double reciprocal_root(double a) {
+    const double y = __builtin_amdgcn_rsq(a);
+    return fma(0.5 * y, fma(-a * y, y, 1.0), y);
+}
+
+// A workgroup has blockDim / 64 / W tokens at a time.  LW: the weights lie in LDS, as the lanes read them.  kThreads: most
+// threads of a workgroup, for the registers.
+template <bool XB, bool RB, int R, int kThreads, bool LW>
+__global__ __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1) void k_add_norm(NormArgs a, int W) {
     __shared__ double s_sum[2][kMaxThreads / 64];
     __shared__ float s_top[2][kMaxThreads / 64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
-    const int groups = blockDim.x >> 4, t = tid & 15;
+    __shared__ __attribute__((aligned(16))) char s_w[LW ? kMaxWeights : 16];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    const int part = wave % W, tokens = waves / W;  // this wave's of its token's; tokens of the workgroup
     const int nblk = (int)(a.K / kRot);
     uint32_t at[R];  // this lane's first element of each block; absent blocks are zeros and are not stored
 #pragma unroll
     for (int r = 0; r < R; r++) {
-        const int b = (tid >> 4) + r * groups;
-        at[r] = b < nblk ? (uint32_t)(b * kRot + 16 * fwht_row16_nibble(t)) : kOutside;
+        const int b = r * 4 * W + 4 * part + (lane >> 4);
+        at[r] = b < nblk ? (uint32_t)(b * kRot + 16 * fwht_row16_nibble(lane & 15)) : kOutside;
     }
     auto row = [&](const void *base, int64_t m, int64_t stride, int64_t bytes) {  // a token past the last: empty
         const bool in = m < a.M;
@@ -80,33 +123,42 @@ __global__ __launch_bounds__(kMaxThreads) void k_add_norm(NormArgs a) {
     };
     const bool has_r = a.r != nullptr;
     const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc((void *)a.w, (short)0, (int)(a.K * 4), 0x00020000);
-    Raw16<false> w[R];
+    // 16 bytes a lane, lanes side by side
+    auto w_place = [&](int r, int i) { return reinterpret_cast<u32x4 *>(s_w) + (((r * W + part) * 4 + i) * 64 + lane); };
+    if constexpr (LW) {
+        if (wave < W) {
 #pragma unroll
-    for (int r = 0; r < R; r++) w[r].load(wr, at[r]);
-
-    struct Token {
+            for (int r = 0; r < R; r++) {
+                Raw16<false> w;
+                w.load(wr, at[r]);
+#pragma unroll
+                for (int i = 0; i < 4; i++) *w_place(r, i) = w.a[i];
+            }
+        }
+        __syncthreads();
+    }
+    int par = 0;
+    // a wave that is left over where W does not divide the waves, or stands behind the last token, goes along with empty rows
+    for (int64_t m0 = (int64_t)blockIdx.x * tokens; m0 < a.M; m0 += (int64_t)gridDim.x * tokens, par ^= 1) {
+        const int64_t m = wave / W < tokens ? m0 + wave / W : a.M;
         Raw16<XB> x[R];
-        Raw16<RB> r[R];
-    };
-    auto load = [&](int64_t m, Token &v) {
+        Raw16<RB> res[R];
         const __amdgpu_buffer_rsrc_t rx = row(a.x, m, a.x_stride * (XB ? 2 : 4), a.K * (XB ? 2 : 4));
 #pragma unroll
-        for (int r = 0; r < R; r++) v.x[r].load(rx, at[r]);
+        for (int r = 0; r < R; r++) x[r].load(rx, at[r]);
         if (has_r) {
             const __amdgpu_buffer_rsrc_t rr = row(a.r, m, a.r_stride * (RB ? 2 : 4), a.K * (RB ? 2 : 4));
 #pragma unroll
-            for (int r = 0; r < R; r++) v.r[r].load(rr, at[r]);
+            for (int r = 0; r < R; r++) res[r].load(rr, at[r]);
         }
-    };
-    auto finish = [&](int64_t m, const Token &in, int par) {
         float v[R][16];
         double sum = 0.0;
 #pragma unroll
         for (int r = 0; r < R; r++) {
-            in.x[r].values(v[r]);
+            x[r].values(v[r]);
             if (has_r) {
                 float y[16];
-                in.r[r].values(y);
+                res[r].values(y);
 #pragma unroll
                 for (int i = 0; i < 16; i++) v[r][i] = v[r][i] + y[i];
                 if constexpr (RB) {
@@ -126,17 +178,27 @@ __global__ __launch_bounds__(kMaxThreads) void k_add_norm(NormArgs a) {
 #pragma unroll
             for (int r = 0; r < R; r++) store16(rh, at[r], RB, v[r]);
         }
-#pragma unroll
-        for (int s = 32; s > 0; s >>= 1) sum += __shfl_xor(sum, s);
-        if (lane == 0) s_sum[par][wave] = sum;
-        __syncthreads();
-        sum = s_sum[par][0];
-        for (int i = 1; i < waves; i++) sum += s_sum[par][i];
-        const float f = (float)(1.0 / sqrt(sum / (double)a.K + a.eps));
+        // a wave reads s_sum[par] and s_top[par] before the next token's first barrier, and they are written
+        // again one token later, behind it
+        sum = wave_sum(sum);
+        if (W > 1) {
+            s_sum[par][wave] = sum;
+            __syncthreads();
+            sum = s_sum[par][wave - part];
+            for (int i = 1; i < W; i++) sum += s_sum[par][wave - part + i];
+        }
+        const float f = (float)reciprocal_root(sum / (double)a.K + a.eps);
 #pragma unroll
         for (int r = 0; r < R; r++) {
+            Raw16<false> w;
+            if constexpr (LW) {
+#pragma unroll
+                for (int i = 0; i < 4; i++) w.a[i] = *w_place(r, i);
+            } else {
+                w.load(wr, at[r]);
+            }
             float wv[16];
-            w[r].values(wv);
+            w.values(wv);
 #pragma unroll
             for (int i = 0; i < 16; i++) v[r][i] = v[r][i] * f * (wv[i] + a.offset);
         }
@@ -146,83 +208,65 @@ __global__ __launch_bounds__(kMaxThreads) void k_add_norm(NormArgs a) {
 #pragma unroll
             for (int r = 0; r < R; r++) store16(rn, at[r], a.normed_bf16, v[r]);
         }
-        if (!a.x_q) return;
+        if (!a.x_q) continue;
         // as k_prepare_tokens has it
         float top = 0.0f;
 #pragma unroll
         for (int r = 0; r < R; r++) {
-            fwht256_row16(v[r], t);
+            fwht256_row16(v[r], lane & 15);
 #pragma unroll
             for (int i = 0; i < 16; i++) top = fmaxf(top, fabsf(v[r][i]));
         }
-#pragma unroll
-        for (int s = 32; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
-        if (lane == 0) s_top[par][wave] = top;
-        __syncthreads();
-        top = s_top[par][0];
-        for (int i = 1; i < waves; i++) top = fmaxf(top, s_top[par][i]);
+        top = wave_max(top);
+        if (W > 1) {
+            s_top[par][wave] = top;
+            __syncthreads();
+            top = s_top[par][wave - part];
+            for (int i = 1; i < W; i++) top = fmaxf(top, s_top[par][wave - part + i]);
+        }
         const float s = top / 127.0f, rs = s >= kQuantFastMin ? 1.0f / s : 0.0f;
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s), row(a.s_x, m, 4, 4), tid == 0 ? 0u : kOutside, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s), row(a.s_x, m, 4, 4), part == 0 && lane == 0 ? 0u : kOutside, 0, 0);
         const __amdgpu_buffer_rsrc_t rq = row(a.x_q, m, a.K, a.K);
 #pragma unroll
         for (int r = 0; r < R; r++) {
             const uint4 q = top > 0.0f ? quant16_auto(v[r], s, rs) : make_uint4(0, 0, 0, 0);
             __builtin_amdgcn_raw_buffer_store_b128(u32x4{q.x, q.y, q.z, q.w}, rq, at[r], 0, 0);
         }
-    };
-
-    // a thread reads s_sum[par] and s_top[par] before the next token's first barrier and they are written
-    // again one token later, after it
-    const int64_t step = gridDim.x;
-    int64_t m = blockIdx.x;  // < M: the grid is at most M
-    if constexpr (R == 1) {
-        Token A, B;
-        load(m, A);
-        for (;;) {
-            load(m + step, B);
-            finish(m, A, 0);
-            m += step;
-            if (m >= a.M) break;
-            load(m + step, A);
-            finish(m, B, 1);
-            m += step;
-            if (m >= a.M) break;
-        }
-    } else {
-        // longer rows: the registers hold one token
-        for (int par = 0; m < a.M; m += step, par ^= 1) {
-            Token A;
-            load(m, A);
-            finish(m, A, par);
-        }
     }
 }
 
-template <bool XB, bool RB, int R>
-hipError_t launch_r(const NormArgs &a, int num_cu, unsigned threads, hipStream_t stream) {
-    // as many workgroups as the card holds at once (looked up once per size)
-    static std::atomic<int> per_cu[kMaxThreads / 64 + 1];
-    int pc = per_cu[threads / 64].load(std::memory_order_relaxed);
-    if (pc == 0) {
-        const hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&pc, k_add_norm<XB, RB, R>, (int)threads, 0);
-        if (e != hipSuccess) return e;
-        if (pc < 1) pc = 1;
-        per_cu[threads / 64].store(pc, std::memory_order_relaxed);
+constexpr int kWavesPerCu = 16;  // tokens' waves on a compute unit: what the registers hold at R 3
+
+template <bool XB, bool RB, int R, int kThreads>
+hipError_t launch_r(const NormArgs &a, int W, int num_cu, hipStream_t stream) {
+    // workgroups of four waves or one token
+    const int waves = W >= 4 || W == 3 ? W : 4;
+    const int64_t tokens = waves / W, need = (a.M + tokens - 1) / tokens;
+    const int64_t most = kWavesPerCu / waves > 1 ? (int64_t)num_cu * (kWavesPerCu / waves) : num_cu;
+    const unsigned grid = (unsigned)(need < most ? need : most);
+    // weights in LDS where a workgroup has several tokens
+    if constexpr (R <= 3) {
+        if (256 * 16 * R * W <= kMaxWeights && need > most) {
+            k_add_norm<XB, RB, R, kThreads, true><<<grid, 64 * waves, 0, stream>>>(a, W);
+            return hipGetLastError();
+        }
     }
-    const int64_t most = (int64_t)num_cu * pc;
-    k_add_norm<XB, RB, R><<<(unsigned)(a.M < most ? a.M : most), threads, 0, stream>>>(a);
+    k_add_norm<XB, RB, R, kThreads, false><<<grid, 64 * waves, 0, stream>>>(a, W);
     return hipGetLastError();
 }
 
+// Blocks a group of 16 lanes (fp32 to bf16; 1, 2 and 3): 1 token of 5120 5.5, 5.0 and 6.2 us, 512 10.6, 9.3 and 9.5, 2048 29.3, 26.2 and
+// 27.1, 8192 102, 89 and 79, where 2 and 3 leave as many places of a token's waves empty; 8192 x 4096 bf16 2 59 and 3
+// 67, 3000 x 8192 47 and 56, where 3 leaves more; 16384 x 1024 bf16 1 32 and 2 37.  4 and 5 blocks in workgroups of 256 threads
+// spill or have too few waves: 8192 x 5120 94 and 82 at best.
 template <bool XB, bool RB>
 hipError_t launch_t(const NormArgs &a, int num_cu, hipStream_t stream) {
-    const int64_t nblk = a.K / kRot, need = (nblk * 16 + kMaxThreads - 1) / kMaxThreads, rounds = need <= 2 ? need : 4;
-    const unsigned threads = (unsigned)(((nblk + rounds - 1) / rounds * 16 + 63) / 64 * 64);
-    switch (rounds) {
-        case 1: return launch_r<XB, RB, 1>(a, num_cu, threads, stream);
-        case 2: return launch_r<XB, RB, 2>(a, num_cu, threads, stream);
-        default: return launch_r<XB, RB, 4>(a, num_cu, threads, stream);
-    }
+    const int64_t nblk = a.K / kRot;
+    auto W = [&](int r) { return (int)((nblk + 4 * r - 1) / (4 * r)); };
+    if (W(1) == 1) return launch_r<XB, RB, 1, 1024>(a, 1, num_cu, stream);
+    if (W(2) > 16) return launch_r<XB, RB, 4, 1024>(a, W(4), num_cu, stream);
+    if (a.M >= 4096 && W(3) <= 4 && 3 * W(3) <= 2 * W(2)) return launch_r<XB, RB, 3, 256>(a, W(3), num_cu, stream);
+    return launch_r<XB, RB, 2, 1024>(a, W(2), num_cu, stream);
 }
 
 }  // namespace
