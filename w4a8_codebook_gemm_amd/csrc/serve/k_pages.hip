@@ -41,12 +41,35 @@ __device__ __forceinline__ Sums scan_threads(int64_t a, int64_t b, int64_t (*s_p
     return Sums{(wave ? fa : 0) + ia - a, (wave ? fb : 0) + ib - b, lane_value(pa, kWaves - 1), lane_value(pb, kWaves - 1)};
 }
 
-// The last i < n with at[i] <= x, at not decreasing and at[0] <= x.
-template <class T>
-__device__ __forceinline__ int find_last(const T *at, int n, T x) {
+// The same of one 32-bit number.
+__device__ __forceinline__ int scan32(int x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);  // row_shr:1, 2, 4, 8
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);  // row_bcast:15, 31
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);
+    return x;
+}
+__device__ __forceinline__ int scan_threads32(int a, int *s_part, int &all) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int incl = scan32(a);
+    __syncthreads();  // the last ones have been read
+    if (lane == 63) s_part[wave] = incl;
+    __syncthreads();
+    const int parts = scan32(lane < kWaves ? s_part[lane & (kWaves - 1)] : 0);
+    const int before = __shfl(parts, wave > 0 ? wave - 1 : 0);
+    all = lane_value(parts, kWaves - 1);
+    return (wave ? before : 0) + incl - a;
+}
+
+// The last i with at[i] <= x of kThreads numbers that do not decrease, at[0] <= x.  (Behind the last sequence they are the
+// total, which is above every x.)
+__device__ __forceinline__ int find_last(const int *at, int x) {
     int lo = 0;
+#pragma unroll
     for (int step = kThreads / 2; step > 0; step >>= 1)
-        if (lo + step < n && at[lo + step] <= x) lo += step;
+        if (at[lo + step] <= x) lo += step;
     return lo;
 }
 
@@ -79,7 +102,6 @@ __global__ __launch_bounds__(kThreads) void k_pages_assign(w4a8_pages p, int shi
         const int64_t lack = ((old + n + P - 1) >> shift) - need;
         const Sums t = scan_threads(need - have, lack, s_part);
         const int all_tokens = (int)((token0 + s.all_a < M ? token0 + s.all_a : M) - (token0 < M ? token0 : M));
-        const int seqs = (int)(p.B - b0 < kThreads ? p.B - b0 : kThreads);
         const int64_t base = token0 < M ? token0 : M;
         s_token[tid] = (int)(row - base);
         s_page[tid] = (int)t.a;  // (the tokens are M at most)
@@ -91,7 +113,7 @@ __global__ __launch_bounds__(kThreads) void k_pages_assign(w4a8_pages p, int shi
                 if (b == p.B - 1) out.cu_tokens[p.B] = (int)end;
             }
             for (int64_t i = first; i < all_tokens; i += share) {
-                const int q = find_last(s_token, seqs, (int)i);
+                const int q = find_last(s_token, (int)i);
                 const int64_t pos = s_old[q] + (i - s_token[q]);
                 const int64_t entry = pos >> shift, held_pages = (s_old[q] + P - 1) >> shift;
                 int page = -1;
@@ -102,7 +124,7 @@ __global__ __launch_bounds__(kThreads) void k_pages_assign(w4a8_pages p, int shi
                 out.slots[base + i] = (uint32_t)page < (uint64_t)p.num_pages ? ((int64_t)page << shift) + (pos & (P - 1)) : -1;
             }
             for (int64_t i = first; i < t.all_a; i += share) {
-                const int q = find_last(s_page, seqs, (int)i);
+                const int q = find_last(s_page, (int)i);
                 const int64_t entry = ((s_old[q] + P - 1) >> shift) + (i - s_page[q]);
                 p.page_table[(b0 + q) * p.table_width + entry] = taken(page0 + i);
             }
@@ -128,60 +150,64 @@ __global__ __launch_bounds__(kThreads) void k_pages_assign(w4a8_pages p, int shi
     }
 }
 
-// From the last sequence to the first, and within one from its last page down.
+// From the last sequence to the first, and within one from its last page down.  1024 sequences at a time, or fewer
+// where their tables have more than 2^30 entries: page counts are 32-bit numbers then.  What a page costs is the
+// instructions of finding it on one compute unit: 24,000 of 1021 sequences take 27 us with 64-bit counts.
 __global__ __launch_bounds__(kThreads) void k_pages_release(w4a8_pages p, int shift, const int32_t *__restrict__ keep_lens,
                                                             int32_t *lens, int32_t *free_count) {
-    __shared__ int64_t s_part[kWaves][2];
-    __shared__ int64_t s_first[kThreads];  // pages behind a sequence's, of the 1024
-    __shared__ int s_have[kThreads];
+    __shared__ int s_part[kWaves];
+    __shared__ int s_first[kThreads];     // pages behind a sequence's, of those at hand
+    __shared__ int64_t s_entry[kThreads];  // its last page's entry in the table, and as many more
     const int tid = threadIdx.x;
-    const int64_t P = int64_t(1) << shift, most = p.table_width << shift;
-    int64_t count = held(p.free_count[0], p.num_pages);
-    for (int64_t b0 = 0; b0 < p.B; b0 += kThreads) {
-        const int64_t b = p.B - 1 - (b0 + tid);  // thread 0 has the last one
+    const int P = 1 << shift, most = (int)(p.table_width << shift);
+    const int at_once = p.table_width > (int64_t(1) << 20) ? (int)((int64_t(1) << 30) / p.table_width) : kThreads;
+    int count = held(p.free_count[0], p.num_pages);
+    for (int64_t b0 = 0; b0 < p.B; b0 += at_once) {
+        const int seqs = (int)(p.B - b0 < at_once ? p.B - b0 : at_once);
+        const int64_t end = p.B - 1 - b0;  // thread 0 has the last one
         int have = 0, gone = 0;
-        if (b >= 0) {
-            const int old = held(p.seq_lens[b], most), keep = held(keep_lens[b], old);
-            have = (int)((old + P - 1) >> shift);
-            gone = have - (int)((keep + P - 1) >> shift);
-            lens[b] = keep;
+        if (tid < seqs) {
+            const int old = held(p.seq_lens[end - tid], most), keep = held(keep_lens[end - tid], old);
+            have = (int)(((uint32_t)old + (P - 1)) >> shift);
+            gone = have - (int)(((uint32_t)keep + (P - 1)) >> shift);
+            lens[end - tid] = keep;
         }
-        const Sums s = scan_threads(gone, 0, s_part);
-        s_first[tid] = s.a;
-        s_have[tid] = have;
+        int all;
+        const int first = scan_threads32(gone, s_part, all);
+        s_first[tid] = first;
+        s_entry[tid] = (end - tid) * p.table_width + have - 1 + first;
         __syncthreads();
-        const int seqs = (int)(p.B - b0 < kThreads ? p.B - b0 : kThreads);
-        for (int64_t i0 = 0; i0 < s.all_a; i0 += kThreads * kPerThread) {
+        auto load = [&](int i0, int page[kPerThread]) {
+#pragma unroll
+            for (int j = 0; j < kPerThread; j++) {
+                const int i = i0 + tid * kPerThread + j;
+                page[j] = i < all ? p.page_table[s_entry[find_last(s_first, i)] - i] : -1;
+            }
+        };
+        int next[kPerThread];
+        load(0, next);
+        for (int i0 = 0; i0 < all; i0 += kThreads * kPerThread) {
             int page[kPerThread];
             int n = 0;
 #pragma unroll
             for (int j = 0; j < kPerThread; j++) {
-                const int64_t i = i0 + tid * kPerThread + j;
-                page[j] = -1;
-                if (i < s.all_a) {
-                    const int q = find_last(s_first, seqs, i);
-                    page[j] = p.page_table[(p.B - 1 - (b0 + q)) * p.table_width + (s_have[q] - 1 - (i - s_first[q]))];
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < kPerThread; j++) {
-                if (page[j] >= p.num_pages) page[j] = -1;
+                page[j] = next[j] < p.num_pages ? next[j] : -1;
                 n += page[j] >= 0;
             }
-            const Sums t = scan_threads(n, 0, s_part);
-            int64_t at = count + t.a;
+            load(i0 + kThreads * kPerThread, next);  // on their way while these are counted
+            int taken;
+            int at = scan_threads32(n, s_part, taken);
 #pragma unroll
             for (int j = 0; j < kPerThread; j++)
                 if (page[j] >= 0) {
-                    if (at < p.num_pages) p.free_pages[at] = page[j];
+                    if (at < p.num_pages - count) p.free_pages[count + at] = page[j];
                     at++;
                 }
-            count += t.all_a;
-            if (count > p.num_pages) count = p.num_pages;
+            count = taken < p.num_pages - count ? count + taken : (int)p.num_pages;
         }
         __syncthreads();
     }
-    if (tid == 0) free_count[0] = (int)count;
+    if (tid == 0) free_count[0] = count;
 }
 
 }  // namespace
