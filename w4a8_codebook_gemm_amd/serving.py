@@ -116,21 +116,21 @@ class Prepared(NamedTuple):
     normed: torch.Tensor | None   # [M, K]
 
 
-def _matrix(t, name: str, m, k, dev):
+def _matrix(t, name: str, shape, dev):
     """Pointer, dtype code and row stride of [M, K] rows of consecutive values."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
     dt = t.dtype
-    if dt not in _FLOATS:
+    if dt is not torch.bfloat16 and dt is not torch.float32:
         raise TypeError(f"{name} has dtype {dt}, expected one of {_FLOATS}")
-    if t.dim() != 2 or t.shape[0] != m or t.shape[1] != k:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(m, k)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     st, sk = t.stride()
-    if sk != 1 and k != 1:
+    if sk != 1 and shape[1] != 1:
         raise ValueError(f"{name}: the values of a row must be consecutive, strides are {t.stride()}")
-    return t.data_ptr(), BF16 if dt is torch.bfloat16 else F32, st if m > 1 else k
+    return t.data_ptr(), BF16 if dt is torch.bfloat16 else F32, st if shape[0] > 1 else shape[1]
 
 
 def add_norm_prepare(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, *, eps: float = 1e-6,
@@ -144,26 +144,30 @@ def add_norm_prepare(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tens
     contiguous, of the residual's type: may be the residual.  out: (x_q, s_x) to write into."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be 2-D [M, K]")
-    m, k = x.shape
+    shape = x.shape
+    m, k = shape
     dev = x.device
     if dev.type != "cuda":
         raise ValueError(f"x must be on a GPU device, got {dev}")
-    xp, xdt, xs = _matrix(x, "x", m, k, dev)
+    # (torch makes a tensor like another one sooner than one from keywords)
+    dense = x.is_contiguous()
+    xp, xdt, xs = _matrix(x, "x", shape, dev)
+    wp = _ptr(weight, "weight", torch.float32, (k,), dev)
     rp, rdt, rs, hp = 0, 0, 0, 0
     if residual is not None:
-        rp, rdt, rs = _matrix(residual, "residual", m, k, dev)
+        rp, rdt, rs = _matrix(residual, "residual", shape, dev)
         if h_out is None:
-            h_out = torch.empty((m, k), dtype=residual.dtype, device=dev)
+            h_out = torch.empty_like(residual) if residual.is_contiguous() else residual.new_empty(m, k)
             hp = h_out.data_ptr()
         else:
-            hp = _ptr(h_out, "h_out", residual.dtype, (m, k), dev)
+            hp = _ptr(h_out, "h_out", residual.dtype, shape, dev)
     elif h_out is not None:
         raise ValueError("h_out without a residual")
     normed, np_, ndt = None, 0, 0
     if normed_dtype is not None:
         if normed_dtype not in _FLOATS:
             raise TypeError(f"normed_dtype {normed_dtype}, expected one of {_FLOATS}")
-        normed = torch.empty((m, k), dtype=normed_dtype, device=dev)
+        normed = torch.empty_like(x, dtype=normed_dtype) if dense else x.new_empty((m, k), dtype=normed_dtype)
         np_, ndt = normed.data_ptr(), BF16 if normed_dtype is torch.bfloat16 else F32
     elif not quantise:
         raise ValueError("neither the quantised norm nor the norm itself is wanted")
@@ -171,16 +175,16 @@ def add_norm_prepare(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tens
     qp = sp = 0
     if quantise:
         if out is None:
-            x_q = torch.empty((m, k), dtype=torch.int8, device=dev)
-            s_x = torch.empty((m,), dtype=torch.float32, device=dev)
+            x_q = torch.empty_like(x, dtype=torch.int8) if dense else x.new_empty((m, k), dtype=torch.int8)
+            s_x = weight.new_empty(m)
             qp, sp = x_q.data_ptr(), s_x.data_ptr()
         else:
             x_q, s_x = out
-            qp, sp = _ptr(x_q, "x_q", torch.int8, (m, k), dev), _ptr(s_x, "s_x", torch.float32, (m,), dev)
+            qp, sp = _ptr(x_q, "x_q", torch.int8, shape, dev), _ptr(s_x, "s_x", torch.float32, (m,), dev)
     elif out is not None:
         raise ValueError("out without quantise")
-    _launch(dev, "w4a8_add_norm_prepare", lib().w4a8_add_norm_prepare, xp, xdt, xs, rp, rdt, rs,
-            _ptr(weight, "weight", torch.float32, (k,), dev), weight_offset, eps, m, k, hp, np_, ndt, qp, sp)
+    _launch(dev, "w4a8_add_norm_prepare", lib().w4a8_add_norm_prepare, xp, xdt, xs, rp, rdt, rs, wp, weight_offset, eps, m, k,
+            hp, np_, ndt, qp, sp)
     return Prepared(h_out, x_q, s_x, normed)
 
 
