@@ -34,6 +34,9 @@ constexpr int kMaxShare = 4 * kWaves;
 template <int NB>
 constexpr int kOver = NB == 2 ? 4 : 8;
 constexpr int kTail = 3;
+// Whole units for single waves, which then join nothing: where every wave has one or more, and the longest unit is longer than
+// the average by no more tiles than a workgroup has units.
+constexpr int kSoloOver = 2;  // as kOver
 
 template <int D, int NB>
 struct Layout {
@@ -68,8 +71,9 @@ __device__ __forceinline__ typename Bytes<N>::type load_once(const uint8_t *p) {
     }
 }
 
-// kSmall: pages of 16 positions, else of 32 or more: a page for all lanes' part of a tile.
-template <int D, int NB, bool BF16, bool kSmall>
+// kSmall: pages of 16 positions, else of 32 or more: a page for all lanes' part of a tile.  MANY: batches of so many units that
+// each wave may have whole ones.
+template <int D, int NB, bool BF16, bool kSmall, bool MANY>
 __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a, int wgs) {
     using Lay = Layout<D, NB>;
     constexpr int RB = Lay::RB;
@@ -81,7 +85,7 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a,
     constexpr int kVW = kVB < 4 ? 1 : kVB / 4;  // dwords they are held in
     __shared__ __attribute__((aligned(16))) float s_o[Lay::kLds];
     constexpr int kQ = NB * kParts * kS * 64;  // fragments of a unit's queries
-    __shared__ half8_t s_q[kQ];
+    __shared__ half8_t s_q[(MANY ? kWaves : 1) * kQ];
     __shared__ float s_m[kWaves][RB], s_l[kWaves][RB];
     __shared__ float2 s_all[RB];
     __shared__ int s_flag;
@@ -105,17 +109,41 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a,
     int64_t units, none;
     int64_t line = total(0, 0, units);
     if (line == 0) return;
+    bool solo = false;  // uniform over the grid
+    if constexpr (MANY) {
+        int longest = 0;
+        for (int64_t b0 = 0; b0 < a.s.B; b0 += 64) {
+            if (a.s.B > 64) x = seq_work<RB, T>(a, b0 + lane);
+            longest = longest > x.tiles ? longest : x.tiles;
+        }
+#pragma unroll
+        for (int i = 1; i < 64; i <<= 1) {
+            const int o = __shfl_xor(longest, i);
+            longest = longest > o ? longest : o;
+        }
+        solo = units >= (int64_t)wgs * kWaves && __builtin_amdgcn_readfirstlane(longest) - div64(line, units) <= div64(units, wgs);
+    }
+    auto sync = [&]() {
+        if (solo) {
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        } else {
+            __syncthreads();
+        }
+    };
+    const int step = solo ? 1 : kWaves;
     int share = 0;
-    for (int64_t c = div64(line + (int64_t)wgs * kWaves - 1, (int64_t)wgs * kWaves) * kWaves; c <= kMaxShare && share == 0; c += kWaves) {
+    if (!solo) for (int64_t c = div64(line + (int64_t)wgs * kWaves - 1, (int64_t)wgs * kWaves) * kWaves; c <= kMaxShare && share == 0; c += kWaves) {
         const int64_t sum = total((int)c, 0, none);
         if (sum <= (int64_t)wgs * c) {
             share = (int)c;
             line = sum;
         }
     }
-    const int over = share == 0 && (NB == 1 || units >= wgs) ? kOver<NB> : 0;
+    const int over = solo ? kSoloOver : share == 0 && (NB == 1 || units >= wgs) ? kOver<NB> : 0;
     line += over * units;
-    const int64_t used = share ? div64(line, share) : wgs, w = blockIdx.x;
+    const int64_t used = share ? div64(line, share) : solo ? (int64_t)wgs * kWaves : wgs;
+    const int64_t w = solo ? (int64_t)blockIdx.x * kWaves + wave : blockIdx.x;
     if (w >= used) return;
     const Line cut{line, used, over, share ? 1 : kTail};
     const int64_t t1 = cut.begin(w + 1);
@@ -151,7 +179,11 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a,
         const int64_t unit0 = base + unit * length;         // the unit's first tile on the line
         const int64_t unit1 = unit0 + length;
         int tile0, tile1;
-        if (!cut.part(at, t1, unit0, unit1, tiles, tile0, tile1)) {
+        if (solo) {  // the units that begin in this wave's part
+            tile0 = 0;
+            tile1 = tiles;
+        }
+        if (solo ? unit0 < at : !cut.part(at, t1, unit0, unit1, tiles, tile0, tile1)) {
             at = unit1;
             continue;
         }
@@ -191,8 +223,8 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a,
         }
 
         const int end = lo_tile + tile1;
-        int first = lo_tile + tile0 + wave;
-        if (first < any_lo / T) first += (any_lo / T - first + kWaves - 1) / kWaves * kWaves;
+        int first = lo_tile + tile0 + (solo ? 0 : wave);
+        if (first < any_lo / T) first += (any_lo / T - first + step - 1) / step * step;
         const int stop = end < tiles_to<T>(any_hi) ? end : tiles_to<T>(any_hi);
         const int P = a.c.page_size, pm = P - 1;
         const int32_t *table = a.s.page_table + b * a.s.table_width;
@@ -303,7 +335,8 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a,
             int ex = 0;
             if (top > 0.0f) frexpf(top, &ex);
             fac[nb] = fmaxf(ldexpf(fabsf(a.scale) * kLog2e * k_part, ex + k_exp - 14 + kValueExp), 0x1p-126f);
-            if (wave == nb) {
+            if (solo || wave == nb) {
+                half8_t *sq = s_q + (solo ? wave * kQ : 0);
 #pragma unroll
                 for (int c = 0; c < kS; c++) {
                     half8_t q0, q1;
@@ -315,12 +348,12 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a,
                         q0[i] = (_Float16)y;
                         q1[i] = (_Float16)(y - (float)(_Float16)y);
                     }
-                    s_q[(nb * kParts * kS + c) * 64 + lane] = q0;
-                    if constexpr (kParts == 2) s_q[((nb * kParts + 1) * kS + c) * 64 + lane] = q1;
+                    sq[(nb * kParts * kS + c) * 64 + lane] = q0;
+                    if constexpr (kParts == 2) sq[((nb * kParts + 1) * kS + c) * 64 + lane] = q1;
                 }
             }
         }
-        __syncthreads();
+        sync();
 
         floatx4 o[NB][kT];
         float m[NB], L[NB];
@@ -340,7 +373,7 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a,
             for (int nb = 0; nb < NB; nb++)
 #pragma unroll
                 for (int x = 0; x < U; x++) s[nb][x][0] = s[nb][x][1] = floatx4{0, 0, 0, 0};
-            const half8_t *qp = s_q + fresh(lane);
+            const half8_t *qp = s_q + (solo ? wave * kQ : 0) + fresh(lane);
             half8_t qf[2][NB][kParts];  // this step's and the next one's
             auto take_q = [&](int c) {
 #pragma unroll
@@ -368,7 +401,7 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a,
                     }
                 __builtin_amdgcn_sched_barrier(0);
             }
-            if constexpr (kMore) load_k(tile + kWaves, cd);
+            if constexpr (kMore) load_k(tile + step, cd);
             __builtin_amdgcn_sched_barrier(0);
             const uint32_t there = cd.there;
             const bool whole = tile * T >= all_lo && all_hi - tile * T >= T && __all(there == (1u << U) - 1);
@@ -448,11 +481,11 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a,
                         __builtin_amdgcn_sched_barrier(0);
                     }
             }
-            if constexpr (kMore) load_v(tile + kWaves, cd);
+            if constexpr (kMore) load_v(tile + step, cd);
         };
         if (first < stop) {
             int tile = first;
-            for (; tile + kWaves < stop; tile += kWaves) work(tile, std::true_type());
+            for (; tile + step < stop; tile += step) work(tile, std::true_type());
             work(tile, std::false_type());
         }
 
@@ -483,7 +516,41 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a,
                 }
             }
         };
-        __syncthreads();
+        int v_exp;
+        const float v_part = frexpf(a.c.v_unit[h], &v_exp);
+        // four values of row r, from value d on, to o; the sum of the probabilities carries the same 2^14 as the products
+        auto finish = [&](int r, int d, const float v[4], float L) {
+            const float inv = L > 0.0f ? v_part / L : 0.0f;
+            float y[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) y[i] = ldexpf(v[i] * inv, v_exp + kValueExp);
+            int token, head;
+            row_at(r, token, head);
+            const int64_t off = ((q.first + token) * a.hq + head) * D + d;
+            if constexpr (BF16)
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.o) + off) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+            else
+                *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + off) = make_float4(y[0], y[1], y[2], y[3]);
+        };
+        sync();
+        if (solo) {
+#pragma unroll
+            for (int x = 0; x < kItems; x++) {
+                if (x * kSumRows >= nrows) break;
+                spread(x);
+                sync();
+#pragma unroll
+                for (int y = 0; y < kSumRows * D / 256; y++) {
+                    const int i = 64 * y + lane, sr = i / (D / 4), sd = 4 * (i % (D / 4)), r = x * kSumRows + sr;
+                    const float4 f = *reinterpret_cast<const float4 *>(s_o + (wave * kSumRows + sr) * Lay::kRow + sd);
+                    const float v[4] = {f.x, f.y, f.z, f.w};
+                    if (r < nrows) finish(r, sd, v, s_l[wave][r]);
+                }
+                sync();
+            }
+            at = unit1;
+            continue;
+        }
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
             const int r = 16 * nb + n;
@@ -565,25 +632,10 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a,
             });
         }
         if (write) {
-            int v_exp;
-            const float v_part = frexpf(a.c.v_unit[h], &v_exp);
 #pragma unroll
             for (int x = 0; x < kItems; x++) {
                 const int r = x * kSumRows + ir;
-                if (r < nrows) {
-                    // the sum of the probabilities carries the same 2^14 as the products
-                    const float inv = st[x].L > 0.0f ? v_part / st[x].L : 0.0f;
-                    float y[4];
-#pragma unroll
-                    for (int i = 0; i < 4; i++) y[i] = ldexpf(v[x][i] * inv, v_exp + kValueExp);
-                    int token, head;
-                    row_at(r, token, head);
-                    const int64_t off = ((q.first + token) * a.hq + head) * D + id;
-                    if constexpr (BF16)
-                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.o) + off) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
-                    else
-                        *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + off) = make_float4(y[0], y[1], y[2], y[3]);
-                }
+                if (r < nrows) finish(r, id, v[x], st[x].L);
             }
         }
         at = unit1;
@@ -593,8 +645,16 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a,
 template <int D, int NB>
 hipError_t launch_nb(const Attn4Args &a, int bf16, int num_cu, hipStream_t stream) {
     const int wgs = kPerCu<NB> * num_cu;
-    auto f = a.page_shift == 4 ? (bf16 ? k_kv4_split<D, NB, true, true> : k_kv4_split<D, NB, false, true>)
-                               : (bf16 ? k_kv4_split<D, NB, true, false> : k_kv4_split<D, NB, false, false>);
+    auto pick = [&](auto many) {
+        constexpr bool M = decltype(many)::value;
+        return a.page_shift == 4 ? (bf16 ? k_kv4_split<D, NB, true, true, M> : k_kv4_split<D, NB, false, true, M>)
+                                 : (bf16 ? k_kv4_split<D, NB, true, false, M> : k_kv4_split<D, NB, false, false, M>);
+    };
+    auto f = pick(std::false_type());
+    // at head_dim 256 the registers do not hold what both ways need
+    if constexpr (NB == 1 && D < 256) {
+        if (a.s.B * a.c.kv_heads >= (int64_t)wgs * kWaves) f = pick(std::true_type());
+    }
     f<<<wgs, kThreads, 0, stream>>>(a, wgs);
     return hipGetLastError();
 }
