@@ -59,7 +59,7 @@ struct Tile {
 template <int D, bool BF16>
 __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves / 4)) void k_kv4_prompt(Attn4Args a, int wgs) {
     using S = Shape<D, BF16>;
-    constexpr int kAhead = D == 128 ? 4 : 2;  // K and V fragments in flight
+    constexpr int kFrags = D == 128 ? 4 : 2;  // K and V fragments in flight
     constexpr int T = S::T, kParts = BF16 ? 1 : 2, kSteps = D / 16, kTiles = D / 32;
     constexpr int kQLds = D == 256 && BF16 ? kQFar : 0;  // query fragments that stay in LDS
     constexpr int kSubs = D == 256 ? 1 : 2, kWide = 32 * kSubs;   // positions of a softmax step: registers
@@ -332,14 +332,14 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
                 floatx16 s[kSubs];
 #pragma unroll
                 for (int y = 0; y < kSubs; y++) s[y] = floatx16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-                half8_t kf[kAhead];
+                half8_t kf[kFrags];
 #pragma unroll
-                for (int x = 0; x < kAhead; x++) kf[x] = k_frag(x);
+                for (int x = 0; x < kFrags; x++) kf[x] = k_frag(x);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int x = 0; x < kSubs * kSteps; x++) {
-                    const half8_t k = kf[x % kAhead];
-                    if (x + kAhead < kSubs * kSteps) kf[x % kAhead] = k_frag(x + kAhead);
+                    const half8_t k = kf[x % kFrags];
+                    if (x + kFrags < kSubs * kSteps) kf[x % kFrags] = k_frag(x + kFrags);
                     const int i = x % kSteps, y = x / kSteps;
                     if (i >= kSteps - kQLds) {
                         const half8_t qx = *reinterpret_cast<const half8_t *>(s_q + (i - (kSteps - kQLds)) * S::kThreads * 16 + tid * 16);
@@ -350,9 +350,9 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
-                half8_t vf[kAhead];
+                half8_t vf[kFrags];
 #pragma unroll
-                for (int x = 0; x < kAhead; x++) vf[x] = v_frag(x);
+                for (int x = 0; x < kFrags; x++) vf[x] = v_frag(x);
                 __builtin_amdgcn_sched_barrier(0);
                 int every = there[0];
 #pragma unroll
@@ -370,7 +370,7 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
 #pragma unroll
                 for (int j = 1; j < 16 * kSubs; j++) top = fmaxf(top, s[j >> 4][j & 15]);
                 top = max_xor32(top);
-                const float mn = fmaxf(m, whole_above(top * fac));
+                const float mn = running_maximum(m, top * fac);
                 const float down = m - mn;
                 if (__any(down < 0.0f)) {
                     const float x = pow2_down(down);
@@ -411,8 +411,8 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
 #pragma unroll
                 for (int x = 0; x < 2 * kSubs * kTiles; x++) {
                     if (kSubs == 2 && x == 2 * kTiles) weights(kSubs - 1);
-                    const half8_t v = vf[x % kAhead];
-                    if (x + kAhead < 2 * kSubs * kTiles) vf[x % kAhead] = v_frag(x + kAhead);
+                    const half8_t v = vf[x % kFrags];
+                    if (x + kFrags < 2 * kSubs * kTiles) vf[x % kFrags] = v_frag(x + kFrags);
 #pragma unroll
                     for (int pt = 0; pt < kParts; pt++)
                         o[x % kTiles] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, pf[x / kTiles][pt], o[x % kTiles], 0, 0, 0);

@@ -426,7 +426,7 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a,
 #pragma unroll
                     for (int j = 0; j < 8; j++) all = fmaxf(all, s[nb][y][j >> 2][j & 3]);
                 all = max_xor32(max_xor16(all));
-                const float mn = fmaxf(m[nb], whole_above(all * fac[nb]));
+                const float mn = running_maximum(m[nb], all * fac[nb]);
                 const float down = m[nb] - mn;             // <= 0
                 const float c = (float)kProbExp - mn;
                 float sum = 0.0f;

@@ -39,10 +39,16 @@ __device__ __forceinline__ half8_t values_natural(uint32_t w, half2_t s) {
 __device__ __forceinline__ uint32_t even_codes(uint32_t first, uint32_t second) { return (first & 0x0F0F0F0Fu) | ((second << 4) & 0xF0F0F0F0u); }
 __device__ __forceinline__ uint32_t odd_codes(uint32_t first, uint32_t second) { return ((first >> 4) & 0x0F0F0F0Fu) | (second & 0xF0F0F0F0u); }
 
-// The running maximum for a largest exponent t = s fac, a whole number.  Exponents are one multiply-add each,
+// The running maximum m, a whole number, after a largest exponent t = s fac.  Exponents are one multiply-add each,
 // s fac - m, which does not round the product as t is rounded: m is 2^-22 of t above it (2 to 4 of its last places),
 // so that none of them passes 0 by rounding.  For |t| up to 2^16 that is 2^-6 before it is rounded up; from 2^26 on it takes a row's
-// weights out of fp16's range.  (Where nothing is seen t is -inf and this no number, which fmaxf passes over.)
-__device__ __forceinline__ float whole_above(float t) { return ceilf(fmaf(fabsf(t), 0x1p-22f, t)); }
+// weights out of fp16's range.  Where m has to grow it grows by kAhead more, so that it seldom does: the weights
+// and sums so far are rescaled each time, D / 2 multiplications a lane.  The largest weight then stands at 2^(kProbExp - 1 - kAhead)
+// or more.  (Where nothing is seen t is -inf, the number above it is none, and m stays.)
+constexpr float kAhead = 3.0f;
+__device__ __forceinline__ float running_maximum(float m, float t) {
+    const float w = ceilf(fmaf(fabsf(t), 0x1p-22f, t));
+    return w > m ? w + kAhead : m;
+}
 
 }  // namespace w4a8
