@@ -23,7 +23,6 @@ namespace {
 
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 
-constexpr int kQFar = 2;          // query fragments of bf16 heads of 256 that stay in LDS
 constexpr int kSchedPV = 0x406;   // what may move over the steps of the second product: vector and scalar arithmetic
 constexpr int kMinTiles = 4;      // tiles a workgroup is worth cutting for
 
@@ -59,15 +58,13 @@ struct Tile {
 template <int D, bool BF16>
 __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves / 4)) void k_kv4_prompt(Attn4Args a, int wgs) {
     using S = Shape<D, BF16>;
-    constexpr int kFrags = D == 128 ? 4 : 2;  // K and V fragments in flight
+    constexpr int kFrags = 2;  // K and V fragments in flight
     constexpr int T = S::T, kParts = BF16 ? 1 : 2, kSteps = D / 16, kTiles = D / 32;
-    constexpr int kQLds = D == 256 && BF16 ? kQFar : 0;  // query fragments that stay in LDS
     constexpr int kSubs = D == 256 ? 1 : 2, kWide = 32 * kSubs;   // positions of a softmax step: registers
     constexpr int kItems = 512 / S::kThreads;  // staging items of a thread: 256 of keys, 256 of values
     using L4 = Tile<D>;
     __shared__ __attribute__((aligned(16))) char s_k[2][L4::kBytes], s_v[2][L4::vBytes];
     __shared__ int s_there[2][S::kGroups];  // of each group of 16 positions: whether its page is there
-    __shared__ __attribute__((aligned(16))) char s_q[kQLds ? kQLds * S::kThreads * 16 : 16];
     __shared__ int64_t s_mine[64], s_incl[64];  // tiles of the only 64 sequences, and up to each
     __shared__ int s_flag;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 31, hh = lane >> 5;
@@ -158,7 +155,7 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
             sees(a, q, div64(r0, a.group), any_lo, all_hi);
             sees(a, q, div64(r0 + nrows - 1, a.group), all_lo, any_hi);
         }
-        half8_t qf[kParts][kSteps - kQLds];
+        half8_t qf[kParts][kSteps];
         float fac;
         {
             float top = 0.0f;
@@ -194,14 +191,9 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
                     v[i] = n < nrows ? ldexpf(a.scale < 0.0f ? -v[i] : v[i], 14 - ex) : 0.0f;
-                    if (s < kSteps - kQLds) {
-                        qf[0][s][i] = (_Float16)v[i];
-                        if constexpr (kParts == 2) qf[1][s][i] = (_Float16)(v[i] - (float)(_Float16)v[i]);
-                    }
+                    qf[0][s][i] = (_Float16)v[i];
+                    if constexpr (kParts == 2) qf[1][s][i] = (_Float16)(v[i] - (float)(_Float16)v[i]);
                 }
-                if (s >= kSteps - kQLds)
-                    *reinterpret_cast<uint4 *>(s_q + (s - (kSteps - kQLds)) * S::kThreads * 16 + tid * 16) =
-                        make_uint4(pack_half(v[0], v[1]), pack_half(v[2], v[3]), pack_half(v[4], v[5]), pack_half(v[6], v[7]));
             }
         }
         floatx16 o[kTiles];
@@ -341,13 +333,8 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
                     const half8_t k = kf[x % kFrags];
                     if (x + kFrags < kSubs * kSteps) kf[x % kFrags] = k_frag(x + kFrags);
                     const int i = x % kSteps, y = x / kSteps;
-                    if (i >= kSteps - kQLds) {
-                        const half8_t qx = *reinterpret_cast<const half8_t *>(s_q + (i - (kSteps - kQLds)) * S::kThreads * 16 + tid * 16);
-                        s[y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, qx, s[y], 0, 0, 0);
-                    } else {
 #pragma unroll
-                        for (int pt = 0; pt < kParts; pt++) s[y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, qf[pt][i < kSteps - kQLds ? i : 0], s[y], 0, 0, 0);
-                    }
+                    for (int pt = 0; pt < kParts; pt++) s[y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, qf[pt][i], s[y], 0, 0, 0);
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 half8_t vf[kFrags];
