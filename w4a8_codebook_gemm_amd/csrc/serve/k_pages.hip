@@ -21,27 +21,8 @@ enum { kTokens = 1, kState = 2 };  // table, offsets, positions, slots; lengths,
 
 __device__ __forceinline__ int held(int64_t x, int64_t most) { return (int)(x < 0 ? 0 : x > most ? most : x); }
 
-// Exclusive prefix sums of two numbers over the workgroup's threads, and their totals.
-struct Sums {
-    int64_t a, b, all_a, all_b;
-};
-__device__ __forceinline__ Sums scan_threads(int64_t a, int64_t b, int64_t (*s_part)[2]) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t ia = scan64(a), ib = scan64(b);
-    __syncthreads();  // the last ones have been read
-    if (lane == 63) {
-        s_part[wave][0] = ia;
-        s_part[wave][1] = ib;
-    }
-    __syncthreads();
-    const int64_t pa = scan64(lane < kWaves ? s_part[lane & (kWaves - 1)][0] : 0);
-    const int64_t pb = scan64(lane < kWaves ? s_part[lane & (kWaves - 1)][1] : 0);
-    const int before = wave > 0 ? wave - 1 : 0;
-    const int64_t fa = __shfl(pa, before), fb = __shfl(pb, before);
-    return Sums{(wave ? fa : 0) + ia - a, (wave ? fb : 0) + ib - b, lane_value(pa, kWaves - 1), lane_value(pb, kWaves - 1)};
-}
-
-// The same of one 32-bit number.
+// Prefix sums over a wave, and exclusive ones over the workgroup's threads with their total: a wave's total counts for
+// `most` at most, so that 16 of them are a 32-bit number (what is beyond it is not asked for).
 __device__ __forceinline__ int scan32(int x) {
     x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);  // row_shr:1, 2, 4, 8
     x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
@@ -51,11 +32,11 @@ __device__ __forceinline__ int scan32(int x) {
     x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);
     return x;
 }
-__device__ __forceinline__ int scan_threads32(int a, int *s_part, int &all) {
+// One barrier: s_part is read before the workgroup's next one, and written again behind that.
+__device__ __forceinline__ int scan_threads(int a, int *s_part, int &all, int most) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int incl = scan32(a);
-    __syncthreads();  // the last ones have been read
-    if (lane == 63) s_part[wave] = incl;
+    if (lane == 63) s_part[wave] = incl < most ? incl : most;
     __syncthreads();
     const int parts = scan32(lane < kWaves ? s_part[lane & (kWaves - 1)] : 0);
     const int before = __shfl(parts, wave > 0 ? wave - 1 : 0);
@@ -75,42 +56,44 @@ __device__ __forceinline__ int find_last(const int *at, int x) {
 
 __global__ __launch_bounds__(kThreads) void k_pages_assign(w4a8_pages p, int shift, const int32_t *__restrict__ new_tokens,
                                                            int64_t M, w4a8_batch out, int what) {
-    __shared__ int64_t s_part[kWaves][2];
+    __shared__ int s_part[2][kWaves], s_lack;
     __shared__ int s_token[kThreads], s_page[kThreads], s_old[kThreads];  // from the 1024 sequences' first on
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, rows = (int)M;
     const int64_t P = int64_t(1) << shift, most = p.table_width << shift;
     const int count = held(p.free_count[0], p.num_pages);
     const int64_t share = (int64_t)gridDim.x * kThreads, first = (int64_t)blockIdx.x * kThreads + tid;
     auto taken = [&](int64_t i) {  // the i-th page off the list
         return i < count ? p.free_pages[count - 1 - i] : -1;
     };
-    int64_t token0 = 0, page0 = 0, lacking = 0;  // in front of the 1024 sequences; pages that tables have no room for
+    if (tid == 0) s_lack = 0;
+    int base = 0, page0 = 0;  // rows and pages in front of the 1024 sequences
     for (int64_t b0 = 0; b0 < p.B; b0 += kThreads) {
         const int64_t b = b0 + tid;
-        int old = 0;
-        int64_t n = 0;
+        int old = 0, n = 0;
         if (b < p.B) {
             old = held(p.seq_lens[b], most);
             n = held(new_tokens[b], M);
         }
         // what lies behind row M - 1 is not there: the rows up to a sequence's first are not known before the sum
-        Sums s = scan_threads(n, 0, s_part);
-        const int64_t at = token0 + s.a, row = at < M ? at : M, end = at + n < M ? at + n : M;
+        int all_tokens, all_pages;
+        const int at = scan_threads(n, s_part[0], all_tokens, rows);
+        const int row = at < rows - base ? base + at : rows, end = n < rows - row ? row + n : rows;
+        all_tokens = all_tokens < rows - base ? all_tokens : rows - base;
         n = end - row;
-        const int64_t len = old + n < most ? old + n : most;
+        const int64_t grown = (int64_t)old + n, len = grown < most ? grown : most;
         const int have = (int)((old + P - 1) >> shift), need = (int)((len + P - 1) >> shift);
-        const int64_t lack = ((old + n + P - 1) >> shift) - need;
-        const Sums t = scan_threads(need - have, lack, s_part);
-        const int all_tokens = (int)((token0 + s.all_a < M ? token0 + s.all_a : M) - (token0 < M ? token0 : M));
-        const int64_t base = token0 < M ? token0 : M;
-        s_token[tid] = (int)(row - base);
-        s_page[tid] = (int)t.a;  // (the tokens are M at most)
+        const int lack = (int)((grown + P - 1) >> shift) - need;  // pages that the table has no room for
+        if (lack) atomicAdd(&s_lack, lack);
+        // (pages, and those that are lacking, are no more than the rows)
+        const int page_at = scan_threads(need - have, s_part[1], all_pages, rows);
+        s_token[tid] = row - base;
+        s_page[tid] = page_at;
         s_old[tid] = old;
         __syncthreads();
         if (what & kTokens) {
             if (blockIdx.x == 0 && b < p.B) {
-                out.cu_tokens[b] = (int)row;
-                if (b == p.B - 1) out.cu_tokens[p.B] = (int)end;
+                out.cu_tokens[b] = row;
+                if (b == p.B - 1) out.cu_tokens[p.B] = end;
             }
             for (int64_t i = first; i < all_tokens; i += share) {
                 const int q = find_last(s_token, (int)i);
@@ -123,29 +106,27 @@ __global__ __launch_bounds__(kThreads) void k_pages_assign(w4a8_pages p, int shi
                 out.positions[base + i] = (int)(pos < INT32_MAX ? pos : INT32_MAX);
                 out.slots[base + i] = (uint32_t)page < (uint64_t)p.num_pages ? ((int64_t)page << shift) + (pos & (P - 1)) : -1;
             }
-            for (int64_t i = first; i < t.all_a; i += share) {
+            for (int64_t i = first; i < all_pages; i += share) {
                 const int q = find_last(s_page, (int)i);
                 const int64_t entry = ((s_old[q] + P - 1) >> shift) + (i - s_page[q]);
                 p.page_table[(b0 + q) * p.table_width + entry] = taken(page0 + i);
             }
         }
         if ((what & kState) && blockIdx.x == 0 && b < p.B) out.seq_lens[b] = (int)len;
-        token0 += s.all_a;
-        page0 += t.all_a;
-        lacking += t.all_b;
+        base += all_tokens;
+        page0 += all_pages;
         __syncthreads();
     }
     if (what & kTokens)
-        for (int64_t i = (token0 < M ? token0 : M) + first; i < M; i += share) {
+        for (int64_t i = base + first; i < M; i += share) {
             out.positions[i] = 0;
             out.slots[i] = -1;
         }
     if (blockIdx.x == 0 && tid == 0) {
         // (every thread of this workgroup has read the count in front of a barrier)
-        const int64_t short_of = (page0 > count ? page0 - count : 0) + lacking;
         if (what & kState) {
-            out.free_count[0] = (int)(page0 < count ? count - page0 : 0);
-            out.missing[0] = (int)(short_of < INT32_MAX ? short_of : INT32_MAX);
+            out.free_count[0] = page0 < count ? count - page0 : 0;
+            out.missing[0] = (page0 > count ? page0 - count : 0) + s_lack;
         }
     }
 }
@@ -155,7 +136,7 @@ __global__ __launch_bounds__(kThreads) void k_pages_assign(w4a8_pages p, int shi
 // instructions of finding it on one compute unit: 24,000 of 1021 sequences take 27 us with 64-bit counts.
 __global__ __launch_bounds__(kThreads) void k_pages_release(w4a8_pages p, int shift, const int32_t *__restrict__ keep_lens,
                                                             int32_t *lens, int32_t *free_count) {
-    __shared__ int s_part[kWaves];
+    __shared__ int s_part[2][kWaves];
     __shared__ int s_first[kThreads];     // pages behind a sequence's, of those at hand
     __shared__ int64_t s_entry[kThreads];  // its last page's entry in the table, and as many more
     const int tid = threadIdx.x;
@@ -173,7 +154,7 @@ __global__ __launch_bounds__(kThreads) void k_pages_release(w4a8_pages p, int sh
             lens[end - tid] = keep;
         }
         int all;
-        const int first = scan_threads32(gone, s_part, all);
+        const int first = scan_threads(gone, s_part[0], all, INT32_MAX);
         s_first[tid] = first;
         s_entry[tid] = (end - tid) * p.table_width + have - 1 + first;
         __syncthreads();
@@ -186,7 +167,8 @@ __global__ __launch_bounds__(kThreads) void k_pages_release(w4a8_pages p, int sh
         };
         int next[kPerThread];
         load(0, next);
-        for (int i0 = 0; i0 < all; i0 += kThreads * kPerThread) {
+        int turn = 1;
+        for (int i0 = 0; i0 < all; i0 += kThreads * kPerThread, turn ^= 1) {
             int page[kPerThread];
             int n = 0;
 #pragma unroll
@@ -196,7 +178,7 @@ __global__ __launch_bounds__(kThreads) void k_pages_release(w4a8_pages p, int sh
             }
             load(i0 + kThreads * kPerThread, next);  // on their way while these are counted
             int taken;
-            int at = scan_threads32(n, s_part, taken);
+            int at = scan_threads(n, s_part[turn], taken, INT32_MAX);
 #pragma unroll
             for (int j = 0; j < kPerThread; j++)
                 if (page[j] >= 0) {
