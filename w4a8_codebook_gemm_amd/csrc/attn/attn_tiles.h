@@ -125,6 +125,29 @@ __device__ __forceinline__ int64_t scan64(int64_t x) {
     return x;
 }
 
+// The same of 32-bit numbers, and the largest of a wave's numbers >= 0, as a uniform one.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ int moved32(int x) { return __builtin_amdgcn_update_dpp(0, x, kCtrl, kRows, 0xF, false); }
+__device__ __forceinline__ int scan32(int x) {
+    x += moved32<0x111, 0xF>(x);
+    x += moved32<0x112, 0xF>(x);
+    x += moved32<0x114, 0xF>(x);
+    x += moved32<0x118, 0xF>(x);
+    x += moved32<0x142, 0xA>(x);
+    x += moved32<0x143, 0xC>(x);
+    return x;
+}
+__device__ __forceinline__ int max_lanes(int x) {
+    auto up = [&](int y) { x = x > y ? x : y; };
+    up(moved32<0x111, 0xF>(x));
+    up(moved32<0x112, 0xF>(x));
+    up(moved32<0x114, 0xF>(x));
+    up(moved32<0x118, 0xF>(x));
+    up(moved32<0x142, 0xA>(x));
+    up(moved32<0x143, 0xC>(x));
+    return lane_value(x, 63);
+}
+
 // Tiles of T positions in front of position `to` >= 0.  Lengths end below 2^31: a signed sum would pass it.
 template <int T>
 __device__ __forceinline__ int tiles_to(int to) {

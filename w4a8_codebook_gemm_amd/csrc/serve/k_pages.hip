@@ -12,7 +12,9 @@ namespace w4a8 {
 namespace {
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
-// Tokens for which one workgroup is enough.
+// Tokens for which one workgroup is enough where lengths or count are written in place, which takes many a second launch: 8 x 250
+// tokens 3.8 us, many 6.4, 8 x 500 4.8 and 6.3, 8 x 1000 6.7 and 6.4, 256 x 16 6.6 and 6.9.  Apart 8 x 250 tokens take one 4.5 us and
+// many 3.9, 8 x 500 5.7 and 3.9, 256 x 16 6.2 and 4.1.
 constexpr int kAlone = 4096;
 constexpr int kPerThread = 4;    // entries of a thread at a time in giving back
 
@@ -21,17 +23,8 @@ enum { kTokens = 1, kState = 2 };  // table, offsets, positions, slots; lengths,
 
 __device__ __forceinline__ int held(int64_t x, int64_t most) { return (int)(x < 0 ? 0 : x > most ? most : x); }
 
-// Prefix sums over a wave, and exclusive ones over the workgroup's threads with their total: a wave's total counts for
-// `most` at most, so that 16 of them are a 32-bit number (what is beyond it is not asked for).
-__device__ __forceinline__ int scan32(int x) {
-    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);  // row_shr:1, 2, 4, 8
-    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
-    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
-    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
-    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);  // row_bcast:15, 31
-    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);
-    return x;
-}
+// Exclusive prefix sums over the workgroup's threads and their total: a wave's total counts for `most` at most, so that
+// 16 of them are a 32-bit number (what is beyond it is not asked for).
 // One barrier: s_part is read before the workgroup's next one, and written again behind that.
 __device__ __forceinline__ int scan_threads(int a, int *s_part, int &all, int most) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -197,7 +190,7 @@ __global__ __launch_bounds__(kThreads) void k_pages_release(w4a8_pages p, int sh
 hipError_t launch_pages_assign(const w4a8_pages &p, int page_shift, const int32_t *new_tokens, int64_t M,
                                const w4a8_batch &out, hipStream_t stream) {
     const bool in_place = out.seq_lens == p.seq_lens || out.free_count == p.free_count;
-    int64_t grid = M <= kAlone ? 1 : (M + kThreads - 1) / kThreads;
+    int64_t grid = in_place && M <= kAlone ? 1 : (M + kThreads - 1) / kThreads;
     if (grid > 512) grid = 512;
     const bool two = in_place && grid > 1;
     k_pages_assign<<<(unsigned)grid, kThreads, 0, stream>>>(p, page_shift, new_tokens, M, out, two ? kTokens : kTokens | kState);
