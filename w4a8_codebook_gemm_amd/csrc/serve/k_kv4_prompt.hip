@@ -55,6 +55,39 @@ struct Tile {
     static __device__ __forceinline__ int q_at(int s, int hh) { return 32 * (s % (D / 32)) + 8 * (s / (D / 32)) + 16 * hh; }
 };
 
+// What sequence b0 + lane has: units, their tiles, the longest one's.  Called by whole waves: sequences of many blocks
+// are summed by all lanes together.
+struct Units {
+    int64_t tiles;
+    int units, longest;
+};
+template <class S>
+__device__ __forceinline__ Units seq_units(const Attn4Args &a, int64_t b0, int lane) {
+    Seq q{0, 0, 0, 0};
+    if (b0 + lane < a.s.B) q = load_seq(a.s, a.M, a.page_shift, b0 + lane);
+    const int64_t blocks = blocks_of<S>(a, q);
+    int64_t tiles = 0;
+    int longest = 0, x;
+    auto add = [&](const Seq &r, int64_t i, int64_t &sum, int &most) {
+        const int c = block_tiles<S>(a, r, i, x);
+        sum += c;
+        most = most > c ? most : c;
+    };
+    for (int64_t i = 0; i < (blocks <= 4 ? blocks : 0); i++) add(q, i, tiles, longest);
+    for (uint64_t many = __ballot(blocks > 4); many; many &= many - 1) {
+        const int src = __ffsll((unsigned long long)many) - 1;
+        const Seq r = {0, lane_value(q.n, src), lane_value(q.len, src), lane_value(q.pos0, src)};
+        const int64_t rb = blocks_of<S>(a, r);
+        int64_t sum = 0;
+        int most = 0;
+        for (int64_t i = lane; i < rb; i += 64) add(r, i, sum, most);
+        sum = lane_value(scan64(sum), 63);
+        if (lane == src) tiles = sum;
+        longest = longest > most ? longest : most;  // (whichever lane has it)
+    }
+    return Units{tiles * a.c.kv_heads, (int)blocks * a.c.kv_heads, longest};
+}
+
 template <int D, bool BF16>
 __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves / 4)) void k_kv4_prompt(Attn4Args a, int wgs) {
     using S = Shape<D, BF16>;
@@ -71,18 +104,30 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
     uint32_t *counters = static_cast<uint32_t *>(a.ws);
     float *pieces = reinterpret_cast<float *>(static_cast<char *>(a.ws) + kAttnCounterBytes);
 
-    int64_t line = 0;
+    int64_t line = 0, incl_line = 0, units = 0;
+    int incl_units = 0, longest = 0;  // (64 sequences have fewer than 2^30 units)
+    Units u{0, 0, 0};
     for (int64_t b0 = 0; b0 < a.s.B; b0 += 64) {
-        const int64_t mine = seq_tiles<S>(a, b0, lane), incl = scan64(mine);
-        line += lane_value(incl, 63);
-        if (a.s.B <= 64) {  // every wave writes the same and reads its own
-            s_mine[lane] = mine;
-            s_incl[lane] = incl;
-        }
+        u = seq_units<S>(a, b0, lane);
+        incl_units = scan32(u.units);
+        incl_line = scan64(u.tiles + (int64_t)S::kOver * u.units);
+        units += lane_value(incl_units, 63);
+        line += lane_value(incl_line, 63);
+        longest = longest > u.longest ? longest : u.longest;
     }
     if (line == 0) return;
     int64_t used = (line + kMinTiles - 1) / kMinTiles;
     if (used > wgs) used = wgs;
+    // Whole units, one a workgroup and a place on the line each, where workgroups are enough and the longest is no more than a cut's
+    // part: it joins nothing.  Cut and whole (us): 5 x 600 fresh tokens (16 / 16 heads of 64) 27.3 and 20.8, 30 x 20 on 500 (32 / 8 of
+    // 128) 29.2 and 21.5, fp32 36.6 and 28.7.  Finding out costs the others 0.3 us.
+    const bool whole = units <= wgs && max_lanes(longest) <= div64(line, used);
+    if (whole) line = used = units;
+    auto places = [&](const Units &x) { return whole ? x.units : x.tiles + (int64_t)S::kOver * x.units; };
+    if (a.s.B <= 64) {  // every wave writes the same and reads its own
+        s_mine[lane] = places(u);
+        s_incl[lane] = whole ? incl_units : incl_line;
+    }
     // workgroups go to the XCDs in turn: neighbours on the line, which read the same pages, share one's L2
     int64_t w = blockIdx.x;
     if (used == wgs && wgs % 8 == 0) w = w % 8 * (wgs / 8) + w / 8;
@@ -95,7 +140,7 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
         // the sequence, cache head and row block that tile `at` is in
         int64_t base = from_base, b = 0, per_head = 0;
         for (int64_t b0 = from; b0 < a.s.B; b0 += 64) {
-            const int64_t mine = a.s.B <= 64 ? s_mine[lane] : seq_tiles<S>(a, b0, lane);
+            const int64_t mine = a.s.B <= 64 ? s_mine[lane] : places(seq_units<S>(a, b0, lane));
             const int64_t incl = a.s.B <= 64 ? s_incl[lane] : scan64(mine);
             const int64_t sum = lane_value(incl, 63);
             if (at < base + sum) {
@@ -117,7 +162,7 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
         for (int64_t r = 0; r < blocks; r += 64) {
             int f = 0, c = 0;
             if (r + lane < blocks) c = block_tiles<S>(a, q, r + lane, f);
-            const int64_t place = r + lane < blocks ? c + S::kOver : 0;
+            const int64_t place = r + lane < blocks ? (whole ? 1 : c + S::kOver) : 0;
             const int64_t incl = scan64(place), sum = lane_value(incl, 63);
             if (at < unit0 + sum) {
                 const int src = __ffsll((unsigned long long)__ballot(at - unit0 < incl)) - 1;
@@ -129,9 +174,9 @@ __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves
             }
             unit0 += sum;
         }
-        const int64_t unit1 = unit0 + S::kOver + tiles;
-        int tile0, tile1;
-        if (!cut.part(at, t1, unit0, unit1, tiles, tile0, tile1)) {
+        const int64_t unit1 = unit0 + (whole ? 1 : S::kOver + tiles);
+        int tile0 = 0, tile1 = tiles;
+        if (!whole && !cut.part(at, t1, unit0, unit1, tiles, tile0, tile1)) {
             at = unit1;
             continue;
         }

@@ -116,12 +116,7 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a,
             if (a.s.B > 64) x = seq_work<RB, T>(a, b0 + lane);
             longest = longest > x.tiles ? longest : x.tiles;
         }
-#pragma unroll
-        for (int i = 1; i < 64; i <<= 1) {
-            const int o = __shfl_xor(longest, i);
-            longest = longest > o ? longest : o;
-        }
-        solo = units >= (int64_t)wgs * kWaves && __builtin_amdgcn_readfirstlane(longest) - div64(line, units) <= div64(units, wgs);
+        solo = units >= (int64_t)wgs * kWaves && max_lanes(longest) - div64(line, units) <= div64(units, wgs);
     }
     auto sync = [&]() {
         if (solo) {
