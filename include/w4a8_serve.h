@@ -137,8 +137,8 @@ typedef struct {
  * outside the cache, -1 among them, are dropped).  With t = max|x| / fl32(6 unit) over a group of 16, in fp32:
  *   b    = the nearest of 1 .. 255 to t by sc(b), ties to even
  *   code = the nearest to fl32(x / fl32(sc(b) unit)), ties to the even code, +-6 beyond; a zero keeps its sign
- * IEEE division throughout, so each value is off by at most a quarter of its group's largest magnitude / 6 * (1 + 2^-5)
- * below 2/3 of it (half a step of the grid).  Bit-exact and deterministic; tokens do not depend on one another.  A NaN leaves
+ * IEEE division throughout.  S = sc(b) unit is within 2^-5 of max|x| / 6 where that is 16 units or more; values are off by
+ * S / 4 at most up to 2 S, S / 2 up to 4 S and S beyond.  Bit-exact and deterministic; tokens do not depend on one another.  A NaN leaves
  * its value without a meaning; an infinity is the largest magnitude, and costs its group's others theirs.
  * Two tokens of a call must not have the same slot.
  *
@@ -183,8 +183,8 @@ W4A8_API int64_t w4a8_kv4_attention_workspace_bytes(int64_t M, int64_t B, int q_
  * Cached values are exact in both products.  Scores, softmax statistics and sums are fp32: an exponent is off by
  * some 2^-24 of the row's largest |score| (in powers of two; from 2^26 on a row has no meaning).  bf16 queries are exact in the products down to 2^-28 of a row's largest
  * value, fp32 queries to 2^-22 of themselves (2^-38 of the row's largest value below 2^-16 of it).  With P the row's largest
- * probability so far, probabilities enter the second product as one fp16 number for bf16: off by 2^-11 of themselves, or by 2^-38 P
- * where they are below 2^-27 P; for fp32 as the sum of two: 2^-22 of themselves, 2^-38 P below 2^-16 P.  A sum that leaves
+ * probability so far, probabilities enter the second product as one fp16 number for bf16: off by 2^-11 of themselves, or by 2^-35 P
+ * where they are below 2^-24 P; for fp32 as the sum of two: 2^-22 of themselves, 2^-35 P below 2^-13 P.  A sum that leaves
  * fp32's range leaves the row without a meaning.  Deterministic.
  */
 W4A8_API int w4a8_kv4_attention(const void *q, int64_t q_stride, int dtype, int64_t M, int q_heads,

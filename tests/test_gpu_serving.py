@@ -238,6 +238,36 @@ def test_assign_numbers_out_of_range(S):
     check_assign(S, p, [100, 1, 20], 16, 140, True)
 
 
+@pytest.mark.parametrize("M", [50, 700, 5000])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_assign_more_tokens_than_rows(S, M, in_place):
+    """Sums of new tokens that pass 32 bits, the rows used up by any of the sequences."""
+    rng = np.random.default_rng(M)
+    count = 2500
+    p = make_pages(S, rng, list(rng.integers(0, 40, count)), 4, 16, 2000)
+    most = np.full(count, 2 ** 31 - 1, np.int32)
+    few = rng.integers(0, 2, count).astype(np.int32)
+    for new in (most, few, np.where(np.arange(count) < 1400, few, most)):
+        check_assign(S, p, new, 16, M, in_place)
+
+
+def test_assign_as_many_rows_as_there_may_be(S):
+    M, B, width = 2 ** 24, 1100, 2 ** 21 // 256
+    pages = S.Pages.empty(B, width, 9000, 256, DEV)
+    new = torch.full((B,), 2 ** 31 - 1, dtype=torch.int32, device=DEV)
+    new[:3] = i32(5, 0, 2 ** 21)
+    out = S.pages_assign(pages, new, M, out=S.Batch.empty(B, M, DEV))
+    torch.cuda.synchronize()
+    assert out.cu_tokens.tolist() == [0, 5, 5, 5 + 2 ** 21] + [M] * (B - 3)
+    assert out.seq_lens.tolist() == [5, 0, 2 ** 21, 2 ** 21] + [0] * (B - 4)   # the fourth's table ends at 2^21
+    rest = M - 5 - 2 ** 21
+    # 1 + 8192 pages, then 807 of the fourth's 8192, whose tokens want rest / 256 pages
+    assert int(out.free_count) == 0 and int(out.missing) == 8193 + -(-rest // 256) - 9000
+    assert torch.equal(out.positions[5 + 2 ** 21:], torch.arange(rest, dtype=torch.int32, device=DEV))
+    held = torch.cat([torch.arange(5, device=DEV), 256 + torch.arange(2 ** 21 + 807 * 256, device=DEV)])
+    assert torch.equal(out.slots[:held.numel()], held) and bool((out.slots[held.numel():] == -1).all())
+
+
 RELEASE = [
     ([1], [0], 16), ([0], [5], 16), ([100, 17, 64], [33, 16, 64], 16), ([100, 17, 64], [-4, 500, 1], 32),
     ([3000, 2999, 1], [0, 0, 0], 16),
@@ -495,7 +525,9 @@ def check_attention(S, q, b, cache, causal=True, window=0, workspace=None, scale
     length = int(max(b.lens.max(), 1))
     e = ((d + 16) * U + (2.0 ** -22 if wide else 0)) * delta
     bound = (2 * e + 8 * U + 2 * (length / 32 + 40) * U + 70 * U + (2.0 ** -21 if wide else 2.0 ** -11)) * size
-    bound = bound + 2.0 ** -38 * top + half_step(q.dtype) * (np.abs(ref) + bound)
+    # a row's largest probability so far stands at 2^10 or more (2^14, less 1 for a whole maximum and 3 by which that grows ahead);
+    # where fp16 numbers have no more bits, from 2^-14 down, they are 2^-24 apart: half of it is 2^-35 of the largest
+    bound = bound + 2.0 ** -35 * top + half_step(q.dtype) * (np.abs(ref) + bound)
     err = np.abs(got - ref)
     assert np.all(err <= bound), float((err / np.maximum(bound, 1e-300)).max())
 
@@ -573,6 +605,22 @@ def test_attention_of_many_short_sequences(S, count, lo, hi, Hq, Hkv, D, page, d
     cache = random_cache(S, rng, b.pages, Hkv, page, D)
     b.table[5, 0] = -1
     b.table[7] = -1
+    q = dev(rng.standard_normal((b.M, Hq, D)).astype(np.float32), dtype)
+    check_attention(S, q, b, cache, window=window)
+
+
+@pytest.mark.parametrize("new,lens,Hq,Hkv,D,window", [
+    ([600] * 5, [600] * 5, 16, 16, 64, 0),                 # a workgroup for each block of rows and head
+    ([20] * 70, [90 + i for i in range(70)], 8, 2, 128, 0),  # the same of more sequences than a wave has lanes
+    ([150, 0, 90, 0, 200, 64], [180, 9, 90, 0, 231, 300], 8, 4, 128, 100),
+    ([0] * 64 + [90, 40], [5] * 64 + [120, 200], 4, 2, 256, 0),
+    ([90] * 3 + [100], [90] * 3 + [3000], 8, 2, 64, 0),    # one is long: cut
+])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attention_of_whole_blocks(S, new, lens, Hq, Hkv, D, window, dtype):
+    rng = np.random.default_rng(sum(new))
+    b = Batch(rng, new, lens, 32, rows_behind=3)
+    cache = random_cache(S, rng, b.pages, Hkv, 32, D)
     q = dev(rng.standard_normal((b.M, Hq, D)).astype(np.float32), dtype)
     check_attention(S, q, b, cache, window=window)
 
