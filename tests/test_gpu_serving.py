@@ -586,6 +586,25 @@ def test_attention_of_many_units(S, new, lo, hi, count, Hq, Hkv, D, dtype):
     check_attention(S, q, b, cache)
 
 
+@pytest.mark.parametrize("new,Hq,Hkv", [(3, 64, 8), (6, 64, 8), (2, 32, 32), (9, 12, 4)])
+@pytest.mark.parametrize("D,page,window", [(64, 16, 0), (64, 64, 70), (128, 16, 90), (128, 32, 0), (256, 16, 0), (256, 32, 33)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attention_of_drafts(S, new, Hq, Hkv, D, page, window, dtype):
+    """Sequences of unlike lengths with 2 to 48 rows, in blocks of 16 and of 32; pages given up, lengths shorter than the draft."""
+    rng = np.random.default_rng(new + D)
+    count = 17
+    lens = [int(x) for x in rng.integers(new, 400, count)]
+    lens[3], lens[9], lens[10] = new - 1, new, 1100
+    news = [new] * count
+    news[5] = 0
+    b = Batch(rng, news, lens, page, rows_behind=new)
+    cache = random_cache(S, rng, b.pages, Hkv, page, D)
+    b.table[7, 0] = -1
+    b.table[11] = b.pages
+    q = dev(rng.standard_normal((b.M, Hq, D)).astype(np.float32), dtype)
+    check_attention(S, q, b, cache, window=window)
+
+
 @pytest.mark.parametrize("count,lo,hi,Hq,Hkv,D,page,dtype,window", [
     (300, 1, 60, 16, 8, 64, 16, BF, 0),
     (300, 30, 260, 24, 8, 128, 32, F32, 0),
@@ -766,7 +785,8 @@ class Far:
 
 @pytest.mark.parametrize("new,Hq,Hkv,D", [
     (1, 6, 1, 256), (1, 8, 2, 128), (1, 2, 2, 64),        # blocks of 16 rows
-    (6, 8, 1, 128), (9, 4, 2, 256),                       # blocks of 32 rows
+    (6, 8, 1, 128), (9, 4, 2, 256),                       # more of them
+    (6, 256, 32, 128), (20, 64, 32, 64),                  # blocks of 32 rows
     (100, 2, 1, 256), (90, 4, 2, 128), (300, 3, 1, 64),   # the prompt kernel
 ])
 @pytest.mark.parametrize("dtype", [BF, F32])

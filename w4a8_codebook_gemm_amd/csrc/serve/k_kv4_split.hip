@@ -27,12 +27,11 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-template <int NB>
-constexpr int kPerCu = NB == 2 ? 1 : 2;  // workgroups on a compute unit
+constexpr int kPerCu = 2;                // workgroups on a compute unit
 constexpr int kRadix = 8;                // pieces that join at a node
-constexpr int kMaxShare = 4 * kWaves;
+constexpr int kMaxShare = 8 * kWaves;
 template <int NB>
-constexpr int kOver = NB == 2 ? 4 : 8;
+constexpr int kOver = NB == 2 ? 10 : 8;
 constexpr int kTail = 3;
 // Whole units for single waves, which then join nothing: where every wave has one or more, and the longest unit is longer than
 // the average by no more tiles than a workgroup has units.
@@ -74,7 +73,7 @@ __device__ __forceinline__ typename Bytes<N>::type load_once(const uint8_t *p) {
 // kSmall: pages of 16 positions, else of 32 or more: a page for all lanes' part of a tile.  MANY: batches of so many units that
 // each wave may have whole ones.
 template <int D, int NB, bool BF16, bool kSmall, bool MANY>
-__global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a, int wgs) {
+__global__ __launch_bounds__(kThreads, kPerCu) void k_kv4_split(Attn4Args a, int wgs) {
     using Lay = Layout<D, NB>;
     constexpr int RB = Lay::RB;
     constexpr int U = 256 / D, T = 32 * U;  // 32-position parts of a tile
@@ -639,7 +638,7 @@ __global__ __launch_bounds__(kThreads, kPerCu<NB>) void k_kv4_split(Attn4Args a,
 
 template <int D, int NB>
 hipError_t launch_nb(const Attn4Args &a, int bf16, int num_cu, hipStream_t stream) {
-    const int wgs = kPerCu<NB> * num_cu;
+    const int wgs = kPerCu * num_cu;
     auto pick = [&](auto many) {
         constexpr bool M = decltype(many)::value;
         return a.page_shift == 4 ? (bf16 ? k_kv4_split<D, NB, true, true, M> : k_kv4_split<D, NB, false, true, M>)
@@ -656,9 +655,7 @@ hipError_t launch_nb(const Attn4Args &a, int bf16, int num_cu, hipStream_t strea
 
 template <int D>
 int64_t bytes_d(int num_cu) {
-    const int64_t one = 2 * (int64_t)kPerCu<1> * num_cu * Layout<D, 1>::kRecord;
-    const int64_t two = 2 * (int64_t)kPerCu<2> * num_cu * Layout<D, 2>::kRecord;
-    return 4 * (one > two ? one : two);
+    return 4 * 2 * (int64_t)kPerCu * num_cu * Layout<D, D < 256 ? 2 : 1>::kRecord;
 }
 
 }  // namespace
@@ -667,11 +664,13 @@ int64_t kv4_split_bytes(int head_dim, int num_cu) {
     return head_dim == 64 ? bytes_d<64>(num_cu) : head_dim == 128 ? bytes_d<128>(num_cu) : bytes_d<256>(num_cu);
 }
 
-hipError_t launch_kv4_split(const Attn4Args &a, int bf16, int blocks, int num_cu, hipStream_t stream) {
+hipError_t launch_kv4_split(const Attn4Args &a, int bf16, int64_t rows, int num_cu, hipStream_t stream) {
+    const int64_t heads = a.s.B * a.c.kv_heads;
+    const bool wide = rows > 16 && heads >= (rows > 32 ? num_cu / 8 : num_cu / 2);
     switch (a.c.head_dim) {
-        case 64: return blocks == 1 ? launch_nb<64, 1>(a, bf16, num_cu, stream) : launch_nb<64, 2>(a, bf16, num_cu, stream);
-        case 128: return blocks == 1 ? launch_nb<128, 1>(a, bf16, num_cu, stream) : launch_nb<128, 2>(a, bf16, num_cu, stream);
-        default: return blocks == 1 ? launch_nb<256, 1>(a, bf16, num_cu, stream) : launch_nb<256, 2>(a, bf16, num_cu, stream);
+        case 64: return wide ? launch_nb<64, 2>(a, bf16, num_cu, stream) : launch_nb<64, 1>(a, bf16, num_cu, stream);
+        case 128: return wide ? launch_nb<128, 2>(a, bf16, num_cu, stream) : launch_nb<128, 1>(a, bf16, num_cu, stream);
+        default: return launch_nb<256, 1>(a, bf16, num_cu, stream);
     }
 }
 

@@ -222,7 +222,7 @@ int w4a8_kv4_attention(const void *q, int64_t q_stride, int dtype, int64_t M, in
                             workspace};
     hipStream_t s = static_cast<hipStream_t>(stream);
     const int64_t rows = rows_per_sequence(M, seqs->B, group);
-    return status_of(rows <= kSplitRows ? w4a8::launch_kv4_split(a, dtype == W4A8_BF16, rows <= 16 ? 1 : 2, num_cu, s)
+    return status_of(rows <= kSplitRows ? w4a8::launch_kv4_split(a, dtype == W4A8_BF16, rows, num_cu, s)
                                         : w4a8::launch_kv4_prompt(a, dtype == W4A8_BF16, num_cu, s));
 }
 

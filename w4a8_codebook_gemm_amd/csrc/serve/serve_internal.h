@@ -51,9 +51,9 @@ struct Attn4Args {
     void *ws;
 };
 static_assert(W4A8_KV4_ATTENTION_COUNTER_BYTES == kAttnCounterBytes, "one counter area for both caches");
-// Few rows a sequence: blocks of 16 (blocks 1) or 32 (2) rows.
+// Few rows a sequence (on average).
 int64_t kv4_split_bytes(int head_dim, int num_cu);
-hipError_t launch_kv4_split(const Attn4Args &a, int bf16, int blocks, int num_cu, hipStream_t stream);
+hipError_t launch_kv4_split(const Attn4Args &a, int bf16, int64_t rows, int num_cu, hipStream_t stream);
 // Many rows a sequence.
 int64_t kv4_prompt_bytes(int head_dim, int num_cu);
 hipError_t launch_kv4_prompt(const Attn4Args &a, int bf16, int num_cu, hipStream_t stream);
