@@ -5,6 +5,9 @@
 // more, and a group's scale bytes of tokens that follow each other, which lie together for values, are
 // one store's.  The quotients are correctly rounded ones from the scale's reciprocal
 // (quant4_r has the proof); two of them become codes in one instruction.
+//
+// HBM bound for large calls: 8192 tokens of 4 heads of 256, bf16, 10.2 us, 4.2 TB/s (its inputs past the caches 9.5), fp32
+// 13.2; 65536 of 8 heads of 128 67.8, 5.1 TB/s; 61 tokens 2.9 us, which is a launch.  A copy runs at 5.39 TB/s here.
 #include "serve_internal.h"
 
 namespace w4a8 {

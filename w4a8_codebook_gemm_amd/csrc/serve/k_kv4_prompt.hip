@@ -16,6 +16,14 @@
 //
 // Split: as in the other kernels, the tiles of all units form one line that is cut evenly over the
 // workgroups; a cut unit's pieces are joined two and two in a tree.
+//
+// Measured (TFLOP/s of the positions that are seen; the library's product of 8192^3 reaches 1036 in fp16 here; the int8 kernel
+// in brackets): 2 x 2048 tokens on 14000, 24 / 4 heads of 256, 1.40 to 1.44 ms, 1070 to 1100 (1.51); 8192 causal tokens, 32 / 8
+// of 128, 577 to 590 us, 930 to 950 (609), 16 / 16 of 64 200, 685 (224); 5 ragged prompts of 128 160, 715 (163); fp32, which
+// has twice the products, 2 x 2048 on 6000 of 128 770, 610 (822), 2 x 1024 on 2000 of 256 322 to 330, 380 (371).  The matrix
+// cores are busy 43% of the cycles at head_dim 256, the vector units 49%: a SIMD's two waves take turns.  At
+// head_dim 64 the softmax has four times the share.  At head_dim 256 bf16 spills 42 registers, outside
+// the loop over tiles.
 #include "kv4_tiles.h"
 
 namespace w4a8 {
@@ -23,17 +31,26 @@ namespace {
 
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 
-constexpr int kSchedPV = 0x406;   // what may move over the steps of the second product: vector and scalar arithmetic
-constexpr int kMinTiles = 4;      // tiles a workgroup is worth cutting for
+// What may move over the steps of the second product: vector and scalar arithmetic.  That and nothing: 8192 of 128 577 and 581
+// us, 5 ragged ones 158 and 160, fp32 4096 of 64 91.2 and 94.2, bf16 8192 of 64 199.6 and 196.5.
+constexpr int kSchedPV = 0x406;
+// Tiles a workgroup is worth cutting for.  1, 4 and 12: 8 x 100 fresh tokens of 128 14.8, 16.0 and 34.0 us, 7 ragged with a
+// window 39.3, 39.6 and 55.8, 8192 of 64 (32 / 8) 387, 383 and 381.
+constexpr int kMinTiles = 4;
 
 template <int D, bool BF16>
 struct Shape {
+    // fp32 rows of 256 need the registers of two waves for their queries.  Two workgroups of 4 waves in place of one of 8 at
+    // head_dim 64 and 128 pay where blocks of 128 rows are fuller: 20 x 100 with a window 35.2 and 30.0 us, 5 x 600 fp32 of 128
+    // 69 and 64, 8192 of 64 200 and 224, of 128 594 and 676, 5 ragged ones 160 and 180.
     static constexpr int kWaves = BF16 || D <= 128 ? 8 : 4;
     static constexpr int kThreads = 64 * kWaves;
     static constexpr int RB = 32 * kWaves;
     static constexpr int T = 8192 / D;       // positions of a tile
     static constexpr int kGroups = T / 16;
-    static constexpr int kOver = D == 256 ? 5 : 3, kTail = D == 256 ? 3 : 2;  // see Line
+    // see Line.  kOver 1, as it is, and 10 (kTail 1, as it is, 6): 8192 of 128 645, 577 and 574 us, 5 ragged ones 186, 158 and
+    // 171, 8192 of 64 203, 200 and 216, fp32 4096 of 64 87.9, 91.2 and 110.7.
+    static constexpr int kOver = D == 256 ? 5 : 3, kTail = D == 256 ? 3 : 2;
     static constexpr int kRegs = D / 2;      // floats of O^T in a lane
     static constexpr int kWaveRecord = 64 * (kRegs + 4);    // a wave's piece: O^T, then m, L
     static constexpr int kRecord = kWaves * kWaveRecord;
@@ -91,7 +108,7 @@ __device__ __forceinline__ Units seq_units(const Attn4Args &a, int64_t b0, int l
 template <int D, bool BF16>
 __global__ __launch_bounds__((Shape<D, BF16>::kThreads), (Shape<D, BF16>::kWaves / 4)) void k_kv4_prompt(Attn4Args a, int wgs) {
     using S = Shape<D, BF16>;
-    constexpr int kFrags = 2;  // K and V fragments in flight
+    constexpr int kFrags = 2;  // K and V fragments in flight (2 and 4: alike)
     constexpr int T = S::T, kParts = BF16 ? 1 : 2, kSteps = D / 16, kTiles = D / 32;
     constexpr int kSubs = D == 256 ? 1 : 2, kWide = 32 * kSubs;   // positions of a softmax step: registers
     constexpr int kItems = 512 / S::kThreads;  // staging items of a thread: 256 of keys, 256 of values

@@ -18,6 +18,14 @@
 // Split: as in the int8 kernel, the tiles of all units form one line that is cut evenly over the
 // workgroups; a workgroup's waves take its tiles in turn and join in LDS, and pieces of a cut unit
 // through the workspace (join_pieces).
+//
+// Measured (one token a sequence; a large copy runs at 5.39 TB/s here; the int8 kernel on the same shapes in brackets): 4 x 90k
+// to 131k tokens, 24 / 4 heads of 256, 90 to 98 us, 4.8 to 5.2 TB/s (160); 32 x 300 to 16000 60 us, 4.1 (92); 64 x 4000,
+// 32 / 8 of 128, 57 us, 5.2 (89), in pages of 16 61 to 66; 256 x 100 to 300 32 us, 1.8 (38); 16 x 8 drafts on 4000 35 us (44),
+// on 200 to 4000 31.5 (46).  Between start and join HBM bounds long calls: their reads alone, the arithmetic taken out, take 91 of
+// 101 us (99 where the codes go through the caches).  Drafts are bound by the vector units, which make fragments of the codes.
+// 1 x 777 of 256 is 16 us (17), latency: offsets, pages, codes and other workgroups' pieces are reads that wait for each other.
+// Tiles have 256 / D parts of 32 positions: two at D 256 take 112 us in place of 102, a whole tile in registers ahead 144 (spills).
 #include <type_traits>
 
 #include "kv4_tiles.h"
@@ -27,15 +35,26 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kPerCu = 2;                // workgroups on a compute unit
-constexpr int kRadix = 8;                // pieces that join at a node
+// Workgroups on a compute unit.  1, 2 and 3 with blocks of 16 rows: 64 x 4000 of 128 75, 58 and (spills) 248 us, 1 x 131000 46 and 41.  1
+// and 2 with blocks of 32 (2 spills 12 to 31 registers): 64 x 6 drafts on 100 to 2000 47.5 and 37, 200 x 8 on 50 to 500 91 and 74,
+// 32 x 16 on 500 to 4000 73 and 66.
+constexpr int kPerCu = 2;
+// Pieces that join at a node.  2, 8 and 32: 1 x 777 of 256 19.2, 15.9 and 16.2 us, 4 long ones 105, 94 to 98 and 104, 16 x 8
+// drafts 44.4, 41.0 and 42.1.
+constexpr int kRadix = 8;
+// None, 4 and 8 kWaves: 8 x 500 to 1000 of 128 14.1, 11.6 and 11.5 us, 1 x 4000 16.5, 13.0 and 13.4, 16 x 8 drafts on 200 to
+// 4000 41.9, 41.0 and 29.7; longer ones take no shares.
 constexpr int kMaxShare = 8 * kWaves;
+// See Line.  Blocks of 16 rows, kOver 4, 8, 16 and 28: 200 x 100 to 3000 of 128 101.5, 93.8, 95.4 and 101.9 us, 32 ragged of
+// 256 59.6, 59.7, 58.1 and 59.9, 4 long ones 104, 98.8, 100.7 and 103.9.  Blocks of 32, 4, 10, 16 and 24: 32 x 16 on 500 to
+// 4000 82, 72, 70 and 73, 64 x 6 58, 47.5, 47 and 51, 200 x 8 95, 89, 88 and 90.  kTail 1, 3 and 8: within 2% everywhere.
 template <int NB>
 constexpr int kOver = NB == 2 ? 10 : 8;
 constexpr int kTail = 3;
 // Whole units for single waves, which then join nothing: where every wave has one or more, and the longest unit is longer than
-// the average by no more tiles than a workgroup has units.
-constexpr int kSoloOver = 2;  // as kOver
+// the average by no more tiles than a workgroup has units.  Workgroups' way and waves' (us): 256 x 100 to 300 (32 / 8 of 128) 46 and 32,
+// fp32 512 x 300 to 900 136 and 113, 1024 x 100 to 300 (16 / 4 of 64) 83 and 56, 256 x 500 to 2000 99 and 100.5.
+constexpr int kSoloOver = 2;  // as kOver (2 and 6: alike)
 
 template <int D, int NB>
 struct Layout {
@@ -645,7 +664,7 @@ hipError_t launch_nb(const Attn4Args &a, int bf16, int num_cu, hipStream_t strea
                                  : (bf16 ? k_kv4_split<D, NB, true, false, M> : k_kv4_split<D, NB, false, false, M>);
     };
     auto f = pick(std::false_type());
-    // at head_dim 256 the registers do not hold what both ways need
+    // (at head_dim 256 the registers do not hold what both ways need)
     if constexpr (NB == 1 && D < 256) {
         if (a.s.B * a.c.kv_heads >= (int64_t)wgs * kWaves) f = pick(std::true_type());
     }
@@ -664,6 +683,12 @@ int64_t kv4_split_bytes(int head_dim, int num_cu) {
     return head_dim == 64 ? bytes_d<64>(num_cu) : head_dim == 128 ? bytes_d<128>(num_cu) : bytes_d<256>(num_cu);
 }
 
+// Blocks of 16 rows read a sequence's codes once for each, at twice the work in flight; blocks of 32 pay where units are many.
+// Blocks of 16 and 32 (us).  24 to 32 rows, 32 / 8 heads of 128: 16 x 6 on 4000 35.0 and 32.9, 16 x 8 37.3 and 35.3, 64 x 6 on
+// 100 to 2000 49 and 37; fewer sequences and heads, 30 x 8 on 2000 to 9000 (8 / 2 of 128) 31.9 and 39.0, 16 x 8 (16 / 4 of 64)
+// 22.9 and 28.3.  33 to 64 rows: 32 x 16 on 500 to 4000 79 and 64, 8 x 16 on 10k to 20k 107 and 85, 4 x 16 on 30k to 60k 145
+// and 116; 8 x 16 on 1000 to 4000 29.9 and 31.0, 2 x 12 on 1000 to 9000 25.7 and 36.5.  At head_dim 256 blocks of 32 leave one
+// wave a SIMD: 61 x 5 on 100 to 4000 74 and 120, 4 x 8 on 30k to 60k 121 and 138, 8 x 10 on 4000 38 and 42.
 hipError_t launch_kv4_split(const Attn4Args &a, int bf16, int64_t rows, int num_cu, hipStream_t stream) {
     const int64_t heads = a.s.B * a.c.kv_heads;
     const bool wide = rows > 16 && heads >= (rows > 32 ? num_cu / 8 : num_cu / 2);
