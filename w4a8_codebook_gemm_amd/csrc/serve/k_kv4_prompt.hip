@@ -34,8 +34,8 @@ typedef float floatx16 __attribute__((ext_vector_type(16)));
 // What may move over the steps of the second product: vector and scalar arithmetic.  That and nothing: 8192 of 128 577 and 581
 // us, 5 ragged ones 158 and 160, fp32 4096 of 64 91.2 and 94.2, bf16 8192 of 64 199.6 and 196.5.
 constexpr int kSchedPV = 0x406;
-// Tiles a workgroup is worth cutting for.  1, 4 and 12: 8 x 100 fresh tokens of 128 14.8, 16.0 and 34.0 us, 7 ragged with a
-// window 39.3, 39.6 and 55.8, 8192 of 64 (32 / 8) 387, 383 and 381.
+// Tiles a workgroup is worth cutting for.  1, 4 and 8: 8 x 300 fresh tokens of 64 (32 / 8) 27.1, 26.9 and 30.6 us, of 128 36.6, 36.3 and
+// 39.1, others alike.
 constexpr int kMinTiles = 4;
 
 template <int D, bool BF16>
