@@ -884,6 +884,50 @@ def test_streams_and_two_calls_at_once(S):
             assert torch.equal(a, o) and torch.equal(c.h, p.h) and torch.equal(c.x_q, p.x_q) and torch.equal(c.s_x, p.s_x)
 
 
+@pytest.mark.parametrize("new", [[1, 3], [50, 70]])
+def test_attention_scales_and_windows_at_their_limits(S, new):
+    rng = np.random.default_rng(31)
+    b = Batch(rng, new, [300, 90], 16)
+    cache = random_cache(S, rng, b.pages, 2, 16, 64)
+    q = dev(rng.standard_normal((b.M, 4, 64)).astype(np.float32), F32)
+    for scale in (-0.2, 0.0, 1e-30):
+        check_attention(S, q, b, cache, scale=scale)
+    seqs = b.seqs()
+    want = S.kv4_attention(q, cache, seqs)
+    for window in (2 ** 40, 2 ** 31, 2 ** 31 - 1, 300):
+        assert torch.equal(S.kv4_attention(q, cache, seqs, window=window), want)
+    assert torch.equal(S.kv4_attention(-q, cache, seqs, scale=-(64 ** -0.5)), want)
+
+
+def test_captured_calls_that_make_their_own_outputs_and_workspace(S):
+    rng = np.random.default_rng(32)
+    b = Batch(rng, [2, 90], [400, 700], 32)
+    cache = random_cache(S, rng, b.pages, 2, 32, 128)
+    q = dev(rng.standard_normal((b.M, 4, 128)).astype(np.float32), BF)
+    x, r, w = torch.randn(9, 768, device=DEV), torch.randn(9, 768, device=DEV), torch.rand(768, device=DEV)
+    p = make_pages(S, rng, [5, 40, 0], 20, 16, 50)
+    pages, new = on_gpu(S, p, 16), i32(3, 200, 0)
+    seqs = b.seqs()
+    calls = lambda out: (S.kv4_attention(q, cache, seqs), *S.add_norm_prepare(x, w, r, normed_dtype=BF),  # noqa: E731
+                         *vars(S.pages_assign(pages, new, 210, out=out)).values())
+    tensors = lambda t: [y for y in t if isinstance(y, torch.Tensor)]  # noqa: E731
+    want = [y.clone() for y in tensors(calls(S.Batch.empty(3, 210, DEV)))]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = tensors(calls(S.Batch.empty(3, 210, DEV)))
+    for turn in range(5):
+        for y in got:
+            y.zero_()
+        graph.replay()
+        again = tensors(calls(S.Batch.empty(3, 210, DEV)))
+        if turn % 2:
+            torch.cuda.synchronize()
+        assert len(got) == len(want) == 11
+        for a, c, e in zip(got, want, again):
+            assert torch.equal(a, c) and torch.equal(e, c)
+
+
 # ----------------------------------------------------------------------------- together
 
 def test_decoder_step_captured_and_replayed(S):
