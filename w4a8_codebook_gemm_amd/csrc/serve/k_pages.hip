@@ -133,10 +133,13 @@ __global__ __launch_bounds__(kThreads) void k_pages_assign(w4a8_pages p, int shi
 // 4.1.  Entries of a thread at a time, 4, 8 and 16: 27.3, 31.7 and 32.0 us for the same with 64-bit counts.
 __global__ __launch_bounds__(kThreads) void k_pages_release(w4a8_pages p, int shift, const int32_t *__restrict__ keep_lens,
                                                             int32_t *lens, int32_t *free_count) {
-    __shared__ int s_part[2][kWaves];
-    __shared__ int s_first[kThreads];     // pages behind a sequence's, of those at hand
-    __shared__ int64_t s_entry[kThreads];  // its last page's entry in the table, and as many more
-    const int tid = threadIdx.x;
+    __shared__ int s_part[2][kWaves], s_some[kWaves];
+    // Of the sequences that give pages back, in turn: pages in front of a sequence's, and its last page's entry in the table and as
+    // many more.  Behind the last of them nothing is found.
+    __shared__ int s_first[kThreads + 1];
+    __shared__ int64_t s_entry[kThreads];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    if (tid == 0) s_first[kThreads] = INT32_MAX;
     const int P = 1 << shift, most = (int)(p.table_width << shift);
     const int at_once = p.table_width > (int64_t(1) << 20) ? (int)((int64_t(1) << 30) / p.table_width) : kThreads;
     int count = held(p.free_count[0], p.num_pages);
@@ -150,16 +153,25 @@ __global__ __launch_bounds__(kThreads) void k_pages_release(w4a8_pages p, int sh
             gone = have - (int)(((uint32_t)keep + (P - 1)) >> shift);
             lens[end - tid] = keep;
         }
+        const uint64_t some = __ballot(gone > 0);
+        if (lane == 0) s_some[wave] = __popcll(some);
         int all;
         const int first = scan_threads(gone, s_part[0], all, INT32_MAX);
-        s_first[tid] = first;
-        s_entry[tid] = (end - tid) * p.table_width + have - 1 + first;
+        const int ranks = scan32(lane < kWaves ? s_some[lane & (kWaves - 1)] : 0), before = __shfl(ranks, wave > 0 ? wave - 1 : 0);
+        const int rank = (wave ? before : 0) + __popcll(some & ((uint64_t(1) << lane) - 1));
+        if (gone > 0) {
+            s_first[rank] = first;
+            s_entry[rank] = (end - tid) * p.table_width + have - 1 + first;
+        }
+        if (tid >= lane_value(ranks, kWaves - 1)) s_first[tid] = INT32_MAX;
         __syncthreads();
         auto load = [&](int i0, int page[kPerThread]) {
+            const int i = i0 + tid * kPerThread;
+            int q = i < all ? find_last(s_first, i) : 0;
 #pragma unroll
             for (int j = 0; j < kPerThread; j++) {
-                const int i = i0 + tid * kPerThread + j;
-                page[j] = i < all ? p.page_table[s_entry[find_last(s_first, i)] - i] : -1;
+                if (j && i + j < all) q += i + j >= s_first[q + 1];  // (each has a page or more)
+                page[j] = i + j < all ? p.page_table[s_entry[q] - (i + j)] : -1;
             }
         };
         int next[kPerThread];
