@@ -19,7 +19,9 @@ constexpr int kThreads = 1024, kWaves = kThreads / 64;
 // tokens 3.8 us, many 6.4, 8 x 500 4.8 and 6.3, 8 x 1000 6.7 and 6.4, 256 x 16 6.6 and 6.9.  Apart 8 x 250 tokens take one 4.5 us and
 // many 3.9, 8 x 500 5.7 and 3.9, 256 x 16 6.2 and 4.1.
 constexpr int kAlone = 4096;
-constexpr int kPerThread = 4;    // entries of a thread at a time in giving back
+// Entries of a thread at a time in giving back.  2, 4 and 8: 231 pages of 61 sequences 3.0, 3.5 and 4.3 us, 3347 of 256 4.2, 4.3 and 5.5,
+// 23,900 of 1021 15.3, 14.5 and 20.3, 17,500 of 16384 32, 40 and 54.
+constexpr int kPerThread = 2;
 
 // What a launch of assigning writes.
 enum { kTokens = 1, kState = 2 };  // table, offsets, positions, slots; lengths, count
@@ -129,8 +131,8 @@ __global__ __launch_bounds__(kThreads) void k_pages_assign(w4a8_pages p, int shi
 
 // From the last sequence to the first, and within one from its last page down.  1024 sequences at a time, or fewer
 // where their tables have more than 2^30 entries: page counts are 32-bit numbers then.  What a page costs is the
-// instructions of finding it on one compute unit: 24,000 of 1021 sequences take 19 us (with 64-bit counts 27), 230 of 61 sequences
-// 4.1.  Entries of a thread at a time, 4, 8 and 16: 27.3, 31.7 and 32.0 us for the same with 64-bit counts.
+// instructions of finding it on one compute unit: a thread finds its first one's sequence by bisection among those that
+// give pages back, and the next one's by a step.  (All by bisection among all sequences 19.1 us for 23,900 pages, with 64-bit counts 27.)
 __global__ __launch_bounds__(kThreads) void k_pages_release(w4a8_pages p, int shift, const int32_t *__restrict__ keep_lens,
                                                             int32_t *lens, int32_t *free_count) {
     __shared__ int s_part[2][kWaves], s_some[kWaves];
