@@ -311,6 +311,19 @@ def test_release_many(S, count, ctx, page):
     check_release(S, p, keep, page, False)
 
 
+@pytest.mark.parametrize("count", [1023, 1024, 2050])
+@pytest.mark.parametrize("every", [1, 2, 65])
+def test_release_of_a_page_each(S, count, every):
+    """Each sequence, or one in `every`, gives back one page; the last of them many."""
+    rng = np.random.default_rng(count + every)
+    lens = rng.integers(17, 33, count)
+    lens[count - 2] = 5000
+    keep = np.where(np.arange(count) % every == 0, 16, lens)
+    keep[count - 2] = 20
+    p = make_pages(S, rng, [int(x) for x in lens], 320, 16, 3)
+    check_release(S, p, keep, 16, False)
+
+
 def test_release_into_a_list_without_room(S):
     """A program that gives a page back twice: the list's end is not passed."""
     p = make_pages(S, np.random.default_rng(2), [100, 90], 8, 16, 3)
