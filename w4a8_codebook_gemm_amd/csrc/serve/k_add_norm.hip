@@ -9,8 +9,9 @@
 // (fewer blocks a lane group) also meet at two barriers, and finish a single token sooner.
 //
 // The sum is fp64 (products of fp32 numbers are exact in it), so the factor does not depend on how the sum is
-// split, but for one rounding in some 2^28.  Its root is the hardware's reciprocal square root (some 2^-28 off) and
-// one Newton step, y + y/2 (1 - a y^2), in fp64: 2^-52, as exact as a division by a root.
+// split, but for one rounding in some 2^28.  Its root is the hardware's reciprocal square root and two Newton steps,
+// y + y/2 (1 - a y^2), in fp64, as exact as a division by a root.  Largest relative error over 2^30 numbers of [1, 4), at four
+// scales: 2^-24.2, 2^-47.7 after one step (which rounds the factor wrongly in one row of some 2^25), 2^-52.7 after two.
 #include "serve_internal.h"
 
 namespace w4a8 {
@@ -96,7 +97,8 @@ __device__ __forceinline__ float wave_max(float x) {
 
 // 1 / sqrt(a), a > 0, normal and finite
 __device__ __forceinline__ double reciprocal_root(double a) {
-    const double y = __builtin_amdgcn_rsq(a);
+    double y = __builtin_amdgcn_rsq(a);
+    y = fma(0.5 * y, fma(-a * y, y, 1.0), y);
     return fma(0.5 * y, fma(-a * y, y, 1.0), y);
 }
 
