@@ -137,9 +137,12 @@ typedef struct {
  * outside the cache, -1 among them, are dropped).  With t = max|x| / fl32(6 unit) over a group of 16, in fp32:
  *   b    = the nearest of 1 .. 255 to t by sc(b), ties to even
  *   code = the nearest to fl32(x / fl32(sc(b) unit)), ties to the even code, +-6 beyond; a zero keeps its sign
- * IEEE division throughout.  S = sc(b) unit is within 2^-5 of max|x| / 6 where that is 16 units or more; values are off by
- * S / 4 at most up to 2 S, S / 2 up to 4 S and S beyond.  Bit-exact and deterministic; tokens do not depend on one another.  A NaN leaves
- * its value without a meaning; an infinity is the largest magnitude, and costs its group's others theirs.
+ * IEEE division throughout.  S = sc(b) unit is within 2^-5 of max|x| / 6 where that is 16 units or more, up to 507904.  In groups whose
+ * max|x| is more than 15 units and at most 3047424, values are off by S / 4 at most up to 2 S, S / 2 up to 4 S and S beyond (and by
+ * what fp32 division moves a border).  Smaller groups have no finer scales: there values are off by as much, or by 3 units (a group
+ * whose largest is 8.9 units has S 1 and is cut to 6).  What is beyond 3047424 units is cut to it.  Bit-exact and deterministic; tokens
+ * do not depend on one another.  A NaN leaves its value without a meaning; an infinity is the largest magnitude, and costs its
+ * group's others theirs.
  * Two tokens of a call must not have the same slot.
  *
  *  k, v   [M] tokens of kv_heads * head_dim consecutive values, k_stride and v_stride elements
