@@ -49,3 +49,101 @@ def test_norm_factors_next_to_a_border(S):  # noqa: F811
     got = S.add_norm_prepare(x, torch.ones(256, device=DEV), eps=0.0, normed_dtype=F32, quantise=False).normed
     factor = got[:, 255].cpu().numpy() * np.float32(2.0 ** 60)
     assert int((factor != want).sum()) == 0
+
+
+# ----------------------------------------------------------------------------- how attention for few rows cuts its work
+
+def split_plan(new, lens, hq, hkv, d):
+    """What k_kv4_split makes of a batch without a window: rows of a block, tiles of a workgroup's share (0: an even
+    cut of the line), whether a unit's cost lies on the line, the most pieces of a unit, whether waves have whole units."""
+    cu, group, waves = torch.cuda.get_device_properties(0).multi_processor_count, hq // hkv, 4
+    rows, heads, wgs = -(-sum(new) * group // len(new)), len(new) * hkv, 2 * cu
+    assert rows <= 64
+    nb = 2 if d < 256 and rows > 16 and heads >= (cu // 8 if rows > 32 else cu // 2) else 1
+    t = 32 * (256 // d)
+    tiles = [max(1, -(-n // t)) for m, n in zip(new, lens) for _ in range(-(-m * group // (16 * nb)) * hkv)]
+    solo = nb == 1 and d < 256 and heads >= wgs * waves and len(tiles) >= wgs * waves and \
+        max(tiles) - sum(tiles) // len(tiles) <= len(tiles) // wgs
+    line, c = sum(tiles), -(-sum(tiles) // (wgs * waves)) * waves
+    while c <= 8 * waves:
+        if sum(-(-x // c) for x in tiles) <= wgs:
+            return 16 * nb, c, False, max(-(-x // c) for x in tiles), solo
+        c += waves
+    over = (10 if nb == 2 else 8) if nb == 1 or len(tiles) >= wgs else 0
+    part = (line + over * len(tiles)) / wgs
+    return 16 * nb, 0, over > 0, int(max(tiles) / part), solo
+
+
+def shared_pages(rng, b, pages):
+    """The batch on a cache of few pages, which its sequences share."""
+    b.pages = pages
+    b.table = rng.integers(0, pages, b.table.shape).astype(np.int32)
+
+
+def attention64(q, cache, b):
+    """Causal attention in 64 bits on the GPU, a sequence and cache head at a time, and what attention_ref.attention gives for
+    its bounds."""
+    M, hq, d = q.shape
+    k, v = (G.dev(x) for x in G.dense(cache))
+    P, hkv, g = k.shape[2], k.shape[1], hq // k.shape[1]
+    o, A, T = (torch.zeros(M, hq, d, dtype=torch.float64, device=DEV) for _ in range(3))
+    delta = torch.zeros(M, hq, 1, dtype=torch.float64, device=DEV)
+    for i, n in enumerate(b.lens.tolist()):
+        t = torch.arange(n, device=DEV)
+        page, rows = G.dev(b.table[i])[t // P].long(), slice(int(b.cu[i]), int(b.cu[i + 1]))
+        new = rows.stop - rows.start
+        hidden = (t > n - new + torch.arange(new, device=DEV)[:, None]).repeat_interleave(g, 0)
+        for h in range(hkv):
+            kh, vh = k[page, h, t % P], v[page, h, t % P]
+            heads = slice(h * g, (h + 1) * g)
+            x = q[rows, heads].double().reshape(new * g, d)
+            z = ((x @ kh.T.contiguous()) * d ** -0.5).masked_fill(hidden, -float("inf"))
+            p = torch.softmax(z, -1)
+            shape = (new, g, d)
+            o[rows, heads], A[rows, heads] = (p @ vh).view(shape), (p @ vh.abs()).view(shape)
+            T[rows, heads] = (p.amax(-1, keepdim=True) * ((~hidden).double() @ vh.abs())).view(shape)
+            size = (x.abs() @ kh.abs().T.contiguous()).masked_fill(hidden, 0.0)
+            delta[rows, heads] = (size.amax(-1) * d ** -0.5).view(new, g, 1)
+    return [x.cpu().numpy() for x in (o, A, T, delta)]
+
+
+def check_twice(S, q, b, cache):  # noqa: F811
+    """Against the 64-bit form, and again to the bit; counters at zero after each call."""
+    hkv, d = cache.k.shape[1], q.shape[2]
+    ws = S.kv4_attention_workspace(b.M, len(b.lens), q.shape[1], hkv, d, DEV)
+    ws[S.COUNTER_BYTES:] = 255
+    seqs, outs = b.seqs(), []
+    for _ in range(2):
+        outs.append(S.kv4_attention(q, cache, seqs, workspace=ws))
+        torch.cuda.synchronize()
+        assert int(ws[:S.COUNTER_BYTES].max()) == 0
+    assert torch.equal(*outs)
+    ref, size, top, delta = attention64(q, cache, b)
+    wide, length = q.dtype == F32, int(b.lens.max())
+    e = ((d + 16) * G.U + (2.0 ** -22 if wide else 0)) * delta
+    bound = (2 * e + 8 * G.U + 2 * (length / 32 + 40) * G.U + 70 * G.U + (2.0 ** -21 if wide else 2.0 ** -11)) * size
+    # the row's largest weight stands at 2^10 or more, fp16's smallest numbers are 2^-24 apart
+    bound = bound + 2.0 ** -35 * top + G.half_step(q.dtype) * (np.abs(ref) + bound)
+    err = np.abs(G.f64(outs[0]) - ref)
+    assert np.all(err <= bound), float((err / np.maximum(bound, 1e-300)).max())
+
+
+@pytest.mark.parametrize("new,lo,hi,count,Hq,Hkv,D,page,behind", [
+    (16, 10000, 20000, 8, 32, 8, 128, 32, False),        # fewer units than workgroups
+    (16, 500, 4000, 32, 32, 8, 128, 16, True),           # as many or more: what a unit costs lies on the line
+    (16, 16000, 30000, 8, 32, 8, 64, 64, False),
+    (6, 2000, 8000, 64, 32, 8, 64, 16, True),
+    (7, 300, 4000, 96, 18, 6, 128, 256, True),
+])
+@pytest.mark.parametrize("dtype", [G.BF, F32])
+def test_blocks_of_32_rows_cut_anywhere(S, new, lo, hi, count, Hq, Hkv, D, page, behind, dtype):  # noqa: F811
+    """Batches whose line is cut evenly, with pieces of units as they come (fewer than the 64 that the bound counts)."""
+    rng = np.random.default_rng(new + count)
+    lens = [int(x) for x in rng.integers(lo, hi, count)]
+    block, share, over, pieces, _ = split_plan([new] * count, lens, Hq, Hkv, D)
+    assert (block, share, over) == (32, 0, behind) and pieces > 0
+    b = G.Batch(rng, [new] * count, lens, page)
+    shared_pages(rng, b, 60)
+    cache = G.random_cache(S, rng, b.pages, Hkv, page, D)
+    q = G.dev(rng.standard_normal((b.M, Hq, D)).astype(np.float32), dtype)
+    check_twice(S, q, b, cache)
