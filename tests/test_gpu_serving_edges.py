@@ -147,3 +147,38 @@ def test_blocks_of_32_rows_cut_anywhere(S, new, lo, hi, count, Hq, Hkv, D, page,
     cache = G.random_cache(S, rng, b.pages, Hkv, page, D)
     q = G.dev(rng.standard_normal((b.M, Hq, D)).astype(np.float32), dtype)
     check_twice(S, q, b, cache)
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,D,page,least", [
+    ([40000], 24, 4, 256, 64, 65),
+    ([131000], 6, 1, 256, 16, 500),                       # nearly every workgroup has a piece of it
+    ([100000, 300], 8, 2, 64, 32, 65),
+    ([70000], 6, 2, 128, 256, 65),
+])
+@pytest.mark.parametrize("dtype", [G.BF, F32])
+def test_units_of_more_than_64_pieces(S, lens, Hq, Hkv, D, page, least, dtype):  # noqa: F811
+    """Three levels of joining, 8 pieces at a node: 24 joins of three roundings, 72 u of A and not 70, while each piece's sum
+    has lens / 32 / 64 steps at most where the bound counts lens / 32."""
+    rng = np.random.default_rng(lens[0])
+    assert split_plan([1] * len(lens), lens, Hq, Hkv, D)[3] >= least
+    b = G.Batch(rng, [1] * len(lens), lens, page)
+    shared_pages(rng, b, 100)
+    cache = G.random_cache(S, rng, b.pages, Hkv, page, D)
+    q = G.dev(rng.standard_normal((b.M, Hq, D)).astype(np.float32), dtype)
+    check_twice(S, q, b, cache)
+
+
+@pytest.mark.parametrize("new,length,Hq,Hkv,D,page", [(70, 70000, 5, 1, 256, 64), (90, 60000, 2, 1, 128, 16), (200, 100000, 2, 2, 64, 32)])
+@pytest.mark.parametrize("dtype", [G.BF, F32])
+def test_row_blocks_of_more_than_64_pieces(S, new, length, Hq, Hkv, D, page, dtype):  # noqa: F811
+    """The prompt kernel's blocks of 256 rows (fp32 of 256: 128) and tiles of 8192 / D positions, cut for all compute units: two
+    and two joined in 7 or 8 levels of three roundings, the rest as above."""
+    cu = torch.cuda.get_device_properties(0).multi_processor_count
+    blocks = -(-new * (Hq // Hkv) // (128 if D == 256 and dtype == F32 else 256)) * Hkv
+    assert new * (Hq // Hkv) > 64 and cu // blocks > 64
+    rng = np.random.default_rng(new)
+    b = G.Batch(rng, [new], [length], page)
+    shared_pages(rng, b, 100)
+    cache = G.random_cache(S, rng, b.pages, Hkv, page, D)
+    q = G.dev(rng.standard_normal((b.M, Hq, D)).astype(np.float32), dtype)
+    check_twice(S, q, b, cache)
