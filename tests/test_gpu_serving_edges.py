@@ -182,3 +182,27 @@ def test_row_blocks_of_more_than_64_pieces(S, new, length, Hq, Hkv, D, page, dty
     cache = G.random_cache(S, rng, b.pages, Hkv, page, D)
     q = G.dev(rng.standard_normal((b.M, Hq, D)).astype(np.float32), dtype)
     check_twice(S, q, b, cache)
+
+
+# ----------------------------------------------------------------------------- pages of wide tables
+
+@pytest.mark.parametrize("B,width", [(3, 2 ** 20 + 1), (1030, 2 ** 20 + 1), (40, 2 ** 25), (11, 2 ** 27 - 1)])
+def test_release_from_wide_tables(S, B, width):  # noqa: F811
+    """Tables of so many entries that fewer than 1024 sequences go at a time: 1023, 32 and 8 of them."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 400, B)
+    lens[::4] = width * 16 - rng.integers(0, 400, len(lens[::4]))
+    keep = np.maximum(lens - rng.integers(-20, 200, B), 0)
+    total, table, free = 30000, torch.empty((B, width), dtype=torch.int32, device=DEV), []
+    at, seqs, entries = iter(rng.permutation(total)), [], []
+    for b in reversed(range(B)):
+        for e in reversed(range(-(-min(keep[b], lens[b]) // 16), -(-lens[b] // 16))):
+            seqs.append(b)
+            entries.append(e)
+            free.append(next(at))
+    table[torch.tensor(seqs, device=DEV), torch.tensor(entries, device=DEV)] = G.dev(np.array(free, np.int32))
+    pages = S.Pages(table, G.dev(lens.astype(np.int32)), torch.full((total,), -9, dtype=torch.int32, device=DEV), G.i32(2), 16)
+    got, count = S.pages_release(pages, G.dev(keep.astype(np.int32)))
+    assert np.array_equal(got.cpu().numpy(), np.minimum(keep, lens)) and int(count) == 2 + len(free)
+    assert pages.free_pages[:2 + len(free)].tolist() == [-9, -9] + [int(x) for x in free]
+    assert bool((pages.free_pages[2 + len(free):] == -9).all())
