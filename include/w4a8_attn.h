@@ -167,7 +167,8 @@ W4A8_API int64_t w4a8_kv_attention_workspace_bytes(int64_t M, int64_t B, int q_h
  *            workspaces of their own.
  *
  * Scores, softmax statistics and sums are fp32: an exponent is off by some 2^-24 of the row's largest
- * |score|, so scores of 2^13 (in powers of two) cost a probability 2^-11 of itself.  bf16 queries are exact
+ * |score|, so scores of 2^13 (in powers of two) cost a probability 2^-11 of itself, and from 2^24 on a row has no
+ * meaning (outputs that are not finite among it).  bf16 queries are exact
  * in the products down to 2^-28 of a row's largest value.  With P the row's largest probability times value
  * scale, probabilities enter the second product as one fp16 number for bf16: off by 2^-11 of themselves, or by
  * 2^-33 P where they are below 2^-22 P; for fp32 as the sum of two: 2^-22 of themselves, 2^-37 P below 2^-15 P,
