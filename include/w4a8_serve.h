@@ -188,8 +188,8 @@ W4A8_API int64_t w4a8_kv4_attention_workspace_bytes(int64_t M, int64_t B, int q_
  * in the products down to 2^-28 of a row's largest value, fp32 queries to 2^-22 of themselves (2^-38 of the row's largest
  * value below 2^-16 of it).  With P the row's largest probability so far, probabilities enter the second product as one
  * fp16 number for bf16: off by 2^-11 of themselves, or by 2^-35 P where they are below 2^-24 P; for fp32 as the sum of
- * two: 2^-22 of themselves, 2^-35 P below 2^-13 P.  A sum that leaves fp32's range leaves the row without a meaning.
- * Deterministic.
+ * two: 2^-22 of themselves, 2^-35 P below 2^-13 P; the parts of P grow by 2^(2^-22 |score|) with scores beyond 2^20.  A sum
+ * that leaves fp32's range leaves the row without a meaning.  Deterministic.
  */
 W4A8_API int w4a8_kv4_attention(const void *q, int64_t q_stride, int dtype, int64_t M, int q_heads,
                                 const w4a8_kv4_cache *cache, const w4a8_sequences *seqs, float sm_scale, int causal,

@@ -42,3 +42,25 @@ def test_int8_cache(A, n, d, dtype, power):  # noqa: F811
     o = A.kv_attention(q, cache, A.Sequences(table, i32(0, n), i32(LENGTH)), scale=2.0 ** power / score).double()
     ratio = o / means(v, n)
     assert float(ratio.min()) > 0.49 and float(ratio.max()) < 2.04
+
+
+@pytest.mark.parametrize("n", [1, 7, 100])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("power", [13, 20, 25.9])
+def test_4_bit_cache(n, d, dtype, power):
+    """Up to 2^20 the weight stands at 2^9 or more.  Below 2^26 the maximum lies 16 + 2 (its rounding) + 3 + 2 above the score, the
+    argument's constant rounds by 2: 2^-11 or more, where an fp16 number has its 11 bits still and the sum of two is off by 2^-25.
+    One number: 2^-11 of the weight; two: 2^-22, or 2^-25 / 2^-11.  Sums: 200 / 32 + 40 steps for numerator and denominator each, 70 for
+    joining, of 2^-24: under 2^-16."""
+    from w4a8_codebook_gemm_amd import serving as S
+    import serving_ref as R
+    k, v, q, score, table = case(d, n, dtype)
+    cache = S.KV4Cache.empty(8, 1, 32, d, DEV)
+    S.kv4_append(k, v, cache, torch.arange(LENGTH, device=DEV))
+    kept = R.values4(*(t.cpu().numpy() for t in (cache.v, cache.v_scale.transpose(2, 3), cache.v_unit)))
+    kept = torch.from_numpy(kept[:, 0].reshape(-1, 1, d)[:LENGTH]).to(DEV)
+    seqs = S.Sequences(table, i32(0, n), i32(LENGTH))
+    ratio = S.kv4_attention(q, cache, seqs, scale=2.0 ** power / score).double() / means(kept, n)
+    weight = 2.0 ** -11 if dtype == BF else 2.0 ** -14 if power > 20 else 2.0 ** -22
+    assert float((ratio - 1).abs().max()) < (weight + 2.0 ** -16 + torch.finfo(dtype).eps / 2) * 1.01
