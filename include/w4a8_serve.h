@@ -169,7 +169,8 @@ W4A8_API int64_t w4a8_kv4_attention_workspace_bytes(int64_t M, int64_t B, int q_
  * t <= p, and with window > 0 also t > p - window.  A query that sees nothing gives 0; pages outside
  * [0, num_pages) are not seen.  Query head h reads cache head h / (q_heads / kv_heads).  Rows of o that
  * belong to no sequence are left as they were.  Which kernel serves a call goes by M * (q_heads / kv_heads) / B, the
- * rows a sequence has on average; any mix of sequences is right.  A query that is not finite leaves its own row
+ * rows a sequence has on average; any mix of sequences is right, but a prompt among many single tokens is
+ * faster in a call of its own.  A query that is not finite leaves its own row
  * without a meaning, a unit outside its range its head's.
  *
  *  q         [M] tokens of q_heads * head_dim consecutive values, q_stride elements apart (a

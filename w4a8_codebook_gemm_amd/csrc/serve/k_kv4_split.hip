@@ -22,7 +22,8 @@
 // Measured (one token a sequence; a large copy runs at 5.39 TB/s here; the int8 kernel on the same shapes in brackets): 4 x 90k
 // to 131k tokens, 24 / 4 heads of 256, 90 to 98 us, 4.8 to 5.2 TB/s (160); 32 x 300 to 16000 60 us, 4.1 (92); 64 x 4000,
 // 32 / 8 of 128, 57 us, 5.2 (89), in pages of 16 61 to 66; 256 x 100 to 300 32 us, 1.8 (38); 16 x 8 drafts on 4000 35 us (44),
-// on 200 to 4000 31.5 (46).  Between start and join HBM bounds long calls: their reads alone, the arithmetic taken out, take 91 of
+// on 200 to 4000 31.5 (46), fp32 41 (16 x 8 on 4000); 61 x 5 on 100 to 4000 of 256 75 to 86, fp32 96; 64 x 6 on 100 to 2000 of 128 38, fp32
+// 47; 256 x 100 to 300 fp32 35.  Between start and join HBM bounds long calls: their reads alone, the arithmetic taken out, take 91 of
 // 101 us (99 where the codes go through the caches).  Drafts are bound by the vector units, which make fragments of the codes.
 // 1 x 777 of 256 is 16 us (17), latency: offsets, pages, codes and other workgroups' pieces are reads that wait for each other.
 // Tiles have 256 / D parts of 32 positions: two at D 256 take 112 us in place of 102, a whole tile in registers ahead 144 (spills).
