@@ -261,10 +261,10 @@ hipError_t launch_r(const NormArgs &a, int W, int num_cu, hipStream_t stream) {
 // 27.1, 8192 102, 89 and 79, where 2 and 3 leave as many places of a token's waves empty; 8192 x 4096 bf16 2 59 and 3
 // 67, 3000 x 8192 47 and 56, where 3 leaves more; 16384 x 1024 bf16 1 32 and 2 37.  4 and 5 blocks in workgroups of 256 threads
 // spill or have too few waves: 8192 x 5120 94 and 82 at best.
-// 3 blocks of an fp32 residual spill 11 to 20 registers in the loop over tokens (of a bf16 one none), and gain less.  2 and 3, bf16 + bf16 /
+// 3 blocks of an fp32 residual spill 11 to 20 registers in the loop over tokens (of a bf16 one 4 at most), and gain less.  2 and 3, bf16 + bf16 /
 // bf16 + fp32 / fp32 + fp32: 8192 x 5120 72 and 59 / 107 and 108 / 123 and 122, 4096 x 5120 38 and 32 / 48 and 48 / 55 and 64, 8192 x 2816
 // 37 and 31 / 49 and 58 / 61 and 70, 8192 x 9216 137 and 116 / 219 and 200 / 251 and 221.
-// K beyond 32768 needs 4 blocks in 1024 threads, 128 registers each, and spills 14 (fp32 + bf16), 42 (bf16 + bf16) and 81: 512 x 65536 77 us
+// K beyond 32768 needs 4 blocks in 1024 threads, 128 registers each, and spills 14 (fp32 + bf16), 42 (bf16 + bf16) and 77 to 81: 512 x 65536 77 us
 // (3.9 TB/s), 81 (2.9), fp32 residuals 152 and 158 (2.4 and 2.8); 512 x 32768, 2 blocks, 4.1 to 4.7 TB/s.
 template <bool XB, bool RB>
 hipError_t launch_t(const NormArgs &a, int num_cu, hipStream_t stream) {
